@@ -10,6 +10,10 @@ missing library raises.
     o = decode_step(q, k, v, g, beta, state)          # state updated in place
     grads = chunk_backward(q, k, v, g, beta, do, h0=None, dht=None)
 
+The operators around the recurrence in a layer (layer.py) are the short causal
+convolution (short_conv*), the norm of queries and keys with the position
+rotation (qk_norm*) and the selective state space scan (selective_scan*).
+
 g selects the gate: [.., H, d] one log-decay per key channel (KDA), [.., H]
 one per head (Gated DeltaNet), None no decay (DeltaNet).
 
@@ -31,7 +35,11 @@ __all__ = ["chunk_forward", "chunk_forward_noalloc", "chunk_forward_states", "ch
            "kda_chunk",
            "workspace_bytes", "backward_workspace_bytes", "make_desc", "make_desc_ex", "KdaError", "status_string",
            "version",
-           "CHUNK_LAUNCHES", "BWD_STAGES"]
+           "CHUNK_LAUNCHES", "BWD_STAGES",
+           "short_conv", "short_conv_forward", "short_conv_step", "short_conv_backward",
+           "selective_scan", "selective_scan_forward", "selective_scan_step", "selective_scan_backward",
+           "selective_scan_workspace_bytes",
+           "qk_norm", "qk_norm_forward", "qk_norm_backward"]
 
 
 def _torch():
@@ -451,3 +459,9 @@ def decode_step(q, k, v, g, beta, state, g_floor: float = -0.125, *, o=None, str
     if st != KDA_OK:
         raise KdaError(st, "kda_decode_step" if gate == KDA_GATE_CHANNEL else "kda_decode_step_gated")
     return o
+
+
+from .layer import (qk_norm, qk_norm_backward, qk_norm_forward, selective_scan,  # noqa: E402
+                    selective_scan_backward, selective_scan_forward, selective_scan_step,
+                    selective_scan_workspace_bytes, short_conv, short_conv_backward, short_conv_forward,
+                    short_conv_step)

@@ -24,6 +24,10 @@ KDA_DTYPE_BF16 = 1
 KDA_GATE_CHANNEL = 0   # g [.., H, d_k]: KDA
 KDA_GATE_HEAD = 1      # g [.., H]: Gated DeltaNet
 KDA_GATE_NONE = 2      # no g: DeltaNet
+KDA_ACT_NONE = 0
+KDA_ACT_SILU = 1
+KDA_NORM_UNIT = 0
+KDA_NORM_RMS = 1
 
 # Every symbol include/kda.h declares.
 EXPORTS = ("kda_status_string", "kda_version", "kda_chunk_forward_workspace_size",
@@ -31,7 +35,11 @@ EXPORTS = ("kda_status_string", "kda_version", "kda_chunk_forward_workspace_size
            "kda_chunk_forward_states_count", "kda_chunk_forward_states", "kda_chunk_forward_mx",
            "kda_chunk_backward_workspace_size", "kda_chunk_backward", "kda_chunk_backward_overlapped",
            "kda_chunk_backward_timed", "kda_decode_step", "kda_decode_step_gated",
-           "kda_chunk_forward_noalloc")
+           "kda_chunk_forward_noalloc",
+           "kda_short_conv_forward", "kda_short_conv_step", "kda_short_conv_backward_workspace_size",
+           "kda_short_conv_backward", "kda_selective_scan_workspace_size", "kda_selective_scan_forward",
+           "kda_selective_scan_step", "kda_selective_scan_backward_workspace_size", "kda_selective_scan_backward",
+           "kda_qk_norm_forward", "kda_qk_norm_backward_workspace_size", "kda_qk_norm_backward")
 
 # Launches of one kda_chunk_forward call, in stream order (kda_chunk_forward_timed):
 # the map sweep and the output sweep are the two instances of kda_chunk_sweep.
@@ -56,6 +64,40 @@ class ChunkDesc(ctypes.Structure):
 class ChunkDescEx(ctypes.Structure):
     """Mirror of kda_chunk_desc_ex_t: the shape and the gate layout."""
     _fields_ = [("shape", ChunkDesc), ("gate", ctypes.c_int)]
+
+
+def _fields(ints: str, tail=(), longs: str = ""):
+    return ([(n, ctypes.c_int) for n in ints.split()] + list(tail) + [(n, ctypes.c_int64) for n in longs.split()])
+
+
+class ConvDesc(ctypes.Structure):
+    """Mirror of kda_conv_desc_t."""
+    _fields_ = _fields("B T D width n_seqs dtype activation", longs="ld_x")
+
+
+class ScanDesc(ctypes.Structure):
+    """Mirror of kda_scan_desc_t."""
+    _fields_ = _fields("B T D N G n_seqs dtype softplus", longs="ld_x ld_dt ld_z ld_b ld_c")
+
+
+class NormDesc(ctypes.Structure):
+    """Mirror of kda_qk_norm_desc_t."""
+    _fields_ = _fields("n_tokens Hq Hk d rot dtype norm interleaved",
+                       (("eps", ctypes.c_float), ("q_scale", ctypes.c_float)), "ld_q ld_k")
+
+
+# Pointer arguments of the operators around the recurrence, each call being
+# (descriptor, pointers ..., [workspace, workspace bytes,] stream).
+LAYER_CALLS = {
+    "kda_short_conv_forward": (ConvDesc, 7, False),
+    "kda_short_conv_step": (ConvDesc, 5, False),
+    "kda_short_conv_backward": (ConvDesc, 11, True),
+    "kda_selective_scan_forward": (ScanDesc, 12, True),
+    "kda_selective_scan_step": (ScanDesc, 10, False),
+    "kda_selective_scan_backward": (ScanDesc, 21, True),
+    "kda_qk_norm_forward": (NormDesc, 8, False),
+    "kda_qk_norm_backward": (NormDesc, 12, True),
+}
 
 
 _lib = None
@@ -113,6 +155,15 @@ def load(path: str = LIBRARY) -> ctypes.CDLL:
                                           ctypes.c_int, ctypes.c_int, ctypes.c_float, vp, vp, vp, vp, vp, vp, vp,
                                           vp]
     lib.kda_decode_step_gated.restype = ctypes.c_int
+    for name, (desc, n_ptr, ws) in LAYER_CALLS.items():
+        fn = getattr(lib, name)
+        fn.argtypes = [ctypes.POINTER(desc)] + [vp] * n_ptr + ([vp, sz] if ws else []) + [vp]
+        fn.restype = ctypes.c_int
+    for name, desc in (("kda_short_conv_backward", ConvDesc), ("kda_selective_scan", ScanDesc),
+                       ("kda_selective_scan_backward", ScanDesc), ("kda_qk_norm_backward", NormDesc)):
+        fn = getattr(lib, name + "_workspace_size")
+        fn.argtypes = [ctypes.POINTER(desc), ctypes.POINTER(sz)]
+        fn.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -215,3 +266,19 @@ def decode_step_gated_raw(N, H, d_k, d_v, dtype, gate, g_floor, q, k, v, g, beta
     """Call kda_decode_step_gated with raw integer addresses; returns the status."""
     return int(load().kda_decode_step_gated(N, H, d_k, d_v, dtype, gate, ctypes.c_float(g_floor), q, k, v, g,
                                             beta, state, o, stream))
+
+
+def layer_workspace_size(name: str, desc) -> int:
+    """Bytes of workspace that `name` (the call without _workspace_size) needs for the descriptor."""
+    out = ctypes.c_size_t(0)
+    st = getattr(load(), name + "_workspace_size")(desc, out)
+    if st != KDA_OK:
+        raise KdaError(st, name + "_workspace_size")
+    return out.value
+
+
+def layer_call(name: str, desc, *args) -> None:
+    """Call one of LAYER_CALLS with raw integer addresses; raises KdaError unless it returns KDA_OK."""
+    st = getattr(_lib or load(), name)(desc, *args)
+    if st != KDA_OK:
+        raise KdaError(st, name)

@@ -1,0 +1,189 @@
+// Internal interface between the C-ABI front end of the operators around the
+// recurrence (kda_layer_api.cpp, plain C++) and the HIP translation units
+// that hold their kernels: the short convolution, the selective scan and the
+// norm of queries and keys.
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+namespace kda {
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// ---- short convolution ---------------------------------------------------
+// One wave owns 64 vectors of channels and `tile` tokens, one workgroup
+// kConvWaves such tiles in a row.
+constexpr int kConvWaves = 4;
+constexpr int kConvBatch = 8;  // token rows a wave loads before it uses them
+
+struct ConvArgs {
+  const void* x;
+  int64_t ld;
+  const float* w;
+  const float* bias;
+  const void* init;
+  const int32_t* cu;  // null: rows of T tokens
+  int n_seqs;
+  int64_t T, tokens;
+  int D;
+  int tile;
+  int64_t n_part;  // workgroups along the tokens
+};
+
+// Tokens per wave: the longest tile (less of the window is read twice) that
+// still leaves `waves` waves.
+inline int conv_tile(int64_t tokens, int64_t channel_waves, int longest, int64_t waves) {
+  int tile = longest;
+  while (tile > kConvBatch && channel_waves * ceil_div(tokens, tile) < waves) tile /= 2;
+  return tile;
+}
+
+int launch_conv_forward(int is_bf16, int width, int silu, const ConvArgs& a, void* y, void* fin, void* stream);
+int launch_conv_step(int is_bf16, int width, int silu, const ConvArgs& a, void* state, void* y, void* stream);
+int launch_conv_backward(int is_bf16, int width, int silu, const ConvArgs& a, const void* dy, const void* dfin,
+                         void* dx, float* dw, float* db, void* dinit, float* part, void* stream);
+
+// Channels of one vector in the forward and in the backward pass.
+constexpr int conv_vec(bool bf16, bool backward) { return bf16 && !backward ? 8 : 4; }
+inline int64_t conv_channel_waves(int D, int vec) { return ceil_div(D < vec ? D : ceil_div(D, vec), 64); }
+inline int conv_forward_tile(int is_bf16, int64_t tokens, int D) {
+  return conv_tile(tokens, conv_channel_waves(D, conv_vec(is_bf16, false)), 16, 2048);
+}
+inline int conv_backward_tile(int64_t tokens, int D) {
+  return conv_tile(tokens, conv_channel_waves(D, conv_vec(false, true)), 64, 2048);
+}
+// Partial sums of dweight and dbias: one row of (width + 1) * D floats per
+// workgroup along the tokens.
+inline int64_t conv_parts(int64_t tokens, int tile) { return ceil_div(ceil_div(tokens, tile), kConvWaves); }
+
+// ---- selective scan --------------------------------------------------------
+// A wave holds 4 channels of 16 lanes; lane j of a channel holds states
+// j, j + 16, ... (NS of them).  A call cuts the tokens of the whole batch
+// into slots of `slot` tokens; each workgroup scans one slot of its channels.
+constexpr int kScanMaxStates = 64;
+constexpr int kScanTile = 64;  // tokens of B and C staged at once (forward)
+inline int scan_ns(int N) { return N <= 16 ? 1 : N <= 32 ? 2 : 4; }
+
+struct ScanArgs {
+  const void *x, *dt, *z, *Bm, *Cm;
+  int64_t ld_x, ld_dt, ld_z, ld_b, ld_c;
+  const float *A, *skip, *bias, *h0;
+  const int32_t* cu;  // null: rows of T tokens
+  int n_seqs;
+  int64_t T, tokens;
+  int D, N, G, softplus;
+  int64_t slot, n_slots;
+  int blocks_per_group;  // workgroups over the channels of one group
+};
+
+// Workspace of a forward call: the state that every slot hands on (from a
+// zero state when its first sequence began earlier) and its sum of delta.
+struct ScanPlan {
+  int64_t slot, n_slots;
+  bool carry;  // some sequence may pass from one slot to the next
+  size_t hend_off, sum_off, ws_bytes;
+};
+constexpr int kScanWaves = 4;  // waves per workgroup (forward)
+
+inline ScanPlan plan_scan(int64_t tokens, int rows, int64_t T, bool packed, int D, int N, int G, int n_cu) {
+  ScanPlan p{};
+  const int64_t cus = n_cu > 0 ? n_cu : 256;
+  const int64_t waves = (int64_t)G * ceil_div(D / G, 4 * kScanWaves) * kScanWaves;  // of one slot
+  if (tokens == 0) {
+    p.slot = 1;
+    p.n_slots = 1;
+  } else if (!packed && waves * rows >= 4 * cus) {
+    p.slot = T;  // the rows alone put a wave on every SIMD
+    p.n_slots = rows;
+  } else {
+    int64_t n = 16 * cus / waves;
+    if (n > tokens / 128) n = tokens / 128;
+    if (n < 1) n = 1;
+    p.slot = ceil_div(ceil_div(tokens, n), kScanTile) * kScanTile;
+    p.n_slots = ceil_div(tokens, p.slot);
+  }
+  p.carry = p.n_slots > 1 && (packed || p.slot % T != 0);
+  const size_t up = 255;
+  const size_t hend = p.carry ? (size_t)p.n_slots * D * N * 4 : 0;
+  p.hend_off = 0;
+  p.sum_off = (hend + up) / 256 * 256;
+  p.ws_bytes = p.carry ? (p.sum_off + (size_t)p.n_slots * D * 4 + up) / 256 * 256 : 0;
+  return p;
+}
+
+int launch_scan_forward(int is_bf16, const ScanArgs& a, const ScanPlan& p, void* o, float* ht, void* ws, void* stream);
+int launch_scan_step(int is_bf16, const ScanArgs& a, float* state, void* o, void* stream);
+
+// Backward: the same slots, short enough that one workgroup keeps B, C and a
+// state every 16 tokens of its slot in LDS.
+constexpr int scan_bwd_waves(int ns) { return ns == 1 ? 8 : 4; }
+constexpr int scan_bwd_slot(int ns) { return ns == 1 ? 256 : ns == 2 ? 128 : 64; }
+
+struct ScanBwdPlan {
+  int64_t slot, n_slots;
+  bool carry;
+  int blocks_per_group;
+  // byte offsets: forward state and adjoint at the slot's edges, sum of
+  // delta, per-slot sums of dA, dskip and ddt_bias, per-workgroup sums of dB, dC
+  size_t hend_off, adj_off, sum_off, da_off, dskip_off, dbias_off, db_off, dc_off, ws_bytes;
+};
+
+inline ScanBwdPlan plan_scan_backward(int64_t tokens, int D, int N, int G) {
+  ScanBwdPlan p{};
+  const int ns = scan_ns(N);
+  p.slot = scan_bwd_slot(ns);
+  p.n_slots = tokens > 0 ? ceil_div(tokens, p.slot) : 1;
+  p.carry = p.n_slots > 1;
+  p.blocks_per_group = (int)ceil_div(D / G, 4 * scan_bwd_waves(ns));
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = (off + bytes + 255) / 256 * 256;
+    return at;
+  };
+  const size_t slots = (size_t)p.n_slots, dn = (size_t)D * N * 4;
+  p.hend_off = take(p.carry ? slots * dn : 0);
+  p.adj_off = take(p.carry ? slots * dn : 0);
+  p.sum_off = take(p.carry ? slots * D * 4 : 0);
+  p.da_off = take(slots * dn);
+  p.dskip_off = take(slots * D * 4);
+  p.dbias_off = take(slots * D * 4);
+  p.db_off = take((size_t)p.blocks_per_group * tokens * G * N * 4);
+  p.dc_off = take((size_t)p.blocks_per_group * tokens * G * N * 4);
+  p.ws_bytes = off;
+  return p;
+}
+
+struct ScanGrads {
+  const void* dout;
+  const float* dht;
+  void *dx, *ddt, *dz, *dB, *dC;
+  float *dA, *dskip, *dbias, *dh0;
+};
+
+int launch_scan_backward(int is_bf16, const ScanArgs& a, const ScanBwdPlan& p, const ScanGrads& g, void* ws,
+                         void* stream);
+
+// ---- norm of queries and keys ----------------------------------------------
+struct NormArgs {
+  const void *q, *k;
+  int64_t ld_q, ld_k;
+  const float *wq, *wk;
+  const int32_t* pos;
+  const float* freq;
+  int n_tokens, Hq, Hk, d, rot;
+  int interleaved;
+  float sum_factor;  // 1 (unit) or 1 / d (rms)
+  float eps, q_scale;
+};
+
+// Workgroups of the backward pass over one of q and k; each leaves one row
+// of d floats of partial sums of the weight's gradient.
+constexpr int kNormParts = 1024;
+
+int launch_norm_forward(int is_bf16, const NormArgs& a, void* qo, void* ko, void* stream);
+int launch_norm_backward(int is_bf16, const NormArgs& a, const void* dqo, const void* dko, void* dq, void* dk,
+                         float* dwq, float* dwk, float* part, void* stream);
+
+}  // namespace kda

@@ -1,0 +1,387 @@
+// Short causal convolution for gfx950: forward, one-token step and backward.
+//
+// With xe a sequence preceded by its initial state's W - 1 inputs and w[j]
+// the taps of a channel (the last one meets the token itself):
+//   u_t = bias + sum_j w[j] xe[t + j],    y = u  or  u sigmoid(u)
+// and backward, with du = dy act'(u) (zero outside the sequence):
+//   dx_s = sum_j w[j] du[s + W - 1 - j],  dw[j] = sum_t du_t xe[t + j],
+//   dbias = sum_t du_t.
+// All of it is bound by memory: a token-channel is read once and written
+// once (twice read in the backward pass) for some 2 W + 8 operations.
+//
+// A lane owns one vector of channels (16 bytes forward, 4 channels backward)
+// and walks a tile of tokens with the last W - 1 inputs in registers, so an
+// input is loaded once per tile and the window costs W - 1 extra rows a
+// tile.  Rows are loaded kConvBatch at a time before the first is used.
+// Every wave's token range is uniform: where its sequences begin and end is
+// scalar control flow.  A last vector that would pass the end of the row is
+// moved back to end with it; its channels overlap the neighbour's and both
+// write the same values (the step, which updates in place, stores the part
+// that is its own instead).
+#include "kda_layer_device.h"
+
+namespace kda {
+
+namespace {
+
+// first channel of a lane's vector
+template <int V>
+__device__ __forceinline__ int channel_of(int vec, int D, bool* active) {
+  const int c = vec * V;
+  *active = c < D;
+  return c + V <= D ? c : D - V;
+}
+
+template <int V, int W>
+__device__ __forceinline__ void load_taps(const float* __restrict__ w, const float* __restrict__ bias, int c,
+                                          float (&taps)[W][V], float (&b)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    b[i] = bias ? bias[c + i] : 0.f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) taps[j][i] = w[(int64_t)(c + i) * W + j];
+  }
+}
+
+// row r of the sequence [lo, hi) preceded by its initial state (r < 0: the state)
+template <typename T, int V, int W>
+__device__ __forceinline__ void load_row(const T* __restrict__ x, int64_t ld, const T* __restrict__ init, int D, int s,
+                                         int64_t lo, int64_t r, int c, float (&v)[V]) {
+  if (r >= 0) {
+    load_vec<T, V>(x + (lo + r) * ld + c, v);
+  } else if (init) {
+    load_vec<T, V>(init + ((int64_t)s * (W - 1) + (W - 1) + r) * D + c, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = 0.f;
+  }
+}
+
+template <typename T, int V, int W, bool SILU>
+__global__ void __launch_bounds__(256) conv_forward(const ConvArgs a, T* __restrict__ y, T* __restrict__ fin) {
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  bool active;
+  const int c = channel_of<V>(blockIdx.y * 64 + lane, a.D, &active);
+  if (!active) return;
+  const T* __restrict__ x = (const T*)a.x;
+  const T* __restrict__ init = (const T*)a.init;
+  const Seqs seqs{a.cu, a.n_seqs, a.T, a.tokens};
+  if (blockIdx.x >= a.n_part) {  // one row of one sequence's final state per wave
+    const int64_t item = (blockIdx.x - a.n_part) * kConvWaves + wave;
+    if (item >= (int64_t)a.n_seqs * (W - 1)) return;
+    const int s = (int)(item / (W - 1)), p = (int)(item % (W - 1));
+    const int64_t lo = seqs.start(s), len = seqs.end(s) - lo;
+    float v[V];
+    load_row<T, V, W>(x, a.ld, init, a.D, s, lo, len - (W - 1) + p, c, v);
+    store_vec<T, V>(fin + item * a.D + c, v);
+    return;
+  }
+  int64_t t = ((int64_t)blockIdx.x * kConvWaves + wave) * a.tile;
+  const int64_t t1 = t + a.tile < a.tokens ? t + a.tile : a.tokens;
+  if (t >= t1) return;
+  float taps[W][V], b[V];
+  load_taps<V, W>(a.w, a.bias, c, taps, b);
+  int s = seqs.from(t + 1) - 1;  // the last sequence that starts at t or before
+  if (s < 0) s = 0;
+  for (; s < a.n_seqs && t < t1; ++s) {
+    const int64_t lo = seqs.start(s), hi = seqs.end(s);
+    if (hi <= t) continue;
+    if (t < lo) t = lo;
+    const int64_t e = hi < t1 ? hi : t1;
+    float win[W - 1][V];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) load_row<T, V, W>(x, a.ld, init, a.D, s, lo, t - lo - (W - 1) + j, c, win[j]);
+    while (t < e) {
+      float r[kConvBatch][V];
+#pragma unroll
+      for (int k = 0; k < kConvBatch; ++k) load_vec<T, V>(x + (t + k < e ? t + k : e - 1) * a.ld + c, r[k]);
+#pragma unroll
+      for (int k = 0; k < kConvBatch; ++k) {
+        float u[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          u[i] = b[i];
+#pragma unroll
+          for (int j = 0; j < W - 1; ++j) u[i] += taps[j][i] * win[j][i];
+          u[i] += taps[W - 1][i] * r[k][i];
+          if (SILU) u[i] *= sigmoid(u[i]);
+#pragma unroll
+          for (int j = 0; j + 1 < W - 1; ++j) win[j][i] = win[j + 1][i];
+          win[W - 2][i] = r[k][i];
+        }
+        if (t + k < e) store_vec<T, V>(y + (t + k) * a.D + c, u);
+      }
+      t += kConvBatch;
+    }
+    t = e;
+  }
+}
+
+// One token: a lane owns V channels of one sequence.
+template <typename T, int V, int W, bool SILU>
+__global__ void __launch_bounds__(256) conv_step(const ConvArgs a, T* __restrict__ state, T* __restrict__ y,
+                                                 int n_vec) {
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t n = id / n_vec;
+  const int c = (int)(id - n * n_vec) * V;
+  if (n >= a.tokens) return;
+  const T* __restrict__ x = (const T*)a.x;
+  T* __restrict__ st = state + n * (W - 1) * a.D + c;
+  float taps[W][V], b[V], win[W][V];
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) load_vec<T, V>(st + (int64_t)j * a.D, win[j]);
+  load_vec<T, V>(x + n * a.ld + c, win[W - 1]);
+  load_taps<V, W>(a.w, a.bias, c, taps, b);
+  float u[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    u[i] = b[i];
+#pragma unroll
+    for (int j = 0; j < W; ++j) u[i] += taps[j][i] * win[j][i];
+    if (SILU) u[i] *= sigmoid(u[i]);
+  }
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) store_vec<T, V>(st + (int64_t)j * a.D, win[j + 1]);
+  store_vec<T, V>(y + n * a.D + c, u);
+}
+
+// du from dy and the pre-activation
+template <bool SILU>
+__device__ __forceinline__ float act_grad(float dy, float u) {
+  if (!SILU) return dy;
+  const float g = sigmoid(u);
+  return dy * (g * (1.f + u * (1.f - g)));
+}
+
+template <typename T, int V, int W, bool SILU>
+__global__ void __launch_bounds__(256)
+conv_backward(const ConvArgs a, const T* __restrict__ dy, const T* __restrict__ dfin, T* __restrict__ dx,
+              T* __restrict__ dinit, float* __restrict__ part) {
+  __shared__ float sums[kConvWaves][W + 1][V][64];
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  bool active;
+  const int c = channel_of<V>(blockIdx.y * 64 + lane, a.D, &active);
+  const T* __restrict__ x = (const T*)a.x;
+  const T* __restrict__ init = (const T*)a.init;
+  const Seqs seqs{a.cu, a.n_seqs, a.T, a.tokens};
+  float taps[W][V], b[V];
+  if (blockIdx.x >= a.n_part) {  // one row of one initial state's gradient per wave
+    const int64_t item = (blockIdx.x - a.n_part) * kConvWaves + wave;
+    if (!active || item >= (int64_t)a.n_seqs * (W - 1)) return;
+    const int s = (int)(item / (W - 1)), p = (int)(item % (W - 1));
+    const int64_t lo = seqs.start(s), len = seqs.end(s) - lo;
+    load_taps<V, W>(a.w, a.bias, c, taps, b);
+    float acc[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.f;
+    if (dfin && p >= len) load_vec<T, V>(dfin + ((int64_t)s * (W - 1) + p - len) * a.D + c, acc);
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {  // row p is tap j of token p - j
+      if (p - j < 0 || p - j >= len) continue;
+      float u[V], g[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) u[i] = b[i];
+#pragma unroll
+      for (int m = 0; m < W; ++m) {
+        float v[V];
+        load_row<T, V, W>(x, a.ld, init, a.D, s, lo, p - j - (W - 1) + m, c, v);
+#pragma unroll
+        for (int i = 0; i < V; ++i) u[i] += taps[m][i] * v[i];
+      }
+      load_vec<T, V>(dy + (lo + p - j) * a.D + c, g);
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] += taps[j][i] * act_grad<SILU>(g[i], u[i]);
+    }
+    store_vec<T, V>(dinit + item * a.D + c, acc);
+    return;
+  }
+  float dw[W][V], db[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    db[i] = 0.f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) dw[j][i] = 0.f;
+  }
+  int64_t t = ((int64_t)blockIdx.x * kConvWaves + wave) * a.tile;
+  const int64_t t1 = t + a.tile < a.tokens ? t + a.tile : a.tokens;
+  if (active && t < t1) {
+    load_taps<V, W>(a.w, a.bias, c, taps, b);
+    int s = seqs.from(t + 1) - 1;
+    if (s < 0) s = 0;
+    for (; s < a.n_seqs && t < t1; ++s) {
+      const int64_t lo = seqs.start(s), hi = seqs.end(s);
+      if (hi <= t) continue;
+      if (t < lo) t = lo;
+      // tokens [t, e) of this sequence: their dx needs du up to W - 1 tokens further
+      const int64_t first = t, e = hi < t1 ? hi : t1, last = e + W - 1;
+      float win[W - 1][V], du[W - 1][V];
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j) {
+        load_row<T, V, W>(x, a.ld, init, a.D, s, lo, t - lo - (W - 1) + j, c, win[j]);
+#pragma unroll
+        for (int i = 0; i < V; ++i) du[j][i] = 0.f;
+      }
+      for (; t < last; t += kConvBatch) {
+        float r[kConvBatch][V], g[kConvBatch][V];
+#pragma unroll
+        for (int k = 0; k < kConvBatch; ++k) {
+          const int64_t at = t + k < hi ? t + k : hi - 1;
+          load_vec<T, V>(x + at * a.ld + c, r[k]);
+          load_vec<T, V>(dy + at * a.D + c, g[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < kConvBatch; ++k) {
+          const bool in_seq = t + k < hi, own = t + k < e;
+          float out[V];
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            float u = b[i];
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) u += taps[j][i] * win[j][i];
+            u += taps[W - 1][i] * r[k][i];
+            const float d = in_seq ? act_grad<SILU>(g[k][i], u) : 0.f;
+            const float dm = own ? d : 0.f;
+            db[i] += dm;
+            if (own) {
+#pragma unroll
+              for (int j = 0; j < W - 1; ++j) dw[j][i] += dm * win[j][i];
+              dw[W - 1][i] += dm * r[k][i];
+            }
+            // dx of token t + k - (W - 1)
+            out[i] = taps[0][i] * d;
+#pragma unroll
+            for (int j = 1; j < W; ++j) out[i] += taps[j][i] * du[W - 1 - j][i];
+#pragma unroll
+            for (int j = 0; j + 1 < W - 1; ++j) {
+              win[j][i] = win[j + 1][i];
+              du[j][i] = du[j + 1][i];
+            }
+            win[W - 2][i] = r[k][i];
+            du[W - 2][i] = d;
+          }
+          const int64_t at = t + k - (W - 1);
+          if (at >= first && at < e) {
+            if (dfin && at >= hi - (W - 1)) {
+              float f[V];
+              load_vec<T, V>(dfin + ((int64_t)s * (W - 1) + at - (hi - (W - 1))) * a.D + c, f);
+#pragma unroll
+              for (int i = 0; i < V; ++i) out[i] += f[i];
+            }
+            store_vec<T, V>(dx + at * a.D + c, out);
+          }
+        }
+      }
+      t = e;
+    }
+  }
+  // the workgroup's partial sums, waves in order
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    sums[wave][W][i][lane] = db[i];
+#pragma unroll
+    for (int j = 0; j < W; ++j) sums[wave][j][i][lane] = dw[j][i];
+  }
+  __syncthreads();
+  if (!active) return;
+  float* __restrict__ row = part + (int64_t)blockIdx.x * (W + 1) * a.D;
+  for (int q = wave; q < (W + 1) * V; q += kConvWaves) {
+    const int j = q / V, i = q % V;
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kConvWaves; ++w) v += sums[w][j][i][lane];
+    row[(int64_t)j * a.D + c + i] = v;
+  }
+}
+
+// dweight [D, W] and dbias [D] from the rows of partial sums: 64 columns a
+// workgroup, the rows dealt to its 16 waves and their sums added in order.
+__global__ void __launch_bounds__(1024) conv_params(const float* __restrict__ part, int64_t n_part, int D, int W,
+                                                    float* __restrict__ dw, float* __restrict__ db) {
+  __shared__ float sums[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t cols = (int64_t)(W + 1) * D, col = (int64_t)blockIdx.x * 64 + lane;
+  float v = 0.f;
+  if (col < cols)
+    for (int64_t r = wave; r < n_part; r += 16) v += part[r * cols + col];
+  sums[wave][lane] = v;
+  __syncthreads();
+  if (wave != 0 || col >= cols) return;
+  v = 0.f;
+#pragma unroll
+  for (int w = 0; w < 16; ++w) v += sums[w][lane];
+  const int j = (int)(col / D), c = (int)(col % D);
+  if (j < W)
+    dw[(int64_t)c * W + j] = v;
+  else if (db)
+    db[c] = v;
+}
+
+template <typename T, int V, int W, bool SILU>
+int forward_t(const ConvArgs& a, void* y, void* fin, hipStream_t st) {
+  const int64_t states = fin ? ceil_div((int64_t)a.n_seqs * (W - 1), kConvWaves) : 0;
+  const dim3 grid((unsigned)(a.n_part + states), (unsigned)ceil_div(ceil_div(a.D, V), 64));
+  return (int)launch_kernel(conv_forward<T, V, W, SILU>, grid, dim3(256), st, a, (T*)y, (T*)fin);
+}
+template <typename T, int V, int W, bool SILU>
+int step_t(const ConvArgs& a, void* state, void* y, hipStream_t st) {
+  const int n_vec = a.D / V;
+  const dim3 grid((unsigned)ceil_div(a.tokens * n_vec, 256));
+  return (int)launch_kernel(conv_step<T, V, W, SILU>, grid, dim3(256), st, a, (T*)state, (T*)y, n_vec);
+}
+template <typename T, int V, int W, bool SILU>
+int backward_t(const ConvArgs& a, const void* dy, const void* dfin, void* dx, float* dw, float* db, void* dinit,
+               float* part, hipStream_t st) {
+  const int64_t states = dinit ? ceil_div((int64_t)a.n_seqs * (W - 1), kConvWaves) : 0;
+  const dim3 grid((unsigned)(a.n_part + states), (unsigned)ceil_div(ceil_div(a.D, V), 64));
+  if (grid.x > 0) {
+    const hipError_t e = launch_kernel(conv_backward<T, V, W, SILU>, grid, dim3(256), st, a, (const T*)dy,
+                                       (const T*)dfin, (T*)dx, (T*)dinit, part);
+    if (e != hipSuccess) return (int)e;
+  }
+  return (int)launch_kernel(conv_params, dim3((unsigned)ceil_div((int64_t)(W + 1) * a.D, 64)), dim3(1024), st, part,
+                            a.n_part, a.D, W, dw, db);
+}
+
+// Chooses the instance: type, taps, activation, and vectors of VEC channels
+// or single ones when a row has fewer than VEC (or, with EXACT, when VEC does
+// not divide the row).
+template <typename T, int VEC, bool EXACT, typename F>
+int dispatch_t(int width, int silu, int D, F&& f) {
+  auto w = [&](auto vec) {
+    auto act = [&](auto taps) {
+      return silu ? f(T{}, vec, taps, std::true_type{}) : f(T{}, vec, taps, std::false_type{});
+    };
+    return width == 2   ? act(std::integral_constant<int, 2>{})
+           : width == 3 ? act(std::integral_constant<int, 3>{})
+                        : act(std::integral_constant<int, 4>{});
+  };
+  return D < VEC || (EXACT && D % VEC != 0) ? w(std::integral_constant<int, 1>{})
+                                            : w(std::integral_constant<int, VEC>{});
+}
+template <bool BACKWARD, bool EXACT, typename F>
+int dispatch(int is_bf16, int width, int silu, int D, F&& f) {
+  return is_bf16 ? dispatch_t<bf16_t, conv_vec(true, BACKWARD), EXACT>(width, silu, D, f)
+                 : dispatch_t<float, conv_vec(false, BACKWARD), EXACT>(width, silu, D, f);
+}
+
+}  // namespace
+
+int launch_conv_forward(int is_bf16, int width, int silu, const ConvArgs& a, void* y, void* fin, void* stream) {
+  return dispatch<false, false>(is_bf16, width, silu, a.D, [&](auto t, auto vec, auto taps, auto act) {
+    return forward_t<decltype(t), vec.value, taps.value, act.value>(a, y, fin, (hipStream_t)stream);
+  });
+}
+int launch_conv_step(int is_bf16, int width, int silu, const ConvArgs& a, void* state, void* y, void* stream) {
+  return dispatch<false, true>(is_bf16, width, silu, a.D, [&](auto t, auto vec, auto taps, auto act) {
+    return step_t<decltype(t), vec.value, taps.value, act.value>(a, state, y, (hipStream_t)stream);
+  });
+}
+int launch_conv_backward(int is_bf16, int width, int silu, const ConvArgs& a, const void* dy, const void* dfin,
+                         void* dx, float* dw, float* db, void* dinit, float* part, void* stream) {
+  return dispatch<true, false>(is_bf16, width, silu, a.D, [&](auto t, auto vec, auto taps, auto act) {
+    return backward_t<decltype(t), vec.value, taps.value, act.value>(a, dy, dfin, dx, dw, db, dinit, part,
+                                                                     (hipStream_t)stream);
+  });
+}
+
+}  // namespace kda

@@ -64,7 +64,7 @@
 extern "C" {
 #endif
 
-#define KDA_VERSION 20000 /* 2.0.0 */
+#define KDA_VERSION 20100 /* 2.1.0 */
 
 typedef enum {
   KDA_OK = 0,
@@ -387,6 +387,203 @@ int kda_decode_step(int N, int H, int d_k, int d_v, kda_dtype_t dtype, float g_f
 int kda_decode_step_gated(int N, int H, int d_k, int d_v, kda_dtype_t dtype, kda_gate_t gate,
                           float g_floor, const void* q, const void* k, const void* v, const void* g,
                           const float* beta, float* state, void* o, void* stream);
+
+/* ---- the operators around the recurrence --------------------------------
+ *
+ * What makes a layer's q, k and v from its projections (a short causal
+ * convolution over the tokens, a norm and a position rotation for every
+ * head), and the recurrence with a diagonal transition that hybrid models
+ * put beside the delta rule (a selective state space scan).  The conventions
+ * at the top of this header hold, with these differences:
+ *   - Some inputs may be column slices of a wider row-major array (the output
+ *     of one projection): `ld_*` is the distance between consecutive tokens'
+ *     rows in elements (0: the row length, that is, contiguous rows), at
+ *     least the row length.  Tokens are numbered through the whole batch, so
+ *     one distance serves every batch row.  A row itself is contiguous.
+ *   - Inputs and outputs need the alignment of their elements only (a slice
+ *     starts anywhere); the workspace needs 256 bytes.
+ *   - There is no floor and no sign rule on any input.
+ *   - Packed batches: cu_seqlens as kda_chunk_forward.  Sequences may be
+ *     empty (their final state is their initial state).
+ *   - Sums, states and statistics are held in fp32, outputs are rounded once.
+ *     Results do not depend on the launch: no atomics, every sum has a fixed
+ *     order.
+ */
+
+typedef enum { KDA_ACT_NONE = 0, KDA_ACT_SILU = 1 } kda_act_t;
+typedef enum { KDA_NORM_UNIT = 0, KDA_NORM_RMS = 1 } kda_norm_t;
+
+/* Shape of one short convolution. */
+typedef struct {
+  int B;            /* batch; must be 1 when n_seqs > 0                      */
+  int T;            /* tokens per batch row (packed total when n_seqs > 0)   */
+  int D;            /* channels                                              */
+  int width;        /* taps: 2, 3 or 4                                       */
+  int n_seqs;       /* 0: B sequences of T tokens; > 0: packed sequences     */
+  kda_dtype_t dtype;/* dtype of x, y, the states and their gradients         */
+  kda_act_t activation;
+  int64_t ld_x;     /* distance between token rows of x, in elements (0: D)  */
+} kda_conv_desc_t;
+
+/*
+ * Short causal convolution, one filter per channel.  For every sequence,
+ * with xe the sequence preceded by its initial state's width - 1 inputs:
+ *     u_t = bias + sum_{j < width} weight[:, j] xe_{t + j}
+ *         (the last tap meets token t, the ones before it earlier tokens)
+ *     y_t = u_t, or u_t sigmoid(u_t) with KDA_ACT_SILU
+ *   x       : [B, T, D] dtype, rows ld_x apart
+ *   weight  : [D, width] fp32           bias: [D] fp32 or NULL
+ *   initial_state : [S, width - 1, D] dtype, oldest input first, or NULL
+ *             (zeros); S = n_seqs or B
+ *   y       : [B, T, D] dtype, written
+ *   final_state : [S, width - 1, D] dtype, written (the sequence's last
+ *             width - 1 inputs, taken from the initial state where it has
+ *             fewer), or NULL
+ * Outputs must not overlap each other or any input.
+ */
+int kda_short_conv_forward(const kda_conv_desc_t* d, const void* x, const float* weight, const float* bias,
+                           const void* initial_state, const int32_t* cu_seqlens, void* y, void* final_state,
+                           void* stream);
+
+/*
+ * One new token for each of d->B sequences (d->T must be 1, d->n_seqs 0),
+ * the state updated in place: x [B, D] (rows ld_x apart), y [B, D], state
+ * [B, width - 1, D].  The same results as kda_short_conv_forward on one
+ * token.  y and state must not overlap each other or any input.
+ */
+int kda_short_conv_step(const kda_conv_desc_t* d, const void* x, const float* weight, const float* bias, void* state,
+                        void* y, void* stream);
+
+/*
+ * Gradients of <dy, y> + <dfinal, final_state>.
+ *   dy      : [B, T, D] dtype;   dfinal : [S, width - 1, D] dtype or NULL (zero)
+ *   dx      : [B, T, D] dtype;   dweight: [D, width] fp32
+ *   dbias   : [D] fp32 or NULL;  dinitial: [S, width - 1, D] dtype or NULL
+ * Every output given is written (dx, dweight are required).  The workspace
+ * (kda_short_conv_backward_workspace_size) holds partial sums of dweight and
+ * dbias over ranges of tokens.  Outputs must not overlap each other, the
+ * inputs or the workspace.
+ */
+int kda_short_conv_backward_workspace_size(const kda_conv_desc_t* d, size_t* bytes);
+int kda_short_conv_backward(const kda_conv_desc_t* d, const void* x, const float* weight, const float* bias,
+                            const void* initial_state, const int32_t* cu_seqlens, const void* dy, const void* dfinal,
+                            void* dx, float* dweight, float* dbias, void* dinitial, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* Shape of one selective scan. */
+typedef struct {
+  int B;            /* batch; must be 1 when n_seqs > 0                      */
+  int T;            /* tokens per batch row (packed total when n_seqs > 0)   */
+  int D;            /* channels                                              */
+  int N;            /* states per channel: 1 .. 64                           */
+  int G;            /* groups of D / G channels that share B and C           */
+  int n_seqs;       /* 0: B sequences of T tokens; > 0: packed sequences     */
+  kda_dtype_t dtype;/* dtype of x, dt, z, B, C, o and their gradients        */
+  int softplus;     /* nonzero: delta = softplus(dt + dt_bias), else dt + dt_bias */
+  int64_t ld_x, ld_dt, ld_z; /* distances between token rows (0: D)          */
+  int64_t ld_b, ld_c;        /* the same for B and C (0: G * N)              */
+} kda_scan_desc_t;
+
+/*
+ * Selective state space scan.  Per sequence, channel c (of group g) and
+ * state n, from h = h0 (or zeros):
+ *     delta_t = softplus(dt_t + dt_bias_c)
+ *     h_t[n]  = exp(delta_t A[c, n]) h_{t-1}[n] + delta_t B_t[g, n] x_t
+ *     y_t     = sum_n C_t[g, n] h_t[n] + skip_c x_t
+ *     o_t     = y_t z_t sigmoid(z_t)       (y_t when z is NULL)
+ *   x, dt, z: [B, T, D] dtype (z may be NULL), rows ld_* apart
+ *   A       : [D, N] fp32               skip, dt_bias: [D] fp32 or NULL (zero)
+ *   Bm, Cm  : [B, T, G, N] dtype, token rows ld_b, ld_c apart
+ *   h0      : [S, D, N] fp32 or NULL (zero state); S = n_seqs or B
+ *   o       : [B, T, D] dtype, written
+ *   ht      : [S, D, N] fp32, written, or NULL
+ * Outputs must not overlap each other, the inputs or the workspace (in
+ * particular ht is not h0: parts of a sequence are scanned at the same time).
+ * A NaN or Inf reaches later tokens of its sequence, never another sequence.
+ * The workspace (kda_selective_scan_workspace_size; 0 bytes when the batch
+ * alone fills the device) holds the state of every range of tokens that the
+ * call scans side by side.
+ */
+int kda_selective_scan_workspace_size(const kda_scan_desc_t* d, size_t* bytes);
+int kda_selective_scan_forward(const kda_scan_desc_t* d, const void* x, const void* dt, const float* A,
+                               const void* Bm, const void* Cm, const float* skip, const void* z,
+                               const float* dt_bias, const float* h0, const int32_t* cu_seqlens, void* o, float* ht,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One new token for each of d->B sequences (d->T must be 1, d->n_seqs 0),
+ * the state [B, D, N] updated in place; o [B, D].  o and state must not
+ * overlap each other or any input.
+ */
+int kda_selective_scan_step(const kda_scan_desc_t* d, const void* x, const void* dt, const float* A, const void* Bm,
+                            const void* Cm, const float* skip, const void* z, const float* dt_bias, float* state,
+                            void* o, void* stream);
+
+/*
+ * Gradients of <dout, o> + <dht, ht>.
+ *   dout    : [B, T, D] dtype;           dht: [S, D, N] fp32 or NULL (zero)
+ *   dx, ddt : [B, T, D] dtype;           dA : [D, N] fp32
+ *   dB, dC  : [B, T, G, N] dtype, contiguous
+ *   dskip, ddt_bias: [D] fp32 or NULL (not written)
+ *   dz      : [B, T, D] dtype; required with z, ignored without
+ *   dh0     : [S, D, N] fp32 or NULL (not written)
+ * The workspace holds partial sums and the states between ranges of tokens.
+ * Outputs must not overlap each other, the inputs or the workspace.  A NaN
+ * or Inf may reach dB and dC of up to 15 tokens before its own, in the same
+ * sequence (their sums over channels are matrix products over 16 tokens).
+ */
+int kda_selective_scan_backward_workspace_size(const kda_scan_desc_t* d, size_t* bytes);
+int kda_selective_scan_backward(const kda_scan_desc_t* d, const void* x, const void* dt, const float* A,
+                                const void* Bm, const void* Cm, const float* skip, const void* z,
+                                const float* dt_bias, const float* h0, const int32_t* cu_seqlens, const void* dout,
+                                const float* dht, void* dx, void* ddt, float* dA, void* dB, void* dC, float* dskip,
+                                void* dz, float* ddt_bias, float* dh0, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/* Shape of one norm of queries and keys. */
+typedef struct {
+  int n_tokens;     /* tokens of the whole batch                             */
+  int Hq, Hk;       /* heads of q and of k                                   */
+  int d;            /* channels per head: even, 2 .. 512                     */
+  int rot;          /* channels rotated: even, 0 .. d (0: no rotation)       */
+  kda_dtype_t dtype;
+  kda_norm_t norm;
+  int interleaved;  /* rotated pairs are channels (2i, 2i + 1), else (i, i + rot / 2) */
+  float eps;        /* >= 0, finite                                          */
+  float q_scale;    /* factor on q's output                                  */
+  int64_t ld_q, ld_k;/* distances between token rows (0: Hq d, Hk d)         */
+} kda_qk_norm_desc_t;
+
+/*
+ * Norm of every query and key head and the rotation by the token's position,
+ * in one pass.  For each head x of d channels:
+ *     r   = (sum x^2 + eps)^-1/2  (KDA_NORM_UNIT: unit vectors, as the delta
+ *           rule's q and k) or (mean x^2 + eps)^-1/2  (KDA_NORM_RMS)
+ *     v   = x r weight
+ *     pair i < rot / 2 of v turned by the angle positions[t] inv_freq[i]:
+ *           (a, b) -> (a cos - b sin, a sin + b cos)
+ *     q_out = q_scale v,  k_out = v
+ *   q, k    : [n_tokens, Hq, d], [n_tokens, Hk, d] dtype, token rows ld_* apart
+ *   q_weight, k_weight: [d] fp32 or NULL (ones)
+ *   positions: [n_tokens] int32, inv_freq: [rot / 2] fp32; NULL when rot is 0
+ *   q_out, k_out: contiguous, written; must not overlap anything
+ * The angle is reduced in 64 bits, so far positions keep their accuracy.
+ */
+int kda_qk_norm_forward(const kda_qk_norm_desc_t* d, const void* q, const void* k, const float* q_weight,
+                        const float* k_weight, const int32_t* positions, const float* inv_freq, void* q_out,
+                        void* k_out, void* stream);
+
+/*
+ * Gradients of <dq_out, q_out> + <dk_out, k_out>; dq_out, dk_out, dq, dk are
+ * contiguous; dq_weight, dk_weight: [d] fp32 or NULL (not written; given
+ * without the weight they are the gradient at a weight of ones).  The
+ * workspace holds partial sums of the weights' gradients.
+ */
+int kda_qk_norm_backward_workspace_size(const kda_qk_norm_desc_t* d, size_t* bytes);
+int kda_qk_norm_backward(const kda_qk_norm_desc_t* d, const void* q, const void* k, const float* q_weight,
+                         const float* k_weight, const int32_t* positions, const float* inv_freq, const void* dq_out,
+                         const void* dk_out, void* dq, void* dk, float* dq_weight, float* dk_weight, void* workspace,
+                         size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,239 @@
+"""Selective scan against its plain 64-bit form, every element.
+
+Tolerance (layer_reference.check): half a step of the output's type plus fp32
+roundings (2^-24) of the magnitudes, the plain form's sums of absolute values.
+A step of the recurrence multiplies by an exponential that is off by at most
+delta |A| + 3 roundings (delta |A| times a decay of e^-(delta |A|) is below
+0.4) and adds two more, so t steps are off by at most 8 t; the sums over
+states and the gates add under 64.  The gradient composes two such
+recurrences (16 t + 128).
+"""
+import pytest
+import torch
+
+import gated_delta_rule_105_amd as kda
+import layer_reference as ref
+from gpu_util import note
+from layer_reference import check
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def inputs(B, T, D, N, dtype, G=1, lengths=None, state=True, gate=True, skip=True, bias=True, softplus=True,
+           fused=False, seed=0):
+    g = torch.Generator().manual_seed(3000 + seed)
+    r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    dt = DT[dtype]
+    cu = None
+    if lengths is not None:
+        B, T = 1, sum(lengths)
+        cu = torch.tensor([sum(lengths[:i]) for i in range(len(lengths) + 1)], dtype=torch.int32).cuda()
+    S = B if cu is None else len(lengths)
+
+    def cut(*widths):
+        if fused:
+            whole = r(B, T, sum(widths) + 3).to(dt).cuda()
+            return [t for t in whole[..., 1: 1 + sum(widths)].split(list(widths), dim=-1)]
+        return [r(B, T, w).to(dt).cuda() for w in widths]
+    x, z = cut(D, D)
+    Bm, Cm = (t.unflatten(-1, (G, N)) for t in cut(G * N, G * N))
+    step = r(B, T, D)
+    p = dict(x=x, dt=(step if softplus else 0.2 * step.abs()).to(dt).cuda(),
+             A=-torch.exp(r(D, N)).cuda(), B=Bm, C=Cm, D=r(D).cuda() if skip else None, z=z if gate else None,
+             dt_bias=(r(D) - 2 if softplus else 0.1 * r(D).abs()).cuda() if bias else None)
+    q = dict(h0=r(S, D, N).cuda() if state else None, cu_seqlens=cu)
+    u = dict(do=r(B, T, D).to(dt).cuda(), dht=r(S, D, N).cuda() if state else None)
+    return p, q, u, softplus
+
+
+CASES = {
+    "one-token": dict(B=1, T=1, D=4, N=16, dtype="bf16"),
+    "one-channel-one-state": dict(B=1, T=20, D=1, N=1, dtype="f32"),
+    "group-edges-15": dict(B=2, T=15, D=16, N=16, dtype="f32", state=False),
+    "group-edges-16": dict(B=2, T=16, D=17, N=16, dtype="f32"),
+    "group-edges-17": dict(B=1, T=17, D=33, N=12, dtype="bf16"),
+    "tile-edges": dict(B=3, T=65, D=20, N=8, dtype="bf16"),
+    "17-states": dict(B=1, T=70, D=18, N=17, dtype="f32"),
+    "32-states": dict(B=1, T=300, D=8, N=32, dtype="bf16"),
+    "33-states": dict(B=2, T=40, D=6, N=33, dtype="f32"),
+    "64-states": dict(B=1, T=280, D=5, N=64, dtype="bf16"),
+    "groups": dict(B=1, T=50, D=24, N=16, G=3, dtype="bf16"),
+    "groups-odd": dict(B=1, T=270, D=63, N=5, G=3, dtype="f32"),
+    "plain": dict(B=1, T=60, D=16, N=16, dtype="bf16", state=False, gate=False, skip=False, bias=False),
+    "delta-given": dict(B=1, T=90, D=16, N=16, dtype="f32", softplus=False),
+    "slots": dict(B=1, T=700, D=20, N=16, dtype="bf16"),
+    "slots-dividing-the-row": dict(B=2, T=768, D=16, N=16, dtype="f32"),
+    "slots-rows": dict(B=3, T=257, D=19, N=16, dtype="f32", state=False),
+    "rows-fill-the-device": dict(B=64, T=20, D=64, N=4, dtype="bf16"),
+    "packed": dict(B=1, T=0, D=20, N=16, dtype="bf16", lengths=[0, 1, 2, 0, 64, 17, 130, 1, 16, 0]),
+    "packed-slots": dict(B=1, T=0, D=21, N=16, dtype="f32", lengths=[3, 400, 0, 0, 129, 1, 256, 255, 64, 0]),
+    "packed-slots-no-state": dict(B=1, T=0, D=9, N=24, dtype="bf16", lengths=[256, 256, 512, 1], state=False),
+    "packed-all-empty": dict(B=1, T=0, D=9, N=4, dtype="f32", lengths=[0, 0, 0]),
+    "slices": dict(B=2, T=45, D=27, N=10, G=3, dtype="bf16", fused=True),
+    "slices-f32": dict(B=1, T=300, D=26, N=16, dtype="f32", fused=True),
+}
+
+
+def longest(c):
+    return max(c["lengths"]) if c.get("lengths") else c["T"]
+
+
+@pytest.mark.parametrize("case", CASES)
+def test_forward(case):
+    p, q, _, softplus = inputs(**CASES[case])
+    note(f"selective_scan_forward {case}")
+    o, ht = kda.selective_scan_forward(**p, **q, dt_softplus=softplus)
+    torch.cuda.synchronize()
+    ro, rht, mo, mht = ref.scan(**p, h0=q["h0"], cu=q["cu_seqlens"], softplus=softplus)
+    n = 64 + 8 * longest(CASES[case])
+    check("o", o, ro, mo, n)
+    check("ht", ht, rht, mht, n)
+
+
+@pytest.mark.parametrize("case", CASES)
+def test_backward(case):
+    p, q, u, softplus = inputs(**CASES[case], seed=1)
+    note(f"selective_scan_backward {case}")
+    g = kda.selective_scan_backward(**p, **q, **u, dt_softplus=softplus)
+    torch.cuda.synchronize()
+    rg, rm = ref.scan_grad(**p, **u, h0=q["h0"], cu=q["cu_seqlens"], softplus=softplus)
+    n = 128 + 16 * longest(CASES[case])
+    tokens = p["x"].shape[0] * p["x"].shape[1]
+    for key, given in (("dx", 1), ("ddt", 1), ("dA", 1), ("dB", 1), ("dC", 1), ("dD", p["D"]), ("dz", p["z"]),
+                       ("ddt_bias", p["dt_bias"]), ("dh0", q["h0"])):
+        if given is None:
+            assert g[key] is None, key
+        else:
+            check(key, g[key], rg[key], rm[key], n + (tokens if key in ("dA", "dD", "ddt_bias") else 0))
+
+
+@pytest.mark.parametrize("S,D,N,G,dtype,fused", [(1, 4, 16, 1, "bf16", False), (5, 33, 16, 3, "bf16", True),
+                                                 (3, 7, 1, 1, "f32", False), (2, 10, 6, 2, "f32", True),
+                                                 (9, 64, 32, 1, "bf16", False), (2, 5, 61, 1, "f32", False),
+                                                 (2, 6, 64, 2, "bf16", True)])
+def test_step_against_the_plain_form(S, D, N, G, dtype, fused):
+    """Five tokens one at a time, the state in place, against the whole sequences in 64 bits."""
+    p, q, _, _ = inputs(S, 5, D, N, dtype, G=G, fused=fused, seed=2)
+    note(f"selective_scan_step S={S} D={D} N={N}")
+    ro, rht, mo, mht = ref.scan(**p, h0=q["h0"])
+    state = q["h0"].clone()
+    for t in range(5):
+        tok = {k: (v[:, t] if k in ("x", "dt", "z", "B", "C") else v) for k, v in p.items()}
+        o = kda.selective_scan_step(state=state, **tok)
+        torch.cuda.synchronize()
+        check("o", o, ro[:, t], mo[:, t], 64 + 40)
+    check("state", state, rht, mht, 64 + 40)
+
+
+def test_prompt_then_steps():
+    """A prompt's final state continued by steps gives what the longer prompt gives."""
+    p, q, _, _ = inputs(2, 200, 24, 16, "f32", seed=3)
+    note("selective_scan prompt then steps")
+    o, ht = kda.selective_scan_forward(**p, **q)
+    cut = {k: (v[:, :197] if k in ("x", "dt", "z", "B", "C") else v) for k, v in p.items()}
+    cut = {k: (v.contiguous() if v is not None and k in ("x", "dt", "z", "B", "C") else v) for k, v in cut.items()}
+    _, state = kda.selective_scan_forward(**cut, h0=q["h0"])
+    ro, rht, mo, mht = ref.scan(**p, h0=q["h0"])
+    for t in range(197, 200):
+        tok = {k: (v[:, t] if k in ("x", "dt", "z", "B", "C") else v) for k, v in p.items()}
+        ot = kda.selective_scan_step(state=state, **tok)
+        check("o", ot, ro[:, t], mo[:, t], 64 + 8 * 200)
+    check("state", state, rht, mht, 64 + 8 * 200)
+    check("ht", ht, rht, mht, 64 + 8 * 200)
+
+
+def test_extreme_rates_and_steps():
+    """Decays of 1 (A = 0), of 0 (A = -inf, huge delta) and tokens without a step (delta = 0) at ragged lengths."""
+    p, q, _, _ = inputs(1, 0, 16, 8, "f32", lengths=[5, 300, 21], seed=4)
+    note("selective_scan extremes")
+    p["A"][0] = 0.0
+    p["A"][1] = float("-inf")
+    p["A"][2] = -1e30
+    p["dt"][0, 100:110] = 60.0
+    p["dt"][0, 120:140, 3:] = -200.0  # softplus of it is 0 in fp32; A = -inf needs a positive step
+    o, ht = kda.selective_scan_forward(**p, **q)
+    torch.cuda.synchronize()
+    ro, rht, mo, mht = ref.scan(**p, h0=q["h0"], cu=q["cu_seqlens"])
+    n = 64 + 8 * 300
+    check("o", o, ro, mo, n)
+    check("ht", ht, rht, mht, n)
+
+
+def test_nan_stays_in_its_sequence_and_channel():
+    p, q, u, _ = inputs(1, 0, 20, 16, "f32", lengths=[50, 300, 40], seed=5)
+    note("selective_scan nan")
+    o, ht = kda.selective_scan_forward(**p, **q)
+    g = kda.selective_scan_backward(**p, **q, **u)
+    p2 = dict(p, x=p["x"].clone())
+    p2["x"][0, 200, 7] = float("nan")
+    o2, ht2 = kda.selective_scan_forward(**p2, **q)
+    hit = torch.zeros_like(o, dtype=torch.bool)
+    hit[0, 200:350, 7] = True
+    assert torch.equal(torch.isnan(o2), hit) and torch.equal(o2[~hit], o[~hit])
+    hit_h = torch.zeros_like(ht, dtype=torch.bool)
+    hit_h[1, 7] = True
+    assert torch.equal(torch.isnan(ht2), hit_h) and torch.equal(ht2[~hit_h], ht[~hit_h])
+    g2 = kda.selective_scan_backward(**p2, **q, **u)
+    for key in ("dx", "ddt", "dz"):
+        other = torch.ones(g[key].shape, dtype=torch.bool, device="cuda")
+        other[0, 50:350, 7] = False
+        assert torch.equal(g2[key][other], g[key][other]), key
+    # tokens of the group of 16 that holds token 200, and earlier ones of its sequence, aside
+    for key in ("dB", "dC"):
+        assert torch.equal(g2[key][0, :185], g[key][0, :185]) and torch.equal(g2[key][0, 350:], g[key][0, 350:]), key
+
+
+def test_slots_do_not_matter():
+    """The same tokens as one batch row and as a packed sequence among others (other ranges of tokens are scanned
+    side by side) agree to rounding."""
+    p, q, u, _ = inputs(1, 700, 20, 16, "f32", seed=6)
+    note("selective_scan slots")
+    o, ht = kda.selective_scan_forward(**p, **q)
+    lead = 77
+    pad = lambda t: torch.cat([torch.zeros_like(t[:, :lead]), t], 1)  # noqa: E731
+    p2 = {k: (pad(v) if k in ("x", "dt", "z", "B", "C") else v) for k, v in p.items()}
+    cu = torch.tensor([0, lead, lead + 700], dtype=torch.int32, device="cuda")
+    h0 = torch.cat([torch.zeros_like(q["h0"]), q["h0"]])
+    o2, ht2 = kda.selective_scan_forward(**p2, h0=h0, cu_seqlens=cu)
+    _, _, mo, mht = ref.scan(**p, h0=q["h0"])
+    n = 2 * (64 + 8 * 700)
+    check("o", o2[:, lead:], o.double().cpu(), mo, n)
+    check("ht", ht2[1:], ht.double().cpu(), mht, n)
+
+
+def test_autograd_and_determinism():
+    p, q, u, _ = inputs(2, 150, 20, 16, "f32", seed=7)
+    note("selective_scan autograd")
+    leaves = {k: v.clone().requires_grad_() for k, v in dict(p, h0=q["h0"]).items()}
+    o, ht = kda.selective_scan(**leaves)
+    ((o * u["do"]).sum() + (ht * u["dht"]).sum()).backward()
+    g = kda.selective_scan_backward(**p, **q, **u)
+    again = kda.selective_scan_backward(**p, **q, **u)
+    for k, name in (("x", "dx"), ("dt", "ddt"), ("A", "dA"), ("B", "dB"), ("C", "dC"), ("D", "dD"), ("z", "dz"),
+                    ("dt_bias", "ddt_bias"), ("h0", "dh0")):
+        assert torch.equal(leaves[k].grad, g[name]), k
+        assert torch.equal(again[name], g[name]), k
+
+
+def test_gradient_against_differences():
+    """The fp32 gradient along random directions against central differences of the 64-bit forward."""
+    p, q, u, _ = inputs(1, 0, 10, 16, "f32", lengths=[40, 0, 300], seed=8)
+    note("selective_scan differences")
+    g = kda.selective_scan_backward(**p, **q, **u)
+    torch.cuda.synchronize()
+    base = {k: ref.f64(v) for k, v in dict(p, h0=q["h0"]).items()}
+    do, dht = ref.f64(u["do"]), ref.f64(u["dht"])
+
+    def f(v):
+        o, ht, _, _ = ref.scan(**v, cu=q["cu_seqlens"])
+        return float((o * do).sum() + (ht * dht).sum())
+    gen = torch.Generator().manual_seed(9)
+    step = 1e-5
+    for key in base:
+        d = torch.randn(base[key].shape, generator=gen, dtype=torch.float64)
+        diff = (f(dict(base, **{key: base[key] + step * d})) - f(dict(base, **{key: base[key] - step * d}))) / (2 * step)
+        got = ref.f64(g["d" + key])
+        # each element is off by at most its share of 16 * 300 + 128 roundings; the directions' signs are random
+        room = 5000 * 2.0 ** -24 * float((got * d).abs().sum()) + 1e-5
+        assert abs(float((got * d).sum()) - diff) <= room, key
