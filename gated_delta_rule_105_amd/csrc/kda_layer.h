@@ -58,9 +58,9 @@ inline int conv_backward_tile(int64_t tokens, int D) {
 inline int64_t conv_parts(int64_t tokens, int tile) { return ceil_div(ceil_div(tokens, tile), kConvWaves); }
 
 // ---- selective scan --------------------------------------------------------
-// A wave holds 4 channels of 16 lanes; lane j of a channel holds states
-// j, j + 16, ... (NS of them).  A call cuts the tokens of the whole batch
-// into slots of `slot` tokens; each workgroup scans one slot of its channels.
+// A call cuts the tokens of the whole batch into slots of `slot` tokens; each
+// workgroup scans one slot of its channels.  The forward scans give a wave 16
+// channels, the backward scan 4 (whose lanes hold scan_ns(N) states each).
 constexpr int kScanMaxStates = 64;
 constexpr int kScanTile = 64;  // tokens of B and C staged at once (forward)
 inline int scan_ns(int N) { return N <= 16 ? 1 : N <= 32 ? 2 : 4; }
@@ -73,42 +73,50 @@ struct ScanArgs {
   int n_seqs;
   int64_t T, tokens;
   int D, N, G, softplus;
+  int has_z;  // 0: z is x again, loaded and not used
   int64_t slot, n_slots;
   int blocks_per_group;  // workgroups over the channels of one group
 };
 
-// Workspace of a forward call: the state that every slot hands on (from a
-// zero state when its first sequence began earlier) and its sum of delta.
+// Workspace of a forward call: the state that every slot hands on, its sum of
+// delta, and a word that says what passes through it.
 struct ScanPlan {
   int64_t slot, n_slots;
   bool carry;  // some sequence may pass from one slot to the next
-  size_t hend_off, sum_off, ws_bytes;
+  size_t hend_off, sum_off, kind_off, ws_bytes;
 };
 constexpr int kScanWaves = 4;  // waves per workgroup (forward)
 
 inline ScanPlan plan_scan(int64_t tokens, int rows, int64_t T, bool packed, int D, int N, int G, int n_cu) {
   ScanPlan p{};
   const int64_t cus = n_cu > 0 ? n_cu : 256;
-  const int64_t waves = (int64_t)G * ceil_div(D / G, 4 * kScanWaves) * kScanWaves;  // of one slot
+  const int64_t waves = (int64_t)G * ceil_div(D / G, 16);  // of one slot
   if (tokens == 0) {
     p.slot = 1;
     p.n_slots = 1;
-  } else if (!packed && waves * rows >= 4 * cus) {
+  } else if (!packed && waves * rows >= 6 * cus) {
     p.slot = T;  // the rows alone put a wave on every SIMD
     p.n_slots = rows;
   } else {
     int64_t n = 16 * cus / waves;
-    if (n > tokens / 128) n = tokens / 128;
+    if (n > tokens / 64) n = tokens / 64;
+    if (n > 512) n = 512;
     if (n < 1) n = 1;
     p.slot = ceil_div(ceil_div(tokens, n), kScanTile) * kScanTile;
     p.n_slots = ceil_div(tokens, p.slot);
   }
   p.carry = p.n_slots > 1 && (packed || p.slot % T != 0);
-  const size_t up = 255;
-  const size_t hend = p.carry ? (size_t)p.n_slots * D * N * 4 : 0;
-  p.hend_off = 0;
-  p.sum_off = (hend + up) / 256 * 256;
-  p.ws_bytes = p.carry ? (p.sum_off + (size_t)p.n_slots * D * 4 + up) / 256 * 256 : 0;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = (off + bytes + 255) / 256 * 256;
+    return at;
+  };
+  const size_t slots = p.carry ? (size_t)p.n_slots : 0;
+  p.hend_off = take(slots * D * N * 4);
+  p.sum_off = take(slots * D * 4);
+  p.kind_off = take(slots * 4);
+  p.ws_bytes = off;
   return p;
 }
 
@@ -124,9 +132,10 @@ struct ScanBwdPlan {
   int64_t slot, n_slots;
   bool carry;
   int blocks_per_group;
-  // byte offsets: forward state and adjoint at the slot's edges, sum of
-  // delta, per-slot sums of dA, dskip and ddt_bias, per-workgroup sums of dB, dC
-  size_t hend_off, adj_off, sum_off, da_off, dskip_off, dbias_off, db_off, dc_off, ws_bytes;
+  // byte offsets: state at the slots' ends and gradient at their starts, sum
+  // of delta, what passes through, per-slot sums of dA, dskip and ddt_bias,
+  // per-workgroup sums of dB and dC
+  size_t hend_off, adj_off, sum_off, kind_off, da_off, dskip_off, dbias_off, db_off, dc_off, ws_bytes;
 };
 
 inline ScanBwdPlan plan_scan_backward(int64_t tokens, int D, int N, int G) {
@@ -146,6 +155,7 @@ inline ScanBwdPlan plan_scan_backward(int64_t tokens, int D, int N, int G) {
   p.hend_off = take(p.carry ? slots * dn : 0);
   p.adj_off = take(p.carry ? slots * dn : 0);
   p.sum_off = take(p.carry ? slots * D * 4 : 0);
+  p.kind_off = take(p.carry ? slots * 4 : 0);
   p.da_off = take(slots * dn);
   p.dskip_off = take(slots * D * 4);
   p.dbias_off = take(slots * D * 4);

@@ -270,6 +270,10 @@ int check_scan(const kda_scan_desc_t* d, ScanSizes* s) {
   // one workgroup per 16 channels and at least 64 tokens, in one grid dimension
   const double groups = (double)d->G * ceil((double)(d->D / d->G) / 16.0);
   if (groups * (ceil((double)n / 64.0) + (double)s->t.seqs + 8.0) > 2.0e9) return KDA_ERR_UNSUPPORTED;
+  // the kernels count tokens in 32 bits and look a tile ahead; a lane's offset inside 16 rows has 32 bits
+  if (n > (size_t)INT32_MAX - 4096) return KDA_ERR_UNSUPPORTED;
+  for (int64_t ld : {a.ld_x, a.ld_dt, a.ld_z, (int64_t)d->D})
+    if (ld > (1 << 24)) return KDA_ERR_UNSUPPORTED;
   a.n_seqs = (int)s->t.seqs;
   a.T = d->T;
   a.tokens = (int64_t)n;
@@ -305,7 +309,9 @@ void scan_args(kda::ScanArgs* a, const void* x, const void* dt, const float* A, 
   a->Bm = Bm;
   a->Cm = Cm;
   a->skip = skip;
-  a->z = z;
+  a->z = z ? z : x;
+  a->has_z = z != nullptr;
+  if (!z) a->ld_z = a->ld_x;
   a->bias = dt_bias;
   a->h0 = h0;
   a->cu = cu;

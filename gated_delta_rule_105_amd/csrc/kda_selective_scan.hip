@@ -12,35 +12,36 @@
 //
 // Every (token, channel, state) costs an exponential of its own, so no
 // matrix product stands for the scan, and at 16 states it is the vector unit
-// that bounds it: per element one exponential (four issue slots), the
-// argument, the update (two) and the sum's product.
+// that bounds it: per element an exponential, its argument, the update (two)
+// and the sum's product.
 //
-// Layout.  A row of 16 lanes holds one channel, lane j the states j, j + 16,
-// ...: a wave has 4 channels, a workgroup of 4 waves 16.  Tokens come in
-// groups of 16, and lane j also prepares token j of the group (delta,
-// delta x, the gates), so that this work is done once per token and channel;
-// inside the recurrence token k's values are lane k's, broadcast over the
-// row as an operand modifier.  The 16 sums over the states of a group are
-// taken together (row_sums), after which lane j holds token j's output.  B
-// and C of 64 tokens are staged in LDS as fp32, [state][token] with rows of
-// 68 words: four tokens are one 16-byte read, free of bank conflicts.
+// Layout of the forward scans ("quads").  A wave holds 16 channels, lane l
+// channel l % 16 and the quarter l / 16 of its states (NS of them), so four
+// lanes share a channel.  Tokens come in groups of 16; the four lanes of a
+// channel each prepare four of them (delta, delta x, the gate), which makes
+// that work once per token and channel, and exchange the results by swapping
+// rows of 16 lanes.  A token's sum over the states is the lane's own products
+// and a sum over the four quarters; those of four tokens are taken together
+// (three swaps, three additions) and come out in the lanes that prepared the
+// tokens.
+// B and C of 64 tokens are staged in LDS as fp32, [token][state]; a lane
+// reads its quarter, the same address for all 16 channels.
 //
 // The time axis is cut into slots when the channels alone do not fill the
 // device.  A first launch scans every slot that a sequence leaves
 // unfinished, from a zero state if the sequence entered it from an earlier
 // slot, and keeps the state it hands on and the slot's sum of delta; the
-// second composes the state entering each slot from those,
-//   h <- exp(A sum delta) h + h_slot,
-// and scans it for good.  Slots are ranges of the batch's tokens, whatever
-// its sequences are: a workgroup walks the sequences of its slot, and a
-// token range that ends inside a group leaves the state alone (delta = 0).
+// second goes over the slots in order and makes true states of those,
+//   h <- exp(A sum delta) h + h_slot;
+// the third scans every slot for good.  Slots are ranges of the batch's
+// tokens, whatever its sequences are: a workgroup walks the sequences of its
+// slot, and a token range that ends inside a group leaves the state alone
+// (delta = 0).
 #include "kda_layer_device.h"
 
 namespace kda {
 
 namespace {
-
-constexpr int kTileLd = kScanTile + 4;  // words per state of a staged tile
 
 // exp(delta A) = exp2(delta A2).  Finite, so that the tokens past a range's
 // end (delta = 0) keep the state whatever A is; NaN stays NaN.
@@ -49,30 +50,43 @@ __device__ __forceinline__ float log2_rate(float a) {
   return v < -3.4e38f ? -3.4e38f : v > 3.4e38f ? 3.4e38f : v;
 }
 
-// The channel of a row of 16 lanes.
+// A lane's channel: its group and number (a real one also where the lane has
+// none of its own), and the states it holds, first + i * step.
 struct Channel {
-  int g, c;      // group, channel (a real one also where the lanes are idle)
+  int g, c;
   bool active;
+  int first, step;
 };
-__device__ __forceinline__ Channel channel_of(const ScanArgs& a, int block, int in_block, int per_block) {
+__device__ __forceinline__ Channel channel_of(const ScanArgs& a, int block, int in_block, int per_block, int first,
+                                              int step) {
   const int per_group = a.D / a.G, g = block / a.blocks_per_group;
   const int at = (block - g * a.blocks_per_group) * per_block + in_block;
-  return Channel{g, g * per_group + (at < per_group ? at : per_group - 1), at < per_group};
+  return Channel{g, g * per_group + (at < per_group ? at : per_group - 1), at < per_group, first, step};
 }
 
 // Workgroup -> (slot, channel block), consecutive channel blocks of a slot on
 // one XCD (workgroups are dealt to the 8 XCDs in turn): their rows share
 // cache lines.  False past the end.
-__device__ __forceinline__ bool work_of(const ScanArgs& a, int64_t* slot, int* block) {
-  const int64_t n_blocks = (int64_t)a.G * a.blocks_per_group, total = a.n_slots * n_blocks;
-  const int64_t id = (int64_t)(blockIdx.x & 7) * ((total + 7) / 8) + (blockIdx.x >> 3);
-  *slot = id / n_blocks;
-  *block = (int)(id - *slot * n_blocks);
-  return id < total && (int64_t)(blockIdx.x >> 3) < (total + 7) / 8;
+__device__ __forceinline__ bool work_of(const ScanArgs& a, int* slot, int* block) {
+  const int n_blocks = a.G * a.blocks_per_group, total = (int)a.n_slots * n_blocks, per = (total + 7) / 8;
+  const int id = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
+  *slot = uniform(id / n_blocks);
+  *block = uniform(id - *slot * n_blocks);
+  return id < total;
 }
 inline dim3 work_grid(const ScanArgs& a) {
   const int64_t total = a.n_slots * a.G * a.blocks_per_group;
   return dim3((unsigned)((total + 7) / 8 * 8));
+}
+
+// A slot's tokens.
+struct Slot {
+  int lo, hi;
+  bool last;
+};
+__device__ __forceinline__ Slot slot_of(const ScanArgs& a, int slot) {
+  const int64_t lo = slot * a.slot, hi = lo + a.slot;
+  return Slot{(int)lo, (int)(hi < a.tokens ? hi : a.tokens), slot + 1 >= a.n_slots};
 }
 
 // Per-channel constants of a lane.
@@ -80,199 +94,395 @@ template <int NS>
 struct Rates {
   float A2[NS];  // log2 e times A, 0 for states past N
   float skip, bias;
-  __device__ __forceinline__ void load(const ScanArgs& a, int c, int j) {
+  __device__ __forceinline__ void load(const ScanArgs& a, const Channel& ch) {
 #pragma unroll
-    for (int i = 0; i < NS; ++i) A2[i] = j + 16 * i < a.N ? log2_rate(a.A[(int64_t)c * a.N + j + 16 * i]) : 0.f;
-    skip = a.skip ? a.skip[c] : 0.f;
-    bias = a.bias ? a.bias[c] : 0.f;
+    for (int i = 0; i < NS; ++i) {
+      const int n = ch.first + i * ch.step;
+      A2[i] = n < a.N ? log2_rate(a.A[(int64_t)ch.c * a.N + n]) : 0.f;
+    }
+    skip = a.skip ? a.skip[ch.c] : 0.f;
+    bias = a.bias ? a.bias[ch.c] : 0.f;
   }
 };
 
+// One row [D, N] of states (zeros where p is null and past N).
 template <int NS>
-__device__ __forceinline__ void load_state(const float* __restrict__ p, int64_t row, const ScanArgs& a, int c, int j,
-                                           float (&h)[NS]) {
+__device__ __forceinline__ void load_state(const float* __restrict__ p, int64_t row, const ScanArgs& a,
+                                           const Channel& ch, float (&h)[NS]) {
 #pragma unroll
-  for (int i = 0; i < NS; ++i)
-    h[i] = p && j + 16 * i < a.N ? p[(row * a.D + c) * a.N + j + 16 * i] : 0.f;
+  for (int i = 0; i < NS; ++i) {
+    const int n = ch.first + i * ch.step;
+    h[i] = p && n < a.N ? p[(row * a.D + ch.c) * a.N + n] : 0.f;
+  }
 }
 template <int NS>
 __device__ __forceinline__ void store_state(float* __restrict__ p, int64_t row, const ScanArgs& a, const Channel& ch,
-                                            int j, const float (&h)[NS]) {
+                                            const float (&h)[NS]) {
   if (!ch.active) return;
 #pragma unroll
-  for (int i = 0; i < NS; ++i)
-    if (j + 16 * i < a.N) p[(row * a.D + ch.c) * a.N + j + 16 * i] = h[i];
+  for (int i = 0; i < NS; ++i) {
+    const int n = ch.first + i * ch.step;
+    if (n < a.N) p[(row * a.D + ch.c) * a.N + n] = h[i];
+  }
 }
 
-// The state entering slot `slot` of a sequence that started at token lo.
+__device__ __forceinline__ float delta_of(const ScanArgs& a, float v) {
+  const float sp = softplus(v);
+  return a.softplus ? sp : v;
+}
+
+// ---- forward scans ("quads") ---------------------------------------------------
+
+// Loads are issued ahead of their use and stay as they come from memory
+// until then: what is converted, or merged after a branch, is waited for.
+
+// Tiles of B and C: TOK tokens from t0 of group g as [token][NP states],
+// zero past the range's end and past N.  A thread holds element
+// threadIdx.x + k THREADS of the tile.
+template <typename T, int NP, int TOK, int THREADS>
+struct TileRows {
+  static constexpr int PER = TOK * NP / THREADS;
+  T b[PER], c[PER];
+  __device__ __forceinline__ void load(const ScanArgs& a, int g, int t0, int end) {
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int el = threadIdx.x + k * THREADS, n = el % NP;
+      const int t = t0 + el / NP;
+      const int64_t tok = t < end ? t : end - 1;
+      const int at = g * a.N + (n < a.N ? n : a.N - 1);
+      b[k] = ((const T*)a.Bm)[tok * a.ld_b + at];
+      c[k] = ((const T*)a.Cm)[tok * a.ld_c + at];
+    }
+  }
+  __device__ __forceinline__ void store(const ScanArgs& a, float* s, int t0, int end) const {
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int el = threadIdx.x + k * THREADS;
+      const bool there = el % NP < a.N && t0 + el / NP < end;
+      s[el] = there ? Elem<T>::to_f32(b[k]) : 0.f;
+      s[TOK * NP + el] = there ? Elem<T>::to_f32(c[k]) : 0.f;
+    }
+  }
+};
+
+// What a scan does: the state only, the outputs, or the state and the
+// gradient sent to the state before the range (adj).
+enum Mode { kState, kOutput, kAdjoint };
+
+// Offsets in bytes of a lane's first token of a group, from the group's row.
+struct LaneOffsets {
+  uint32_t x, dt, z, o;
+};
+
+// A lane's four tokens of a group: q, q + 4, q + 8 and q + 12.
+template <typename T, Mode M>
+struct Four {
+  T x_[4], dt_[4], z_[4], g_[4];
+  // whole group: one scalar address and one lane offset per array
+  __device__ __forceinline__ void load(const ScanArgs& a, const T* __restrict__ dout, const LaneOffsets& l, int t) {
+    auto row = [&](const void* p, int64_t ld, int m, uint32_t off) {
+      return *(const T*)((const char*)((const T*)p + (t + 4 * (int64_t)m) * ld) + off);
+    };
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      x_[m] = row(a.x, a.ld_x, m, l.x);
+      dt_[m] = row(a.dt, a.ld_dt, m, l.dt);
+      if (M != kState) z_[m] = row(a.z, a.ld_z, m, l.z);
+      if (M == kAdjoint) g_[m] = row(dout, a.D, m, l.o);
+    }
+  }
+  // a group cut short at `end`: the last token for those past it
+  __device__ __forceinline__ void load(const ScanArgs& a, const T* __restrict__ dout, const Channel& ch, int t, int q,
+                                       int end) {
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const int64_t tok = t + 4 * m + q < end ? t + 4 * m + q : end - 1;
+      x_[m] = ((const T*)a.x)[tok * a.ld_x + ch.c];
+      dt_[m] = ((const T*)a.dt)[tok * a.ld_dt + ch.c];
+      if (M != kState) z_[m] = ((const T*)a.z)[tok * a.ld_z + ch.c];
+      if (M == kAdjoint) g_[m] = dout[tok * a.D + ch.c];
+    }
+  }
+};
+
+// v's row k of 16 lanes in every row, for k = 0 .. 3
+__device__ __forceinline__ void spread_rows(float v, float (&out)[4]) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, v);
+  const auto odd = __builtin_amdgcn_permlane16_swap(u, u, false, false);  // rows (0, 0, 2, 2), (1, 1, 3, 3)
+  const auto a = __builtin_amdgcn_permlane32_swap(odd[0], odd[0], false, false);
+  const auto b = __builtin_amdgcn_permlane32_swap(odd[1], odd[1], false, false);
+  out[0] = __builtin_bit_cast(float, (uint32_t)a[0]);
+  out[1] = __builtin_bit_cast(float, (uint32_t)b[0]);
+  out[2] = __builtin_bit_cast(float, (uint32_t)a[1]);
+  out[3] = __builtin_bit_cast(float, (uint32_t)b[1]);
+}
+
+// Sums over the four rows of 16 lanes: row k of the result is the sum of
+// p[k]'s rows.  Each swap pairs two values' halves, so that one addition
+// serves both.
+__device__ __forceinline__ float sum_rows(const float (&p)[4]) {
+  auto fold = [](float x, float y, auto swap) {
+    const auto s = swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y));
+    return __builtin_bit_cast(float, (uint32_t)s[0]) + __builtin_bit_cast(float, (uint32_t)s[1]);
+  };
+  auto halves = [](uint32_t x, uint32_t y) { return __builtin_amdgcn_permlane32_swap(x, y, false, false); };
+  auto rows = [](uint32_t x, uint32_t y) { return __builtin_amdgcn_permlane16_swap(x, y, false, false); };
+  return fold(fold(p[0], p[2], halves), fold(p[1], p[3], halves), rows);
+}
+
 template <int NS>
-__device__ __forceinline__ void incoming(const ScanArgs& a, const float* __restrict__ hend,
-                                         const float* __restrict__ sum, int64_t lo, int64_t slot, int c, int j,
-                                         const Rates<NS>& r, float (&h)[NS]) {
-  int64_t i = lo / a.slot;
-  load_state<NS>(hend, i, a, c, j, h);
-  for (++i; i < slot; ++i) {
-    float e[NS];
-    load_state<NS>(hend, i, a, c, j, e);
-    const float sd = sum[i * a.D + c];
+__device__ __forceinline__ void load_lds(const float* p, float (&v)[NS]) {
+  if constexpr (NS >= 4) {
 #pragma unroll
-    for (int n = 0; n < NS; ++n) h[n] = exp2_fast(sd * r.A2[n]) * h[n] + e[n];
+    for (int i = 0; i < NS; i += 4) {
+      const f32x4 x = *(const f32x4*)(p + i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[i + e] = x[e];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NS; ++i) v[i] = p[i];
   }
 }
 
-// Tiles of B and C: element (n, t) of tokens [t0, t0 + TOK) of group g,
-// zero past the range's end and past N.  A thread holds one state of every
-// (THREADS / 16)-th token.
-template <typename T, int NS, int TOK, int THREADS>
-struct TileLoad {
-  static constexpr int PER = TOK * 16 / THREADS;  // tokens a thread
-  float b[NS][PER], c[NS][PER];
-  __device__ __forceinline__ void load(const ScanArgs& a, int g, int64_t t0, int64_t end) {
-    const int n = threadIdx.x & 15, t = threadIdx.x >> 4;
-#pragma unroll
-    for (int i = 0; i < NS; ++i)
-#pragma unroll
-      for (int k = 0; k < PER; ++k) {
-        const int64_t tok = t0 + t + k * (THREADS / 16);
-        const bool there = n + 16 * i < a.N && tok < end;
-        const int at = g * a.N + n + 16 * i;
-        b[i][k] = there ? load_f32((const T*)a.Bm + tok * a.ld_b + at) : 0.f;
-        c[i][k] = there ? load_f32((const T*)a.Cm + tok * a.ld_c + at) : 0.f;
-      }
-  }
-  // s: [2][NS * 16][LD], B first
-  template <int LD>
-  __device__ __forceinline__ void store(float* s, int at = 0) const {
-    const int n = threadIdx.x & 15, t = threadIdx.x >> 4;
-#pragma unroll
-    for (int i = 0; i < NS; ++i)
-#pragma unroll
-      for (int k = 0; k < PER; ++k) {
-        s[(n + 16 * i) * LD + at + t + k * (THREADS / 16)] = b[i][k];
-        s[(NS * 16 + n + 16 * i) * LD + at + t + k * (THREADS / 16)] = c[i][k];
-      }
-  }
+// State of one scan: the state itself, and for kAdjoint the gradient sent
+// back and the product of the decays so far.
+template <int NS>
+struct Scanned {
+  float h[NS], adj[NS], run[NS];
 };
 
-// Lane j's token of a group: its inputs, and what the recurrence takes of it.
-template <typename T>
-struct Token {
-  float x, dt, z;
-  __device__ __forceinline__ void load(const ScanArgs& a, const Channel& ch, int64_t t, int64_t end) {
-    x = dt = z = 0.f;
-    if (t >= end || !ch.active) return;
-    x = load_f32((const T*)a.x + t * a.ld_x + ch.c);
-    dt = load_f32((const T*)a.dt + t * a.ld_dt + ch.c);
-    if (a.z) z = load_f32((const T*)a.z + t * a.ld_z + ch.c);
+// One group of 16 tokens from token t.  WHOLE: all of them are before `end`.
+// s: this lane's quarter of the group's first token of B; C is `c_off` floats
+// further.  Returns this lane's sum of delta.
+template <typename T, int NS, Mode M, bool WHOLE>
+__device__ __forceinline__ float scan_group(const ScanArgs& a, const Channel& ch, const Rates<NS>& r, int q,
+                                            const Four<T, M>& in, const LaneOffsets& l, int t, int end,
+                                            const float* s, int c_off, Scanned<NS>& st, T* __restrict__ o) {
+  constexpr int NP = 4 * NS;
+  float y[4], sum = 0.f;
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    const bool there = WHOLE || t + 4 * m + q < end;
+    float d = delta_of(a, Elem<T>::to_f32(in.dt_[m]) + r.bias), v = d * Elem<T>::to_f32(in.x_[m]);
+    if (!WHOLE) {
+      d = there ? d : 0.f;
+      v = there ? v : 0.f;
+    }
+    sum += d;
+    float delta[4], dx[4], dy[4], part[4];
+    spread_rows(d, delta);
+    spread_rows(v, dx);
+    if (M == kAdjoint) {
+      const float z = Elem<T>::to_f32(in.z_[m]), gate = z * sigmoid(z);
+      float g = Elem<T>::to_f32(in.g_[m]);
+      g *= a.has_z ? gate : 1.f;
+      spread_rows(there ? g : 0.f, dy);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float B[NS], C[NS];
+      load_lds<NS>(s + (4 * m + k) * NP, B);
+      if (M != kState) load_lds<NS>(s + c_off + (4 * m + k) * NP, C);
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        const float e = exp2_fast(delta[k] * r.A2[i]);
+        st.h[i] = e * st.h[i] + dx[k] * B[i];
+        if (M == kOutput) part[k] = i ? part[k] + C[i] * st.h[i] : C[i] * st.h[i];
+        if (M == kAdjoint) {
+          st.run[i] *= e;
+          st.adj[i] += st.run[i] * (C[i] * dy[k]);
+        }
+      }
+    }
+    if (M == kOutput) y[m] = sum_rows(part);
   }
-};
+  if (M == kOutput && ch.active) {
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const float x = Elem<T>::to_f32(in.x_[m]), z = Elem<T>::to_f32(in.z_[m]), gate = z * sigmoid(z);
+      const float v = (y[m] + r.skip * x) * (a.has_z ? gate : 1.f);
+      T* at = (T*)((char*)(o + (t + 4 * (int64_t)m) * a.D) + l.o);
+      if (WHOLE || t + 4 * m + q < end) *at = Elem<T>::from_f32(v);
+    }
+  }
+  return sum;
+}
 
-// Scans tokens [t0, end) of one sequence from h.  OUT: writes o; else only
-// the state, and returns the sum of delta (this lane's tokens of it).
-template <typename T, int NS, bool OUT>
-__device__ __forceinline__ float scan_range(const ScanArgs& a, const Channel& ch, const Rates<NS>& r, int j,
-                                            int64_t t0, int64_t end, float* s, float (&h)[NS], T* __restrict__ o) {
-  constexpr int THREADS = 64 * kScanWaves, BUF = 2 * NS * 16 * kTileLd;
-  TileLoad<T, NS, kScanTile, THREADS> tile;
-  Token<T> next;
+// Scans tokens [t0, end) of one sequence.  Returns the lane's sum of delta.
+template <typename T, int NS, Mode M>
+__device__ __forceinline__ float scan_range(const ScanArgs& a, const Channel& ch, const Rates<NS>& r, int q,
+                                            const LaneOffsets& l, int t0, int end, float* s, Scanned<NS>& st,
+                                            T* __restrict__ o, const T* __restrict__ dout) {
+  constexpr int THREADS = 64 * kScanWaves, NP = 4 * NS, C_OFF = kScanTile * NP, BUF = 2 * C_OFF;
+  TileRows<T, NP, kScanTile, THREADS> tile;
+  Four<T, M> next;
   float sum = 0.f;
+  if (t0 + 16 <= end) next.load(a, dout, l, t0);
   tile.load(a, ch.g, t0, end);
-  next.load(a, ch, t0 + j, end);
   __syncthreads();  // the range before may still be reading
-  tile.template store<kTileLd>(s);
+  tile.store(a, s, t0, end);
   __syncthreads();
   int buf = 0;
-  for (int64_t t = t0; t < end; t += kScanTile) {
-    const bool more = t + kScanTile < end;
+  for (int t = t0; t < end; t += kScanTile) {
+    const bool more = end - t > kScanTile;
     if (more) tile.load(a, ch.g, t + kScanTile, end);
-    const float* sb = s + buf * BUF + j * kTileLd;
-    const float* sc = sb + NS * 16 * kTileLd;
-    for (int q = 0; q < kScanTile && t + q < end; q += 16) {
-      const Token<T> cur = next;
-      const int64_t tok = t + q + j;
-      next.load(a, ch, tok + 16, end);
-      const float v = cur.dt + r.bias;
-      const bool there = tok < end && ch.active;
-      const float delta = there ? (a.softplus ? softplus(v) : v) : 0.f;
-      const float dx = there ? delta * cur.x : 0.f;
-      if (!OUT) sum += delta;
-      float p[16];
-      static_for<4>([&](auto k4) {
-        f32x4 B[NS], C[NS];
-#pragma unroll
-        for (int i = 0; i < NS; ++i) {
-          B[i] = *(const f32x4*)(sb + i * 16 * kTileLd + q + 4 * k4);
-          if (OUT) C[i] = *(const f32x4*)(sc + i * 16 * kTileLd + q + 4 * k4);
-        }
-        static_for<4>([&](auto e) {
-          constexpr int k = 4 * decltype(k4)::value + decltype(e)::value;
-          const float dk = row_bcast<k>(delta), xk = row_bcast<k>(dx);
-          float y = 0.f;
-#pragma unroll
-          for (int i = 0; i < NS; ++i) {
-            h[i] = exp2_fast(dk * r.A2[i]) * h[i] + xk * B[i][decltype(e)::value];
-            if (OUT) y += C[i][decltype(e)::value] * h[i];
-          }
-          p[k] = y;
-        });
-      });
-      if (OUT) {
-        float y = row_sums(p, j) + r.skip * cur.x;
-        if (a.z) y *= cur.z * sigmoid(cur.z);
-        if (there) o[tok * a.D + ch.c] = Elem<T>::from_f32(y);
-      }
+    const float* sq = s + buf * BUF + q * NS;
+    int u = t;
+    for (; u + 16 <= end && u < t + kScanTile; u += 16) {
+      const Four<T, M> cur = next;
+      if (u + 32 <= end) next.load(a, dout, l, u + 16);
+      sum += scan_group<T, NS, M, true>(a, ch, r, q, cur, l, u, end, sq + (u - t) * NP, C_OFF, st, o);
+    }
+    if (u < end && u < t + kScanTile) {
+      Four<T, M> cur;
+      cur.load(a, dout, ch, u, q, end);
+      sum += scan_group<T, NS, M, false>(a, ch, r, q, cur, l, u, end, sq + (u - t) * NP, C_OFF, st, o);
     }
     if (more) {
       buf ^= 1;
-      tile.template store<kTileLd>(s + buf * BUF);
+      tile.store(a, s + buf * BUF, t + kScanTile, end);
       __syncthreads();
     }
   }
   return sum;
 }
 
-// Forward.  OUT = false: the first launch, over what a slot leaves unfinished.
-template <typename T, int NS, bool OUT>
-__global__ void __launch_bounds__(64 * kScanWaves)
-scan_forward(const ScanArgs a, float* __restrict__ hend, float* __restrict__ sum, T* __restrict__ o,
-             float* __restrict__ ht) {
-  __shared__ __align__(16) float s[2 * 2 * NS * 16 * kTileLd];
-  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), j = lane & 15;
-  int64_t slot;
-  int block;
-  if (!work_of(a, &slot, &block)) return;
-  const Channel ch = channel_of(a, block, wave * 4 + (lane >> 4), 4 * kScanWaves);
+// A workgroup's place in the forward scans.
+template <int NS>
+struct QuadWork {
+  int slot, q;
+  Slot tok;
+  Channel ch;
   Rates<NS> r;
-  r.load(a, ch.c, j);
+  LaneOffsets l;
+  __device__ __forceinline__ bool init(const ScanArgs& a, size_t esz) {
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    int block;
+    if (!work_of(a, &slot, &block)) return false;
+    q = lane >> 4;
+    ch = channel_of(a, block, wave * 16 + (lane & 15), 16 * kScanWaves, q * NS, 1);
+    r.load(a, ch);
+    tok = slot_of(a, slot);
+    const uint32_t e = (uint32_t)esz;
+    l = LaneOffsets{e * (uint32_t)(q * a.ld_x + ch.c), e * (uint32_t)(q * a.ld_dt + ch.c),
+                    e * (uint32_t)(q * a.ld_z + ch.c), e * (uint32_t)(q * (int64_t)a.D + ch.c)};
+    return true;
+  }
+};
+
+// What the first launch found of a slot (one word per slot): whether a
+// sequence goes on past its end, and whether that one entered it from an
+// earlier slot; and, for the backward pass, whether one entered it.
+enum SlotKind { kNothing = 0, kStarted = 1, kPassed = 2, kEntered = 4 };
+
+// Forward.  M = kState: the first launch, over what a slot leaves unfinished;
+// kOutput: the last one, hend then holding the states at the slots' ends.
+template <typename T, int NS, Mode M>
+__global__ void __launch_bounds__(64 * kScanWaves, 2)
+scan_forward(const ScanArgs a, float* __restrict__ hend, float* __restrict__ sum, int* __restrict__ kind,
+             T* __restrict__ o, float* __restrict__ ht) {
+  __shared__ __align__(16) float s[2 * 2 * kScanTile * 4 * NS];
+  QuadWork<NS> w;
+  if (!w.init(a, sizeof(T))) return;
   const Seqs seqs{a.cu, a.n_seqs, a.T, a.tokens};
-  const int64_t lo = slot * a.slot, hi = lo + a.slot < a.tokens ? lo + a.slot : a.tokens;
-  float h[NS];
-  if (!OUT) {
-    const int n = seqs.from(hi) - 1;  // the last sequence that starts in the slot or before
-    if (slot + 1 >= a.n_slots || n < 0 || seqs.end(n) <= hi) return;
-    const int64_t start = seqs.start(n);
+  const int lo = w.tok.lo, hi = w.tok.hi;
+  Scanned<NS> st;
+  if (M == kState) {
+    const int n = uniform(seqs.from(hi)) - 1;  // the last sequence that starts in the slot or before
+    const bool on = !w.tok.last && n >= 0 && uniform((int)seqs.end(n)) > hi;
+    const int start = on ? uniform((int)seqs.start(n)) : 0;
     const bool own = start >= lo;
-    load_state<NS>(own ? a.h0 : nullptr, n, a, ch.c, j, h);
-    const float d = scan_range<T, NS, false>(a, ch, r, j, own ? start : lo, hi, s, h, (T*)nullptr);
-    store_state<NS>(hend, slot, a, ch, j, h);
-    const float total = row_sum(d);
-    if (!own && ch.active && j == 0) sum[slot * a.D + ch.c] = total;
+    if (threadIdx.x == 0) kind[w.slot] = !on ? kNothing : own ? kStarted : kPassed;
+    if (!on) return;
+    load_state<NS>(own ? a.h0 : nullptr, n, a, w.ch, st.h);
+    const float d = scan_range<T, NS, M>(a, w.ch, w.r, w.q, w.l, own ? start : lo, hi, s, st, (T*)nullptr,
+                                         (const T*)nullptr);
+    store_state<NS>(hend, w.slot, a, w.ch, st.h);
+    const float total = sum_rows({d, d, d, d});
+    if (!own && w.ch.active && w.q == 0) sum[(int64_t)w.slot * a.D + w.ch.c] = total;
     return;
   }
-  int n = seqs.from(lo);
-  if (n > 0 && seqs.end(n - 1) > lo) {  // a sequence that entered from an earlier slot
-    const int64_t end = seqs.end(n - 1);
-    incoming<NS>(a, hend, sum, seqs.start(n - 1), slot, ch.c, j, r, h);
-    scan_range<T, NS, true>(a, ch, r, j, lo, end < hi ? end : hi, s, h, o);
-    if (ht && end <= hi) store_state<NS>(ht, n - 1, a, ch, j, h);
+  int n = uniform(seqs.from(lo));
+  if (n > 0) {
+    const int end = uniform((int)seqs.end(n - 1));
+    if (end > lo) {  // a sequence that entered from an earlier slot
+      load_state<NS>(hend, w.slot - 1, a, w.ch, st.h);
+      scan_range<T, NS, M>(a, w.ch, w.r, w.q, w.l, lo, end < hi ? end : hi, s, st, o, (const T*)nullptr);
+      if (ht && end <= hi) store_state<NS>(ht, n - 1, a, w.ch, st.h);
+    }
   }
   // those that start here; the last slot also has the empty ones behind the last token
-  for (; n < a.n_seqs && (slot + 1 >= a.n_slots || seqs.start(n) < hi); ++n) {
-    const int64_t start = seqs.start(n), end = seqs.end(n);
-    load_state<NS>(a.h0, n, a, ch.c, j, h);
-    if (start < end) scan_range<T, NS, true>(a, ch, r, j, start, end < hi ? end : hi, s, h, o);
-    if (ht && end <= hi) store_state<NS>(ht, n, a, ch, j, h);
+  for (; n < a.n_seqs; ++n) {
+    const int start = uniform((int)seqs.start(n)), end = uniform((int)seqs.end(n));
+    if (!w.tok.last && start >= hi) break;
+    load_state<NS>(a.h0, n, a, w.ch, st.h);
+    if (start < end)
+      scan_range<T, NS, M>(a, w.ch, w.r, w.q, w.l, start, end < hi ? end : hi, s, st, o, (const T*)nullptr);
+    if (ht && end <= hi) store_state<NS>(ht, n, a, w.ch, st.h);
   }
+}
+
+// The second launch: true states at the slots' ends out of what each slot
+// made of a zero state, in place, and (blockIdx.y = 1) likewise the gradients
+// of the states at the slots' starts, from the last slot to the first:
+//   h_i <- h_i + exp(A sum_i) h_{i-1},   g_i <- g_i + exp(A sum_i) g_{i+1}
+// for the slots that a sequence passes through.  A lane takes one state of
+// one channel; the 8 waves of a workgroup take an eighth of the slots each,
+// first composing it to (product of the decays, state), then again from the
+// state that the waves before hand on, so that the chain is an eighth as
+// long.  Loads go ahead of it in batches.
+constexpr int kChainWaves = 8, kChainBatch = 16;
+__global__ void __launch_bounds__(64 * kChainWaves)
+scan_chain(const float* __restrict__ A, int64_t dn, int N, int D, int n_slots, float* __restrict__ hend,
+           float* __restrict__ adj, const float* __restrict__ sum, const int* __restrict__ kind) {
+  __shared__ float decay[kChainWaves][64], state[kChainWaves][64];
+  __shared__ int through[kChainWaves];  // one sequence passes all of a wave's slots
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const bool back = blockIdx.y != 0;
+  float* __restrict__ v = back ? adj : hend;
+  int64_t el = (int64_t)blockIdx.x * 64 + lane;
+  const bool there = el < dn;
+  el = there ? el : dn - 1;
+  const int64_t c = el / N;
+  const float A2 = log2_rate(A[el]);
+  const int per = (n_slots + kChainWaves - 1) / kChainWaves;
+  // positions along the chain: slot i, or n_slots - 1 - i going back
+  const int first = wave * per, last = first + per < n_slots ? first + per : n_slots;
+  int unbroken = 1;
+  auto walk = [&](float& d, float& h, bool write) {
+    for (int i0 = first; i0 < last; i0 += kChainBatch) {
+      float s[kChainBatch], x[kChainBatch];
+      int kd[kChainBatch];
+#pragma unroll
+      for (int k = 0; k < kChainBatch; ++k) {
+        const int i = i0 + k < last ? i0 + k : last - 1, slot = back ? n_slots - 1 - i : i;
+        s[k] = sum[(int64_t)slot * D + c];
+        x[k] = v[(int64_t)slot * dn + el];
+        kd[k] = kind[slot];
+      }
+#pragma unroll
+      for (int k = 0; k < kChainBatch; ++k) {
+        if (i0 + k >= last) break;
+        // what the slot holds counts only where a sequence leaves it (back: enters it)
+        const bool passed = kd[k] & kPassed, holds = back ? kd[k] & kEntered : kd[k] & (kStarted | kPassed);
+        const float e = passed ? exp2_fast(s[k] * A2) : 0.f;
+        h = (passed ? e * h : 0.f) + (holds ? x[k] : 0.f);
+        d = passed ? e * d : 0.f;
+        unbroken = passed ? unbroken : 0;
+        if (write && there) v[(int64_t)(back ? n_slots - 1 - i0 - k : i0 + k) * dn + el] = h;
+      }
+    }
+  };
+  float d = 1.f, h = 0.f;
+  walk(d, h, false);
+  decay[wave][lane] = d;
+  state[wave][lane] = h;
+  through[wave] = unbroken;
+  __syncthreads();
+  h = 0.f;
+  for (int w = 0; w < wave; ++w) h = (through[w] ? decay[w][lane] * h : 0.f) + state[w][lane];
+  walk(d, h, true);
 }
 
 // ---- one token ---------------------------------------------------------------
@@ -312,7 +522,7 @@ __global__ void __launch_bounds__(256) scan_step(const ScanArgs a, float* __rest
   }
   const float x = load_f32((const T*)a.x + seq * a.ld_x + c);
   const float v = load_f32((const T*)a.dt + seq * a.ld_dt + c) + (a.bias ? a.bias[c] : 0.f);
-  const float z = a.z ? load_f32((const T*)a.z + seq * a.ld_z + c) : 0.f;
+  const float z = a.has_z ? load_f32((const T*)a.z + seq * a.ld_z + c) : 0.f;
   const float delta = a.softplus ? softplus(v) : v;
   float y = 0.f;
 #pragma unroll
@@ -333,144 +543,137 @@ __global__ void __launch_bounds__(256) scan_step(const ScanArgs a, float* __rest
   if constexpr (LPC >= 16) y += dpp<kRowMirror>(y);
   if (sub == 0) {
     y += (a.skip ? a.skip[c] : 0.f) * x;
-    if (a.z) y *= z * sigmoid(z);
+    if (a.has_z) y *= z * sigmoid(z);
     o[id] = Elem<T>::from_f32(y);
   }
 }
 
 // ---- backward ------------------------------------------------------------------
-// Three launches.  The first, only when sequences pass from slot to slot,
-// walks every slot once and leaves what its neighbours need: the state it
-// hands on (as forward), the gradient it hands back (the part of the state
-// gradient at its start that its own tokens make, summed forward in time
-// with the running product of the decays), and its sum of delta.  The second
-// takes a slot with the state entering it and the gradient of the state
-// leaving it composed from those: it runs forward leaving the state before
-// every group of 16 tokens in LDS, then walks the groups back, redoing each
-// group's recurrence in registers.  The third adds the partial sums.
-//
-// Sums over channels (dB, dC) of one token are products of the 4 rows of a
-// wave: v_mfma_f32_16x16x4f32 with the token's dy (delta x) in row k of the
-// left operand, zeros in the others, and h (dh) as it lies in the registers,
-// so a group's 16 products accumulate into one [16 tokens][16 states] tile.
-// The matrix pipe does them beside the vector unit.  The tiles of the waves
-// are added in LDS, those of the workgroups by the third launch.
-template <typename T>
-struct TokenGrad : Token<T> {
-  float dout;
-  __device__ __forceinline__ void load(const ScanArgs& a, const T* __restrict__ g, const Channel& ch, int64_t t,
-                                       int64_t end) {
-    Token<T>::load(a, ch, t, end);
-    dout = t < end && ch.active ? load_f32(g + t * a.D + ch.c) : 0.f;
+// Two launches, only when sequences pass from slot to slot, make the states
+// and gradients between the slots: every slot is walked once for the state
+// it hands on (as forward) and the gradient it hands back (the part of the
+// state gradient at its start that its own tokens make, summed forward in
+// time with the running product of the decays), and scan_chain composes
+// those.  The next takes every slot from both: it runs forward leaving the
+// state before every group of 16 tokens in LDS, then walks the groups back,
+// redoing each group's recurrence in registers.  The last two add the
+// partial sums.
+template <typename T, int NS>
+__global__ void __launch_bounds__(64 * kScanWaves, 2)
+scan_backward_carry(const ScanArgs a, const T* __restrict__ dout, const float* __restrict__ dht,
+                    float* __restrict__ hend, float* __restrict__ adj, float* __restrict__ sum,
+                    int* __restrict__ kind) {
+  __shared__ __align__(16) float s[2 * 2 * kScanTile * 4 * NS];
+  QuadWork<NS> w;
+  if (!w.init(a, sizeof(T))) return;
+  const Seqs seqs{a.cu, a.n_seqs, a.T, a.tokens};
+  const int lo = w.tok.lo, hi = w.tok.hi;
+  Scanned<NS> st;
+  int n = uniform(seqs.from(lo));
+  const int before = n > 0 ? uniform((int)seqs.end(n - 1)) : lo;
+  int found = kNothing;
+  if (before > lo) {  // entered from an earlier slot
+    found = kEntered | (before > hi ? kPassed : 0);
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      st.h[i] = st.adj[i] = 0.f;
+      st.run[i] = 1.f;
+    }
+    const float d = scan_range<T, NS, kAdjoint>(a, w.ch, w.r, w.q, w.l, lo, before < hi ? before : hi, s, st,
+                                                (T*)nullptr, dout);
+    if (before <= hi) {
+      float last[NS];
+      load_state<NS>(dht, n - 1, a, w.ch, last);
+#pragma unroll
+      for (int i = 0; i < NS; ++i) st.adj[i] += st.run[i] * last[i];
+    } else {
+      store_state<NS>(hend, w.slot, a, w.ch, st.h);
+      const float total = sum_rows({d, d, d, d});
+      if (w.ch.active && w.q == 0) sum[(int64_t)w.slot * a.D + w.ch.c] = total;
+    }
+    store_state<NS>(adj, w.slot, a, w.ch, st.adj);
+  }
+  n = uniform(seqs.from(hi)) - 1;
+  const int start = n >= 0 ? uniform((int)seqs.start(n)) : -1;
+  if (start >= lo && uniform((int)seqs.end(n)) > hi) {  // starts here and goes on
+    found |= kStarted;
+    load_state<NS>(a.h0, n, a, w.ch, st.h);
+    scan_range<T, NS, kState>(a, w.ch, w.r, w.q, w.l, start, hi, s, st, (T*)nullptr, dout);
+    store_state<NS>(hend, w.slot, a, w.ch, st.h);
+  }
+  if (threadIdx.x == 0) kind[w.slot] = found;
+}
+
+// Layout of the backward scan ("rows").  A row of 16 lanes holds one channel,
+// lane j the states j, j + 16, ... and, of a group of 16 tokens, the inputs
+// of token j; a wave has 4 channels.  In the recurrence token k's values are
+// lane k's, broadcast over the row as an operand modifier, and the sums over
+// the states of a group's 16 tokens are taken together (row_sums).  Sums over
+// channels, of which the backward pass has two per element, are products of
+// the wave's 4 rows: v_mfma_f32_16x16x4f32 with the token's dy (delta x) in
+// row k of the left operand, zeros in the others, and h (dh) as it lies in
+// the registers, so a group's 16 products accumulate into one [16 tokens][16
+// states] tile.  The tiles of the waves are added in LDS, those of the
+// workgroups by a later launch.  B and C of the slot are staged as
+// [state][token] with rows of slot + 4 words: four tokens are one 16-byte
+// read, free of bank conflicts.
+
+// Tiles of B and C as [state][token]; a thread holds one state of every
+// (THREADS / 16)-th token.
+template <typename T, int NS, int TOK, int THREADS>
+struct TileCols {
+  static constexpr int PER = TOK * 16 / THREADS;  // tokens a thread
+  T b[NS][PER], c[NS][PER];
+  __device__ __forceinline__ void load(const ScanArgs& a, int g, int t0, int end) {
+    const int n = threadIdx.x & 15, t = threadIdx.x >> 4;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int tk = t0 + t + k * (THREADS / 16);
+      const int64_t tok = tk < end ? tk : end - 1;
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        const int at = g * a.N + (n + 16 * i < a.N ? n + 16 * i : a.N - 1);
+        b[i][k] = ((const T*)a.Bm)[tok * a.ld_b + at];
+        c[i][k] = ((const T*)a.Cm)[tok * a.ld_c + at];
+      }
+    }
+  }
+  // s: [2][NS * 16][LD], B first, the tile's tokens from column `at`
+  template <int LD>
+  __device__ __forceinline__ void store(const ScanArgs& a, float* s, int at, int t0, int end) const {
+    const int n = threadIdx.x & 15, t = threadIdx.x >> 4;
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+#pragma unroll
+      for (int k = 0; k < PER; ++k) {
+        const int tok = t + k * (THREADS / 16);
+        const bool there = n + 16 * i < a.N && t0 + tok < end;
+        s[(n + 16 * i) * LD + at + tok] = there ? Elem<T>::to_f32(b[i][k]) : 0.f;
+        s[(NS * 16 + n + 16 * i) * LD + at + tok] = there ? Elem<T>::to_f32(c[i][k]) : 0.f;
+      }
   }
 };
 
-// Tokens [t0, end) from state h: the state after them, and in adj the sum of
-// the gradients they send to the state before them, times `run` (the product
-// of their decays when it starts at 1).  Returns this lane's part of the sum
-// of delta.
-template <typename T, int NS>
-__device__ __forceinline__ float carry_range(const ScanArgs& a, const T* __restrict__ dout, const Channel& ch,
-                                             const Rates<NS>& r, int j, int64_t t0, int64_t end, float* s,
-                                             float (&h)[NS], float (&adj)[NS], float (&run)[NS]) {
-  constexpr int THREADS = 64 * kScanWaves;
-  TileLoad<T, NS, kScanTile, THREADS> tile;
-  TokenGrad<T> next;
-  float sum = 0.f;
-  next.load(a, dout, ch, t0 + j, end);
-  for (int64_t t = t0; t < end; t += kScanTile) {
-    tile.load(a, ch.g, t, end);
-    __syncthreads();
-    tile.template store<kTileLd>(s);
-    __syncthreads();
-    const float* sb = s + j * kTileLd;
-    const float* sc = sb + NS * 16 * kTileLd;
-    for (int q = 0; q < kScanTile && t + q < end; q += 16) {
-      const TokenGrad<T> cur = next;
-      const int64_t tok = t + q + j;
-      next.load(a, dout, ch, tok + 16, end);
-      const float v = cur.dt + r.bias;
-      const bool there = tok < end && ch.active;
-      const float delta = there ? (a.softplus ? softplus(v) : v) : 0.f;
-      const float dx = there ? delta * cur.x : 0.f;
-      const float dy = there ? (a.z ? cur.dout * (cur.z * sigmoid(cur.z)) : cur.dout) : 0.f;
-      sum += delta;
-      static_for<4>([&](auto k4) {
-        f32x4 B[NS], C[NS];
-#pragma unroll
-        for (int i = 0; i < NS; ++i) {
-          B[i] = *(const f32x4*)(sb + i * 16 * kTileLd + q + 4 * k4);
-          C[i] = *(const f32x4*)(sc + i * 16 * kTileLd + q + 4 * k4);
-        }
-        static_for<4>([&](auto e) {
-          constexpr int k = 4 * decltype(k4)::value + decltype(e)::value;
-          const float dk = row_bcast<k>(delta), xk = row_bcast<k>(dx), gk = row_bcast<k>(dy);
-#pragma unroll
-          for (int i = 0; i < NS; ++i) {
-            const float d = exp2_fast(dk * r.A2[i]);
-            h[i] = d * h[i] + xk * B[i][decltype(e)::value];
-            run[i] *= d;
-            adj[i] += run[i] * (C[i][decltype(e)::value] * gk);
-          }
-        });
-      });
-    }
+// Lane j's token of a group (the range's last one past its end).
+template <typename T>
+struct Token {
+  T x_, dt_, z_, dout_;
+  __device__ __forceinline__ void load(const ScanArgs& a, const T* __restrict__ g, const Channel& ch, int t, int end) {
+    const int64_t tok = t < end ? t : end - 1;
+    x_ = ((const T*)a.x)[tok * a.ld_x + ch.c];
+    dt_ = ((const T*)a.dt)[tok * a.ld_dt + ch.c];
+    z_ = ((const T*)a.z)[tok * a.ld_z + ch.c];
+    dout_ = g[tok * a.D + ch.c];
   }
-  return sum;
-}
+  __device__ __forceinline__ float x() const { return Elem<T>::to_f32(x_); }
+  __device__ __forceinline__ float dt() const { return Elem<T>::to_f32(dt_); }
+  __device__ __forceinline__ float z() const { return Elem<T>::to_f32(z_); }
+  __device__ __forceinline__ float dout() const { return Elem<T>::to_f32(dout_); }
+};
 
-template <typename T, int NS>
-__global__ void __launch_bounds__(64 * kScanWaves)
-scan_backward_carry(const ScanArgs a, const T* __restrict__ dout, const float* __restrict__ dht,
-                    float* __restrict__ hend, float* __restrict__ adj, float* __restrict__ sum) {
-  __shared__ __align__(16) float s[2 * NS * 16 * kTileLd];
-  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), j = lane & 15;
-  int64_t slot;
-  int block;
-  if (!work_of(a, &slot, &block)) return;
-  const Channel ch = channel_of(a, block, wave * 4 + (lane >> 4), 4 * kScanWaves);
-  Rates<NS> r;
-  r.load(a, ch.c, j);
-  const Seqs seqs{a.cu, a.n_seqs, a.T, a.tokens};
-  const int64_t lo = slot * a.slot, hi = lo + a.slot < a.tokens ? lo + a.slot : a.tokens;
-  float h[NS], g[NS], run[NS];
-  int n = seqs.from(lo);
-  if (n > 0 && seqs.end(n - 1) > lo) {  // entered from an earlier slot
-    const int64_t end = seqs.end(n - 1);
-#pragma unroll
-    for (int i = 0; i < NS; ++i) {
-      h[i] = g[i] = 0.f;
-      run[i] = 1.f;
-    }
-    const float d = carry_range<T, NS>(a, dout, ch, r, j, lo, end < hi ? end : hi, s, h, g, run);
-    if (end <= hi) {
-      float last[NS];
-      load_state<NS>(dht, n - 1, a, ch.c, j, last);
-#pragma unroll
-      for (int i = 0; i < NS; ++i) g[i] += run[i] * last[i];
-    } else {
-      store_state<NS>(hend, slot, a, ch, j, h);
-      const float total = row_sum(d);
-      if (ch.active && j == 0) sum[slot * a.D + ch.c] = total;
-    }
-    store_state<NS>(adj, slot, a, ch, j, g);
-  }
-  n = seqs.from(hi) - 1;
-  if (n >= 0 && seqs.start(n) >= lo && seqs.end(n) > hi) {  // starts here and goes on
-    load_state<NS>(a.h0, n, a, ch.c, j, h);
-#pragma unroll
-    for (int i = 0; i < NS; ++i) {
-      g[i] = 0.f;
-      run[i] = 1.f;
-    }
-    carry_range<T, NS>(a, dout, ch, r, j, seqs.start(n), hi, s, h, g, run);
-    store_state<NS>(hend, slot, a, ch, j, h);
-  }
-}
-
-// What the second launch reads and writes beside the inputs.
+// What the backward scan reads and writes beside the inputs.
 struct ScanBwdBuffers {
-  const float *hend, *adj, *sum;  // of every slot; null without carry
+  const float *hend, *adj;    // at every slot's end and start; null without carry
   float *da, *dskip, *dbias;      // per slot
   float *db, *dc;                 // per workgroup of channels
 };
@@ -490,15 +693,15 @@ scan_backward(const ScanArgs a, const ScanGrads g, const ScanBwdBuffers w) {
   constexpr int WV = Lds::WV, LD = Lds::LD, THREADS = 64 * WV;
   __shared__ Lds s;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), j = lane & 15;
-  int64_t slot;
-  int block;
+  int slot, block;
   if (!work_of(a, &slot, &block)) return;
-  const Channel ch = channel_of(a, block, wave * 4 + (lane >> 4), 4 * WV);
+  const Channel ch = channel_of(a, block, wave * 4 + (lane >> 4), 4 * WV, j, 16);
   const int in_group = block - ch.g * a.blocks_per_group;
   Rates<NS> r;
-  r.load(a, ch.c, j);
+  r.load(a, ch);
   const Seqs seqs{a.cu, a.n_seqs, a.T, a.tokens};
-  const int64_t lo = slot * a.slot, hi = lo + a.slot < a.tokens ? lo + a.slot : a.tokens;
+  const Slot own = slot_of(a, slot);
+  const int lo = own.lo, hi = own.hi;
   const T* __restrict__ dout = (const T*)g.dout;
   float dA[NS], dskip = 0.f, dbias = 0.f;
 #pragma unroll
@@ -507,13 +710,13 @@ scan_backward(const ScanArgs a, const ScanGrads g, const ScanBwdBuffers w) {
 
   // tokens [t0, end) of one sequence: h the state before them, gr the
   // gradient of the state after them; leaves the gradient of h in gr
-  auto range = [&](int64_t t0, int64_t end, float(&h)[NS], float(&gr)[NS]) {
-    const int groups = (int)((end - t0 + 15) / 16);
+  auto range = [&](int t0, int end, float(&h)[NS], float(&gr)[NS]) {
+    const int groups = (end - t0 + 15) / 16;
     __syncthreads();  // the range before may still be reading
     for (int t = 0; t < groups * 16; t += kScanTile) {
-      TileLoad<T, NS, kScanTile, THREADS> tile;
+      TileCols<T, NS, kScanTile, THREADS> tile;
       tile.load(a, ch.g, t0 + t, end);
-      tile.template store<LD>(s.bc, t);
+      tile.template store<LD>(a, s.bc, t, t0 + t, end);
     }
     __syncthreads();
     const float* sb = s.bc + j * LD;
@@ -523,10 +726,9 @@ scan_backward(const ScanArgs a, const ScanGrads g, const ScanBwdBuffers w) {
       for (int i = 0; i < NS; ++i) s.before[wave][q][i][lane] = h[i];
       if (q + 1 == groups) break;
       Token<T> cur;
-      cur.load(a, ch, t0 + q * 16 + j, end);
-      const float v = cur.dt + r.bias;
-      const float delta = ch.active ? (a.softplus ? softplus(v) : v) : 0.f;
-      const float dx = delta * cur.x;
+      cur.load(a, dout, ch, t0 + q * 16 + j, end);
+      const float delta = ch.active ? delta_of(a, cur.dt() + r.bias) : 0.f;
+      const float dx = ch.active ? delta * cur.x() : 0.f;
       static_for<4>([&](auto k4) {
         f32x4 B[NS];
 #pragma unroll
@@ -540,16 +742,16 @@ scan_backward(const ScanArgs a, const ScanGrads g, const ScanBwdBuffers w) {
         });
       });
     }
-    TokenGrad<T> next;
+    Token<T> next;
     next.load(a, dout, ch, t0 + (groups - 1) * 16 + j, end);
     for (int q = groups - 1; q >= 0; --q) {
-      const TokenGrad<T> cur = next;
-      const int64_t tok = t0 + q * 16 + j;
+      const Token<T> cur = next;
+      const int tok = t0 + q * 16 + j;
       if (q > 0) next.load(a, dout, ch, tok - 16, end);
-      const float v = cur.dt + r.bias;
+      const float v = cur.dt() + r.bias;
       const bool there = tok < end && ch.active;
-      const float delta = there ? (a.softplus ? softplus(v) : v) : 0.f;
-      const float dx = there ? delta * cur.x : 0.f;
+      const float delta = there ? delta_of(a, v) : 0.f;
+      const float dx = there ? delta * cur.x() : 0.f;
       float first[NS], hh[16][NS], dd[16][NS], p[16];
 #pragma unroll
       for (int i = 0; i < NS; ++i) first[i] = s.before[wave][q][i][lane];
@@ -573,12 +775,12 @@ scan_backward(const ScanArgs a, const ScanGrads g, const ScanBwdBuffers w) {
           p[k] = y;
         });
       });
-      float dy = cur.dout;
-      if (a.z) {
-        const float y = row_sums(p, j) + r.skip * cur.x, sg = sigmoid(cur.z);
-        const float dz = cur.dout * y * (sg * (1.f + cur.z * (1.f - sg)));
-        dy = cur.dout * (cur.z * sg);
-        if (there) ((T*)g.dz)[tok * a.D + ch.c] = Elem<T>::from_f32(dz);
+      float dy = cur.dout();
+      if (a.has_z) {
+        const float y = row_sums(p, j) + r.skip * cur.x(), sg = sigmoid(cur.z());
+        const float dz = cur.dout() * y * (sg * (1.f + cur.z() * (1.f - sg)));
+        dy = cur.dout() * (cur.z() * sg);
+        if (there) ((T*)g.dz)[(int64_t)tok * a.D + ch.c] = Elem<T>::from_f32(dz);
       }
       dy = there ? dy : 0.f;
       f32x4 tb[NS], tc[NS];
@@ -612,11 +814,11 @@ scan_backward(const ScanArgs a, const ScanGrads g, const ScanBwdBuffers w) {
         });
       });
       const float s1 = kLn2 * row_sums(p1, j), s2 = row_sums(p2, j);
-      const float ddt = (s1 + cur.x * s2) * (a.softplus ? sigmoid(v) : 1.f);
+      const float ddt = (s1 + cur.x() * s2) * (a.softplus ? sigmoid(v) : 1.f);
       if (there) {
-        ((T*)g.dx)[tok * a.D + ch.c] = Elem<T>::from_f32(r.skip * dy + delta * s2);
-        ((T*)g.ddt)[tok * a.D + ch.c] = Elem<T>::from_f32(ddt);
-        dskip += dy * cur.x;
+        ((T*)g.dx)[(int64_t)tok * a.D + ch.c] = Elem<T>::from_f32(r.skip * dy + delta * s2);
+        ((T*)g.ddt)[(int64_t)tok * a.D + ch.c] = Elem<T>::from_f32(ddt);
+        dskip += dy * cur.x();
         dbias += ddt;
       }
       // the workgroup's dB and dC of these tokens, waves in order
@@ -632,12 +834,12 @@ scan_backward(const ScanArgs a, const ScanGrads g, const ScanBwdBuffers w) {
 #pragma unroll
       for (int at = threadIdx.x; at < 2 * NS * 256; at += THREADS) {
         const int which = at / (NS * 256), i = at / 256 % NS, el = at % 256, n = (el & 15) + 16 * i;
-        const int64_t t = t0 + q * 16 + (el >> 4);
+        const int t = t0 + q * 16 + (el >> 4);
         float sum = 0.f;
 #pragma unroll
         for (int wv = 0; wv < WV; ++wv) sum += s.tiles[buf][wv][which][i][el];
         if (n < a.N && t < end)
-          (which ? w.dc : w.db)[((in_group * a.tokens + t) * a.G + ch.g) * a.N + n] = sum;
+          (which ? w.dc : w.db)[(((int64_t)in_group * a.tokens + t) * a.G + ch.g) * a.N + n] = sum;
       }
       buf ^= 1;
     }
@@ -645,45 +847,36 @@ scan_backward(const ScanArgs a, const ScanGrads g, const ScanBwdBuffers w) {
 
   float h[NS], gr[NS];
   // gradient of the state of sequence n at `end`, or at the slot's end
-  auto leaving = [&](int n, int64_t end) {
-    if (end <= hi) {
-      load_state<NS>(g.dht, n, a, ch.c, j, gr);
-      return;
-    }
-    int64_t i = (end - 1) / a.slot;
-    load_state<NS>(w.adj, i, a, ch.c, j, gr);
-    for (--i; i > slot; --i) {
-      float e[NS];
-      load_state<NS>(w.adj, i, a, ch.c, j, e);
-      const float sd = w.sum[i * a.D + ch.c];
-#pragma unroll
-      for (int k = 0; k < NS; ++k) gr[k] = exp2_fast(sd * r.A2[k]) * gr[k] + e[k];
-    }
+  auto leaving = [&](int n, int end) {
+    load_state<NS>(end <= hi ? g.dht : w.adj, end <= hi ? n : slot + 1, a, ch, gr);
   };
-  int n = seqs.from(lo);
-  if (n > 0 && seqs.end(n - 1) > lo) {
-    const int64_t end = seqs.end(n - 1);
-    incoming<NS>(a, w.hend, w.sum, seqs.start(n - 1), slot, ch.c, j, r, h);
-    leaving(n - 1, end);
-    range(lo, end < hi ? end : hi, h, gr);
+  int n = uniform(seqs.from(lo));
+  if (n > 0) {
+    const int end = uniform((int)seqs.end(n - 1));
+    if (end > lo) {  // entered from an earlier slot
+      load_state<NS>(w.hend, slot - 1, a, ch, h);
+      leaving(n - 1, end);
+      range(lo, end < hi ? end : hi, h, gr);
+    }
   }
-  for (; n < a.n_seqs && (slot + 1 >= a.n_slots || seqs.start(n) < hi); ++n) {
-    const int64_t start = seqs.start(n), end = seqs.end(n);
-    load_state<NS>(a.h0, n, a, ch.c, j, h);
+  for (; n < a.n_seqs; ++n) {
+    const int start = uniform((int)seqs.start(n)), end = uniform((int)seqs.end(n));
+    if (!own.last && start >= hi) break;
+    load_state<NS>(a.h0, n, a, ch, h);
     leaving(n, end);
     if (start < end) range(start, end < hi ? end : hi, h, gr);
-    if (g.dh0) store_state<NS>(g.dh0, n, a, ch, j, gr);
+    if (g.dh0) store_state<NS>(g.dh0, n, a, ch, gr);
   }
-  store_state<NS>(w.da, slot, a, ch, j, dA);
+  store_state<NS>(w.da, slot, a, ch, dA);
   dskip = row_sum(dskip);
   dbias = row_sum(dbias);
   if (ch.active && j == 0) {
-    w.dskip[slot * a.D + ch.c] = dskip;
-    w.dbias[slot * a.D + ch.c] = dbias;
+    w.dskip[(int64_t)slot * a.D + ch.c] = dskip;
+    w.dbias[(int64_t)slot * a.D + ch.c] = dbias;
   }
 }
 
-// Third launch, part one: dA, dskip and dbias, the slots' rows added: 64
+// The sums of dA, dskip and dbias over the slots: 64
 // columns a workgroup, rows dealt to 16 waves whose sums are added in order.
 __global__ void __launch_bounds__(1024)
 scan_sum_slots(const float* __restrict__ da, const float* __restrict__ ds, const float* __restrict__ db, int n_rows,
@@ -713,7 +906,7 @@ scan_sum_slots(const float* __restrict__ da, const float* __restrict__ ds, const
   out[col] = v;
 }
 
-// Part two: dB and dC, the channel workgroups' sums added.
+// dB and dC: the channel workgroups' sums added.
 template <typename T>
 __global__ void __launch_bounds__(256)
 scan_sum_channels(const float* __restrict__ db, const float* __restrict__ dc, int n_rows, int64_t cols,
@@ -730,20 +923,32 @@ scan_sum_channels(const float* __restrict__ db, const float* __restrict__ dc, in
 }
 
 // ---- launches ------------------------------------------------------------------
+template <typename F>
+int launch_chain(const ScanArgs& a, F* hend, F* adj, const F* sum, const int* kind, hipStream_t st) {
+  const int64_t dn = (int64_t)a.D * a.N;
+  return (int)launch_kernel(scan_chain, dim3((unsigned)ceil_div(dn, 64), adj ? 2 : 1), dim3(64 * kChainWaves), st, a.A,
+                            dn, a.N, a.D, (int)a.n_slots, hend, adj, sum, kind);
+}
+
 template <typename T, int NS>
 int forward_t(ScanArgs a, const ScanPlan& p, void* o, float* ht, void* ws, hipStream_t st) {
   a.slot = p.slot;
   a.n_slots = p.n_slots;
-  a.blocks_per_group = (int)ceil_div(a.D / a.G, 4 * kScanWaves);
-  float* hend = p.carry ? (float*)((char*)ws + p.hend_off) : nullptr;
-  float* sum = p.carry ? (float*)((char*)ws + p.sum_off) : nullptr;
+  a.blocks_per_group = (int)ceil_div(a.D / a.G, 16 * kScanWaves);
+  float *hend = nullptr, *sum = nullptr;
+  int* kind = nullptr;
   if (p.carry) {
-    const hipError_t e = launch_kernel(scan_forward<T, NS, false>, work_grid(a), dim3(64 * kScanWaves), st, a, hend,
-                                       sum, (T*)nullptr, (float*)nullptr);
+    hend = (float*)((char*)ws + p.hend_off);
+    sum = (float*)((char*)ws + p.sum_off);
+    kind = (int*)((char*)ws + p.kind_off);
+    const hipError_t e = launch_kernel(scan_forward<T, NS, kState>, work_grid(a), dim3(64 * kScanWaves), st, a, hend,
+                                       sum, kind, (T*)nullptr, (float*)nullptr);
     if (e != hipSuccess) return (int)e;
+    const int err = launch_chain(a, hend, (float*)nullptr, sum, kind, st);
+    if (err != 0) return err;
   }
-  return (int)launch_kernel(scan_forward<T, NS, true>, work_grid(a), dim3(64 * kScanWaves), st, a, hend, sum, (T*)o,
-                            ht);
+  return (int)launch_kernel(scan_forward<T, NS, kOutput>, work_grid(a), dim3(64 * kScanWaves), st, a, hend, sum, kind,
+                            (T*)o, ht);
 }
 
 template <typename T>
@@ -764,6 +969,30 @@ int step_t(const ScanArgs& a, float* state, void* o, hipStream_t st) {
   return a.N % 4 == 0 ? lanes(std::true_type{}) : lanes(std::false_type{});
 }
 
+// f(element type, states per lane) for the forward scans, which share a
+// channel's states among 4 lanes, and for the backward scan (16 lanes)
+template <typename F>
+int dispatch_quads(int is_bf16, int N, F&& f) {
+  auto states = [&](auto t) {
+    return N <= 4    ? f(t, std::integral_constant<int, 1>{})
+           : N <= 8  ? f(t, std::integral_constant<int, 2>{})
+           : N <= 16 ? f(t, std::integral_constant<int, 4>{})
+           : N <= 32 ? f(t, std::integral_constant<int, 8>{})
+                     : f(t, std::integral_constant<int, 16>{});
+  };
+  return is_bf16 ? states(bf16_t{}) : states(float{});
+}
+template <typename F>
+int dispatch_rows(int is_bf16, int N, F&& f) {
+  auto states = [&](auto t) {
+    const int ns = scan_ns(N);
+    return ns == 1   ? f(t, std::integral_constant<int, 1>{})
+           : ns == 2 ? f(t, std::integral_constant<int, 2>{})
+                     : f(t, std::integral_constant<int, 4>{});
+  };
+  return is_bf16 ? states(bf16_t{}) : states(float{});
+}
+
 template <typename T, int NS>
 int backward_t(ScanArgs a, const ScanBwdPlan& p, const ScanGrads& g, void* ws, hipStream_t st) {
   char* base = (char*)ws;
@@ -771,15 +1000,21 @@ int backward_t(ScanArgs a, const ScanBwdPlan& p, const ScanGrads& g, void* ws, h
   a.slot = p.slot;
   a.n_slots = p.n_slots;
   float *hend = at(p.hend_off), *adj = at(p.adj_off), *sum = at(p.sum_off);
+  int* kind = (int*)(base + p.kind_off);
   hipError_t e;
   if (p.carry) {
-    a.blocks_per_group = (int)ceil_div(a.D / a.G, 4 * kScanWaves);
-    e = launch_kernel(scan_backward_carry<T, NS>, work_grid(a), dim3(64 * kScanWaves), st, a, (const T*)g.dout,
-                      g.dht, hend, adj, sum);
-    if (e != hipSuccess) return (int)e;
+    a.blocks_per_group = (int)ceil_div(a.D / a.G, 16 * kScanWaves);
+    const int err = dispatch_quads(sizeof(T) == 2, a.N, [&](auto t, auto ns) {
+      typedef decltype(t) U;
+      return (int)launch_kernel(scan_backward_carry<U, ns.value>, work_grid(a), dim3(64 * kScanWaves), st, a,
+                                (const U*)g.dout, g.dht, hend, adj, sum, kind);
+    });
+    if (err != 0) return err;
+    const int err2 = launch_chain(a, hend, adj, sum, kind, st);
+    if (err2 != 0) return err2;
   }
   a.blocks_per_group = p.blocks_per_group;
-  const ScanBwdBuffers w{hend, adj, sum, at(p.da_off), at(p.dskip_off), at(p.dbias_off), at(p.db_off), at(p.dc_off)};
+  const ScanBwdBuffers w{hend, adj, at(p.da_off), at(p.dskip_off), at(p.dbias_off), at(p.db_off), at(p.dc_off)};
   e = launch_kernel(scan_backward<T, NS>, work_grid(a), dim3(64 * scan_bwd_waves(NS)), st, a, g, w);
   if (e != hipSuccess) return (int)e;
   const int64_t dn = (int64_t)a.D * a.N, cols = a.tokens * a.G * a.N;
@@ -790,30 +1025,18 @@ int backward_t(ScanArgs a, const ScanBwdPlan& p, const ScanGrads& g, void* ws, h
                             p.blocks_per_group, cols, a.cu, a.n_seqs, (int64_t)a.G * a.N, (T*)g.dB, (T*)g.dC);
 }
 
-// f(element type, states per lane) for a call's type and number of states
-template <typename F>
-int dispatch(int is_bf16, int N, F&& f) {
-  auto states = [&](auto t) {
-    const int ns = scan_ns(N);
-    return ns == 1   ? f(t, std::integral_constant<int, 1>{})
-           : ns == 2 ? f(t, std::integral_constant<int, 2>{})
-                     : f(t, std::integral_constant<int, 4>{});
-  };
-  return is_bf16 ? states(bf16_t{}) : states(float{});
-}
-
 }  // namespace
 
 int launch_scan_forward(int is_bf16, const ScanArgs& a, const ScanPlan& p, void* o, float* ht, void* ws,
                         void* stream) {
-  return dispatch(is_bf16, a.N, [&](auto t, auto ns) {
+  return dispatch_quads(is_bf16, a.N, [&](auto t, auto ns) {
     return forward_t<decltype(t), ns.value>(a, p, o, ht, ws, (hipStream_t)stream);
   });
 }
 
 int launch_scan_backward(int is_bf16, const ScanArgs& a, const ScanBwdPlan& p, const ScanGrads& g, void* ws,
                          void* stream) {
-  return dispatch(is_bf16, a.N, [&](auto t, auto ns) {
+  return dispatch_rows(is_bf16, a.N, [&](auto t, auto ns) {
     return backward_t<decltype(t), ns.value>(a, p, g, ws, (hipStream_t)stream);
   });
 }
