@@ -274,6 +274,7 @@ int check_scan(const kda_scan_desc_t* d, ScanSizes* s) {
   if (n > (size_t)INT32_MAX - 4096) return KDA_ERR_UNSUPPORTED;
   for (int64_t ld : {a.ld_x, a.ld_dt, a.ld_z, (int64_t)d->D})
     if (ld > (1 << 24)) return KDA_ERR_UNSUPPORTED;
+  if ((int64_t)d->D * d->N > (1 << 28)) return KDA_ERR_UNSUPPORTED;  // likewise inside a row of states
   a.n_seqs = (int)s->t.seqs;
   a.T = d->T;
   a.tokens = (int64_t)n;
@@ -376,7 +377,7 @@ int kda_selective_scan_backward_workspace_size(const kda_scan_desc_t* d, size_t*
   ScanSizes s;
   const int st = check_scan(d, &s);
   if (st != KDA_OK) return st;
-  *bytes = kda::plan_scan_backward(s.a.tokens, d->D, d->N, d->G).ws_bytes;
+  *bytes = kda::plan_scan_backward(s.a.tokens, s.a.n_seqs, d->D, d->N, d->G).ws_bytes;
   return KDA_OK;
 }
 
@@ -394,7 +395,7 @@ int kda_selective_scan_backward(const kda_scan_desc_t* d, const void* x, const v
     return KDA_ERR_INVALID_ARGUMENT;
   if (!A || !dA) return KDA_ERR_INVALID_ARGUMENT;
   if ((d->n_seqs > 0) != (cu_seqlens != nullptr)) return KDA_ERR_INVALID_ARGUMENT;
-  const kda::ScanBwdPlan p = kda::plan_scan_backward(s.a.tokens, d->D, d->N, d->G);
+  const kda::ScanBwdPlan p = kda::plan_scan_backward(s.a.tokens, s.a.n_seqs, d->D, d->N, d->G);
   if ((st = check_workspace(workspace, workspace_bytes, p.ws_bytes)) != KDA_OK) return st;
   Buffers b;
   scan_inputs(&b, s, x, dt, A, Bm, Cm, skip, z, dt_bias);

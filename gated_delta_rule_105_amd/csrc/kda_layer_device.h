@@ -98,7 +98,8 @@ template <int K>
 __device__ __forceinline__ float row_bcast(float v) {
   return dpp<0x150 + K>(v);
 }
-constexpr int kRowMirror = 0x140, kHalfMirror = 0x141, kQuadMirror = 0x1b, kPairSwap = 0xb1;
+constexpr int kRowMirror = 0x140, kHalfMirror = 0x141, kQuadMirror = 0x1b, kPairSwap = 0xb1, kQuadSwap = 0x4e,
+              kRotate4 = 0x124, kRotate8 = 0x128;
 
 // sum over the row, in every lane
 __device__ __forceinline__ float row_sum(float v) {
@@ -107,21 +108,6 @@ __device__ __forceinline__ float row_sum(float v) {
   v += dpp<kHalfMirror>(v);
   v += dpp<kRowMirror>(v);
   return v;
-}
-
-// Sixteen sums over the row at once: lane j returns the sum over the row's
-// lanes of p[j].  Each step halves the tokens a lane answers for and adds the
-// mirror lane's share of them, 15 additions in place of 64.
-__device__ __forceinline__ float row_sums(float (&p)[16], int j) {
-  const bool b3 = j & 8, b2 = j & 4, b1 = j & 2, b0 = j & 1;
-  float s8[8], s4[4], s2[2];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) s8[k] = (b3 ? p[k + 8] : p[k]) + dpp<kRowMirror>(b3 ? p[k] : p[k + 8]);
-#pragma unroll
-  for (int k = 0; k < 4; ++k) s4[k] = (b2 ? s8[k + 4] : s8[k]) + dpp<kHalfMirror>(b2 ? s8[k] : s8[k + 4]);
-#pragma unroll
-  for (int k = 0; k < 2; ++k) s2[k] = (b1 ? s4[k + 2] : s4[k]) + dpp<kQuadMirror>(b1 ? s4[k] : s4[k + 2]);
-  return (b0 ? s2[1] : s2[0]) + dpp<kPairSwap>(b0 ? s2[0] : s2[1]);
 }
 
 // calls f(std::integral_constant<int, 0>) .. f(<N - 1>)

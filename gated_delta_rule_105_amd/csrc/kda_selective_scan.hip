@@ -309,11 +309,30 @@ __device__ __forceinline__ float scan_group(const ScanArgs& a, const Channel& ch
   return sum;
 }
 
+// What the backward pass keeps of every group of 16 tokens: the state before
+// it, scanned from what the range started from, and the range's sum of delta
+// before it.  Groups are numbered by groups_at(): ranges follow one another,
+// each starts a group of its own.
+struct GroupStates {
+  float *h, *sum;
+};
+__device__ __forceinline__ int groups_at(int t0, int seq, int slot) { return t0 / 16 + seq + slot; }
+
+template <int NS>
+__device__ __forceinline__ void keep_group(const ScanArgs& a, const Channel& ch, const GroupStates& k, int group,
+                                           const float (&h)[NS], float sum) {
+  store_state<NS>(k.h, group, a, ch, h);
+  const float total = sum_rows({sum, sum, sum, sum});
+  if (ch.active && ch.first == 0) k.sum[(int64_t)group * a.D + ch.c] = total;
+}
+
 // Scans tokens [t0, end) of one sequence.  Returns the lane's sum of delta.
-template <typename T, int NS, Mode M>
+// KEEP: leaves what GroupStates says from group `group` on.
+template <typename T, int NS, Mode M, bool KEEP = false>
 __device__ __forceinline__ float scan_range(const ScanArgs& a, const Channel& ch, const Rates<NS>& r, int q,
                                             const LaneOffsets& l, int t0, int end, float* s, Scanned<NS>& st,
-                                            T* __restrict__ o, const T* __restrict__ dout) {
+                                            T* __restrict__ o, const T* __restrict__ dout, GroupStates keep = {},
+                                            int group = 0) {
   constexpr int THREADS = 64 * kScanWaves, NP = 4 * NS, C_OFF = kScanTile * NP, BUF = 2 * C_OFF;
   TileRows<T, NP, kScanTile, THREADS> tile;
   Four<T, M> next;
@@ -332,11 +351,13 @@ __device__ __forceinline__ float scan_range(const ScanArgs& a, const Channel& ch
     for (; u + 16 <= end && u < t + kScanTile; u += 16) {
       const Four<T, M> cur = next;
       if (u + 32 <= end) next.load(a, dout, l, u + 16);
+      if (KEEP) keep_group<NS>(a, ch, keep, group++, st.h, sum);
       sum += scan_group<T, NS, M, true>(a, ch, r, q, cur, l, u, end, sq + (u - t) * NP, C_OFF, st, o);
     }
     if (u < end && u < t + kScanTile) {
       Four<T, M> cur;
       cur.load(a, dout, ch, u, q, end);
+      if (KEEP) keep_group<NS>(a, ch, keep, group++, st.h, sum);
       sum += scan_group<T, NS, M, false>(a, ch, r, q, cur, l, u, end, sq + (u - t) * NP, C_OFF, st, o);
     }
     if (more) {
@@ -432,7 +453,8 @@ scan_forward(const ScanArgs a, float* __restrict__ hend, float* __restrict__ sum
 // first composing it to (product of the decays, state), then again from the
 // state that the waves before hand on, so that the chain is an eighth as
 // long.  Loads go ahead of it in batches.
-constexpr int kChainWaves = 8, kChainBatch = 16;
+constexpr int kChainWaves = 8;
+template <int BATCH>
 __global__ void __launch_bounds__(64 * kChainWaves)
 scan_chain(const float* __restrict__ A, int64_t dn, int N, int D, int n_slots, float* __restrict__ hend,
            float* __restrict__ adj, const float* __restrict__ sum, const int* __restrict__ kind) {
@@ -451,18 +473,18 @@ scan_chain(const float* __restrict__ A, int64_t dn, int N, int D, int n_slots, f
   const int first = wave * per, last = first + per < n_slots ? first + per : n_slots;
   int unbroken = 1;
   auto walk = [&](float& d, float& h, bool write) {
-    for (int i0 = first; i0 < last; i0 += kChainBatch) {
-      float s[kChainBatch], x[kChainBatch];
-      int kd[kChainBatch];
+    for (int i0 = first; i0 < last; i0 += BATCH) {
+      float s[BATCH], x[BATCH];
+      int kd[BATCH];
 #pragma unroll
-      for (int k = 0; k < kChainBatch; ++k) {
+      for (int k = 0; k < BATCH; ++k) {
         const int i = i0 + k < last ? i0 + k : last - 1, slot = back ? n_slots - 1 - i : i;
         s[k] = sum[(int64_t)slot * D + c];
         x[k] = v[(int64_t)slot * dn + el];
         kd[k] = kind[slot];
       }
 #pragma unroll
-      for (int k = 0; k < kChainBatch; ++k) {
+      for (int k = 0; k < BATCH; ++k) {
         if (i0 + k >= last) break;
         // what the slot holds counts only where a sequence leaves it (back: enters it)
         const bool passed = kd[k] & kPassed, holds = back ? kd[k] & kEntered : kd[k] & (kStarted | kPassed);
@@ -549,20 +571,21 @@ __global__ void __launch_bounds__(256) scan_step(const ScanArgs a, float* __rest
 }
 
 // ---- backward ------------------------------------------------------------------
-// Two launches, only when sequences pass from slot to slot, make the states
-// and gradients between the slots: every slot is walked once for the state
-// it hands on (as forward) and the gradient it hands back (the part of the
-// state gradient at its start that its own tokens make, summed forward in
-// time with the running product of the decays), and scan_chain composes
-// those.  The next takes every slot from both: it runs forward leaving the
-// state before every group of 16 tokens in LDS, then walks the groups back,
-// redoing each group's recurrence in registers.  The last two add the
-// partial sums.
+// The first launch walks every slot forward once and leaves the state before
+// every group of 16 tokens, the state that the slot hands on, and the
+// gradient it hands back (the part of the state gradient at its start that
+// its own tokens make, summed forward in time with the running product of
+// the decays).  A range that continues an earlier slot's sequence starts from
+// zero there; what the state that truly enters adds to a group's state is
+// exp(A sum delta) times it.  scan_chain, when sequences pass from slot to
+// slot, composes the states and gradients between them.  The next launch
+// walks the groups of every slot back, redoing each group's recurrence in
+// registers.  The last two add the partial sums.
 template <typename T, int NS>
 __global__ void __launch_bounds__(64 * kScanWaves, 2)
-scan_backward_carry(const ScanArgs a, const T* __restrict__ dout, const float* __restrict__ dht,
-                    float* __restrict__ hend, float* __restrict__ adj, float* __restrict__ sum,
-                    int* __restrict__ kind) {
+scan_backward_states(const ScanArgs a, const T* __restrict__ dout, const float* __restrict__ dht,
+                     float* __restrict__ hend, float* __restrict__ adj, float* __restrict__ sum,
+                     int* __restrict__ kind, const GroupStates keep) {
   __shared__ __align__(16) float s[2 * 2 * kScanTile * 4 * NS];
   QuadWork<NS> w;
   if (!w.init(a, sizeof(T))) return;
@@ -579,8 +602,8 @@ scan_backward_carry(const ScanArgs a, const T* __restrict__ dout, const float* _
       st.h[i] = st.adj[i] = 0.f;
       st.run[i] = 1.f;
     }
-    const float d = scan_range<T, NS, kAdjoint>(a, w.ch, w.r, w.q, w.l, lo, before < hi ? before : hi, s, st,
-                                                (T*)nullptr, dout);
+    const float d = scan_range<T, NS, kAdjoint, true>(a, w.ch, w.r, w.q, w.l, lo, before < hi ? before : hi, s, st,
+                                                      (T*)nullptr, dout, keep, groups_at(lo, n - 1, w.slot));
     if (before <= hi) {
       float last[NS];
       load_state<NS>(dht, n - 1, a, w.ch, last);
@@ -593,36 +616,41 @@ scan_backward_carry(const ScanArgs a, const T* __restrict__ dout, const float* _
     }
     store_state<NS>(adj, w.slot, a, w.ch, st.adj);
   }
-  n = uniform(seqs.from(hi)) - 1;
-  const int start = n >= 0 ? uniform((int)seqs.start(n)) : -1;
-  if (start >= lo && uniform((int)seqs.end(n)) > hi) {  // starts here and goes on
-    found |= kStarted;
+  for (; n < a.n_seqs; ++n) {
+    const int start = uniform((int)seqs.start(n)), end = uniform((int)seqs.end(n));
+    if (start >= hi) break;
+    if (start >= end) continue;
     load_state<NS>(a.h0, n, a, w.ch, st.h);
-    scan_range<T, NS, kState>(a, w.ch, w.r, w.q, w.l, start, hi, s, st, (T*)nullptr, dout);
-    store_state<NS>(hend, w.slot, a, w.ch, st.h);
+    scan_range<T, NS, kState, true>(a, w.ch, w.r, w.q, w.l, start, end < hi ? end : hi, s, st, (T*)nullptr, dout, keep,
+                                    groups_at(start, n, w.slot));
+    if (end > hi) {  // goes on past the slot
+      found |= kStarted;
+      store_state<NS>(hend, w.slot, a, w.ch, st.h);
+    }
   }
-  if (threadIdx.x == 0) kind[w.slot] = found;
+  if (kind && threadIdx.x == 0) kind[w.slot] = found;
 }
 
 // Layout of the backward scan ("rows").  A row of 16 lanes holds one channel,
 // lane j the states j, j + 16, ... and, of a group of 16 tokens, the inputs
 // of token j; a wave has 4 channels.  In the recurrence token k's values are
-// lane k's, broadcast over the row as an operand modifier, and the sums over
-// the states of a group's 16 tokens are taken together (row_sums).  Sums over
-// channels, of which the backward pass has two per element, are products of
-// the wave's 4 rows: v_mfma_f32_16x16x4f32 with the token's dy (delta x) in
-// row k of the left operand, zeros in the others, and h (dh) as it lies in
-// the registers, so a group's 16 products accumulate into one [16 tokens][16
-// states] tile.  The tiles of the waves are added in LDS, those of the
-// workgroups by a later launch.  B and C of the slot are staged as
-// [state][token] with rows of slot + 4 words: four tokens are one 16-byte
-// read, free of bank conflicts.
+// lane k's, broadcast over the row as an operand modifier; the sums over the
+// states of a group's tokens are folded lane by lane (RowSums) as the tokens
+// come.  Sums over channels, of which the backward pass has two per element,
+// are those of the wave's 4 rows: v_mfma_f32_16x16x4f32 with ones in row k of
+// the left operand, zeros in the others, and the products of token k (dh
+// delta x, h dy) on the right, so that a group's 16 tokens accumulate into
+// one [16 tokens][16 states] tile beside the vector unit.  The tiles of the
+// waves are added in LDS, those of the workgroups by a later launch.  B and C
+// of 64 tokens are staged as [state][token] with rows of 68 words: four
+// tokens are one 16-byte read, free of bank conflicts.
+constexpr int kColLd = kScanTile + 4;
 
 // Tiles of B and C as [state][token]; a thread holds one state of every
 // (THREADS / 16)-th token.
-template <typename T, int NS, int TOK, int THREADS>
+template <typename T, int NS, int THREADS>
 struct TileCols {
-  static constexpr int PER = TOK * 16 / THREADS;  // tokens a thread
+  static constexpr int PER = kScanTile * 16 / THREADS;  // tokens a thread
   T b[NS][PER], c[NS][PER];
   __device__ __forceinline__ void load(const ScanArgs& a, int g, int t0, int end) {
     const int n = threadIdx.x & 15, t = threadIdx.x >> 4;
@@ -638,9 +666,8 @@ struct TileCols {
       }
     }
   }
-  // s: [2][NS * 16][LD], B first, the tile's tokens from column `at`
-  template <int LD>
-  __device__ __forceinline__ void store(const ScanArgs& a, float* s, int at, int t0, int end) const {
+  // s: [2][NS * 16][kColLd], B first
+  __device__ __forceinline__ void store(const ScanArgs& a, float* s, int t0, int end) const {
     const int n = threadIdx.x & 15, t = threadIdx.x >> 4;
 #pragma unroll
     for (int i = 0; i < NS; ++i)
@@ -648,119 +675,142 @@ struct TileCols {
       for (int k = 0; k < PER; ++k) {
         const int tok = t + k * (THREADS / 16);
         const bool there = n + 16 * i < a.N && t0 + tok < end;
-        s[(n + 16 * i) * LD + at + tok] = there ? Elem<T>::to_f32(b[i][k]) : 0.f;
-        s[(NS * 16 + n + 16 * i) * LD + at + tok] = there ? Elem<T>::to_f32(c[i][k]) : 0.f;
+        s[(n + 16 * i) * kColLd + tok] = there ? Elem<T>::to_f32(b[i][k]) : 0.f;
+        s[(NS * 16 + n + 16 * i) * kColLd + tok] = there ? Elem<T>::to_f32(c[i][k]) : 0.f;
       }
   }
 };
 
-// Lane j's token of a group (the range's last one past its end).
-template <typename T>
+// Sixteen sums over a row of 16 lanes, lane j's result that of token j.  The
+// tokens come in order, from either end; each fold halves the tokens a lane
+// answers for and adds the share of the lane 1, 2, 4 or 8 off, which answers
+// for the other half and for the same of the halvings before, so 16 sums take
+// 15 additions in place of 64.
+struct RowSums {
+  float v[16], v2[8], v4[4], v8[2], total;
+  template <int CTRL>
+  __device__ __forceinline__ static float fold(float lo, float hi, bool up) {
+    return (up ? hi : lo) + dpp<CTRL>(up ? lo : hi);
+  }
+  // after v[K] has been set; DOWN: the tokens come from the last to the first
+  template <int K, bool DOWN>
+  __device__ __forceinline__ void done(int j) {
+    constexpr int at = DOWN ? 0 : 1;
+    if constexpr (K % 2 == at) v2[K / 2] = fold<kPairSwap>(v[K & ~1], v[K | 1], j & 1);
+    if constexpr (K % 4 == 3 * at) v4[K / 4] = fold<kQuadSwap>(v2[K / 2 & ~1], v2[K / 2 | 1], j & 2);
+    if constexpr (K % 8 == 7 * at) v8[K / 8] = fold<kRotate4>(v4[K / 4 & ~1], v4[K / 4 | 1], j & 4);
+    if constexpr (K == 15 * at) total = fold<kRotate8>(v8[0], v8[1], j & 8);
+  }
+};
+
+// 1 in lane K of every row, 0 elsewhere, from the same for lane 0
+template <int K>
+__device__ __forceinline__ float one_at(float first) {
+  if constexpr (K == 0) return first;
+  else return dpp<0x120 + K>(first);  // rotates each row by K lanes
+}
+
+// What the backward scan reads and writes beside the inputs.
+struct ScanBwdBuffers {
+  const float *hend, *adj;    // at every slot's end and start; null without carry
+  GroupStates groups;
+  float *da, *dskip, *dbias;  // per slot
+  float *db, *dc;             // per workgroup of channels
+};
+
+// Lane j's token of a group, and the lane's states before the group.
+template <typename T, int NS>
 struct Token {
   T x_, dt_, z_, dout_;
-  __device__ __forceinline__ void load(const ScanArgs& a, const T* __restrict__ g, const Channel& ch, int t, int end) {
-    const int64_t tok = t < end ? t : end - 1;
-    x_ = ((const T*)a.x)[tok * a.ld_x + ch.c];
-    dt_ = ((const T*)a.dt)[tok * a.ld_dt + ch.c];
-    z_ = ((const T*)a.z)[tok * a.ld_z + ch.c];
-    dout_ = g[tok * a.D + ch.c];
+  float h_[NS], sum_;
+  __device__ __forceinline__ void load(const ScanArgs& a, const T* __restrict__ dout, const GroupStates& k,
+                                       const Channel& ch, const LaneOffsets& l, int t, int group) {
+    auto at = [&](const void* p, int64_t ld, uint32_t off) {
+      return *(const T*)((const char*)((const T*)p + t * ld) + off);
+    };
+    x_ = at(a.x, a.ld_x, l.x);
+    dt_ = at(a.dt, a.ld_dt, l.dt);
+    z_ = at(a.z, a.ld_z, l.z);
+    dout_ = at(dout, a.D, l.o);
+    const float* row = k.sum + (int64_t)group * a.D;
+    sum_ = *(const float*)((const char*)row + 4u * (uint32_t)ch.c);
+    const float* states = k.h + (int64_t)group * a.D * a.N;
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      const int n = ch.first + 16 * i;
+      h_[i] = *(const float*)((const char*)states + 4u * (uint32_t)(ch.c * a.N + (n < a.N ? n : a.N - 1)));
+    }
   }
   __device__ __forceinline__ float x() const { return Elem<T>::to_f32(x_); }
   __device__ __forceinline__ float dt() const { return Elem<T>::to_f32(dt_); }
   __device__ __forceinline__ float z() const { return Elem<T>::to_f32(z_); }
   __device__ __forceinline__ float dout() const { return Elem<T>::to_f32(dout_); }
 };
-
-// What the backward scan reads and writes beside the inputs.
-struct ScanBwdBuffers {
-  const float *hend, *adj;    // at every slot's end and start; null without carry
-  float *da, *dskip, *dbias;      // per slot
-  float *db, *dc;                 // per workgroup of channels
-};
+__device__ __forceinline__ LaneOffsets lane_offsets(const ScanArgs& a, int token, int c, size_t esz) {
+  const uint32_t e = (uint32_t)esz;
+  return LaneOffsets{e * (uint32_t)(token * a.ld_x + c), e * (uint32_t)(token * a.ld_dt + c),
+                     e * (uint32_t)(token * a.ld_z + c), e * (uint32_t)(token * (int64_t)a.D + c)};
+}
 
 template <typename T, int NS>
-struct BwdLds {
-  static constexpr int WV = scan_bwd_waves(NS), SLOT = scan_bwd_slot(NS), LD = SLOT + 4;
-  __align__(16) float bc[2 * NS * 16 * LD];     // B, C of the slot
-  float before[WV][SLOT / 16][NS][64];          // state before every group
-  float tiles[2][WV][2][NS][256];               // dB, dC of a group, per wave
-};
-
-template <typename T, int NS>
-__global__ void __launch_bounds__(64 * scan_bwd_waves(NS))
+__global__ void __launch_bounds__(64 * kScanBwdWaves, NS == 1 ? 3 : 1)
 scan_backward(const ScanArgs a, const ScanGrads g, const ScanBwdBuffers w) {
-  typedef BwdLds<T, NS> Lds;
-  constexpr int WV = Lds::WV, LD = Lds::LD, THREADS = 64 * WV;
-  __shared__ Lds s;
+  constexpr int WV = kScanBwdWaves, THREADS = 64 * WV;
+  __shared__ __align__(16) float bc[2 * NS * 16 * kColLd];  // B, C of a tile
+  __shared__ float tiles[2][WV][2][NS][256];                // dB, dC of a group, per wave
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), j = lane & 15;
   int slot, block;
   if (!work_of(a, &slot, &block)) return;
   const Channel ch = channel_of(a, block, wave * 4 + (lane >> 4), 4 * WV, j, 16);
-  const int in_group = block - ch.g * a.blocks_per_group;
+  const int group = uniform(ch.g), in_group = block - group * a.blocks_per_group;
   Rates<NS> r;
   r.load(a, ch);
   const Seqs seqs{a.cu, a.n_seqs, a.T, a.tokens};
   const Slot own = slot_of(a, slot);
   const int lo = own.lo, hi = own.hi;
   const T* __restrict__ dout = (const T*)g.dout;
+  const LaneOffsets l = lane_offsets(a, j, ch.c, sizeof(T));
+  const float first_one = j == 0 ? 1.f : 0.f;
   float dA[NS], dskip = 0.f, dbias = 0.f;
 #pragma unroll
   for (int i = 0; i < NS; ++i) dA[i] = 0.f;
   int buf = 0;
 
-  // tokens [t0, end) of one sequence: h the state before them, gr the
-  // gradient of the state after them; leaves the gradient of h in gr
-  auto range = [&](int t0, int end, float(&h)[NS], float(&gr)[NS]) {
-    const int groups = (end - t0 + 15) / 16;
+  // tokens [t0, end) of one sequence, whose groups are `at`, at + 1, ...: h
+  // the state that entered the range (zero when the groups' states have it),
+  // gr the gradient of the state after it; leaves the gradient of the state
+  // before it in gr
+  auto range = [&](int t0, int end, int at, const float(&h)[NS], float(&gr)[NS]) {
+    int q = (end - t0 - 1) / 16;
+    TileCols<T, NS, THREADS> tile;
+    tile.load(a, group, t0 + (q & ~3) * 16, end);
+    Token<T, NS> next;
+    const int left = end - t0 - 16 * q;  // tokens of the last group
+    next.load(a, dout, w.groups, ch, lane_offsets(a, j < left ? j : left - 1, ch.c, sizeof(T)), t0 + 16 * q, at + q);
     __syncthreads();  // the range before may still be reading
-    for (int t = 0; t < groups * 16; t += kScanTile) {
-      TileCols<T, NS, kScanTile, THREADS> tile;
-      tile.load(a, ch.g, t0 + t, end);
-      tile.template store<LD>(a, s.bc, t, t0 + t, end);
-    }
+    tile.store(a, bc, t0 + (q & ~3) * 16, end);
     __syncthreads();
-    const float* sb = s.bc + j * LD;
-    const float* sc = sb + NS * 16 * LD;
-    for (int q = 0; q < groups; ++q) {
-#pragma unroll
-      for (int i = 0; i < NS; ++i) s.before[wave][q][i][lane] = h[i];
-      if (q + 1 == groups) break;
-      Token<T> cur;
-      cur.load(a, dout, ch, t0 + q * 16 + j, end);
-      const float delta = ch.active ? delta_of(a, cur.dt() + r.bias) : 0.f;
-      const float dx = ch.active ? delta * cur.x() : 0.f;
-      static_for<4>([&](auto k4) {
-        f32x4 B[NS];
-#pragma unroll
-        for (int i = 0; i < NS; ++i) B[i] = *(const f32x4*)(sb + i * 16 * LD + q * 16 + 4 * k4);
-        static_for<4>([&](auto e) {
-          constexpr int k = 4 * decltype(k4)::value + decltype(e)::value;
-          const float dk = row_bcast<k>(delta), xk = row_bcast<k>(dx);
-#pragma unroll
-          for (int i = 0; i < NS; ++i)
-            h[i] = exp2_fast(dk * r.A2[i]) * h[i] + xk * B[i][decltype(e)::value];
-        });
-      });
-    }
-    Token<T> next;
-    next.load(a, dout, ch, t0 + (groups - 1) * 16 + j, end);
-    for (int q = groups - 1; q >= 0; --q) {
-      const Token<T> cur = next;
-      const int tok = t0 + q * 16 + j;
-      if (q > 0) next.load(a, dout, ch, tok - 16, end);
-      const float v = cur.dt() + r.bias;
-      const bool there = tok < end && ch.active;
+    bool there = ch.active && j < left;
+    for (; q >= 0; --q) {
+      const Token<T, NS> cur = next;
+      const int t = t0 + 16 * q;
+      if (q > 0) next.load(a, dout, w.groups, ch, l, t - 16, at + q - 1);
+      if ((q & 3) == 0 && q > 0) tile.load(a, group, t - kScanTile, end);
+      const float* sb = bc + j * kColLd + (q & 3) * 16;
+      const float* sc = sb + NS * 16 * kColLd;
+      const float v = cur.dt() + r.bias, x = cur.x();
       const float delta = there ? delta_of(a, v) : 0.f;
-      const float dx = there ? delta * cur.x() : 0.f;
-      float first[NS], hh[16][NS], dd[16][NS], p[16];
+      const float dx = there ? delta * x : 0.f;
+      float first[NS], hh[16][NS], dd[16][NS];
 #pragma unroll
-      for (int i = 0; i < NS; ++i) first[i] = s.before[wave][q][i][lane];
+      for (int i = 0; i < NS; ++i) first[i] = cur.h_[i] + exp2_fast(cur.sum_ * r.A2[i]) * h[i];
+      RowSums ys;
       static_for<4>([&](auto k4) {
         f32x4 B[NS], C[NS];
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
-          B[i] = *(const f32x4*)(sb + i * 16 * LD + q * 16 + 4 * k4);
-          C[i] = *(const f32x4*)(sc + i * 16 * LD + q * 16 + 4 * k4);
+          B[i] = *(const f32x4*)(sb + i * 16 * kColLd + 4 * k4);
+          C[i] = *(const f32x4*)(sc + i * 16 * kColLd + 4 * k4);
         }
         static_for<4>([&](auto e) {
           constexpr int k = 4 * decltype(k4)::value + decltype(e)::value;
@@ -769,56 +819,66 @@ scan_backward(const ScanArgs a, const ScanGrads g, const ScanBwdBuffers w) {
 #pragma unroll
           for (int i = 0; i < NS; ++i) {
             dd[k][i] = exp2_fast(dk * r.A2[i]);
-            hh[k][i] = dd[k][i] * (k ? hh[k ? k - 1 : 0][i] : first[i]) + xk * B[i][decltype(e)::value];
-            y += C[i][decltype(e)::value] * hh[k][i];
+            const float put = xk * B[i][decltype(e)::value];
+            hh[k][i] = __builtin_fmaf(dd[k][i], k ? hh[k ? k - 1 : 0][i] : first[i], put);
+            y = i ? y + C[i][decltype(e)::value] * hh[k][i] : C[i][decltype(e)::value] * hh[k][i];
           }
-          p[k] = y;
+          ys.v[k] = y;
+          ys.template done<k, false>(j);
         });
+        __builtin_amdgcn_sched_barrier(0);
       });
-      float dy = cur.dout();
-      if (a.has_z) {
-        const float y = row_sums(p, j) + r.skip * cur.x(), sg = sigmoid(cur.z());
-        const float dz = cur.dout() * y * (sg * (1.f + cur.z() * (1.f - sg)));
-        dy = cur.dout() * (cur.z() * sg);
-        if (there) ((T*)g.dz)[(int64_t)tok * a.D + ch.c] = Elem<T>::from_f32(dz);
-      }
+      const float z = cur.z(), dout_j = cur.dout(), sg = sigmoid(z), y = ys.total + r.skip * x;
+      const float dz = dout_j * y * (sg * (1.f + z * (1.f - sg)));
+      float dy = dout_j * (a.has_z ? z * sg : 1.f);
       dy = there ? dy : 0.f;
       f32x4 tb[NS], tc[NS];
 #pragma unroll
       for (int i = 0; i < NS; ++i) tb[i] = tc[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
-      float p1[16], p2[16];
+      RowSums s1, s2;
+      // other registers to the compiler, which would else keep the 32 values
+      // broadcast above for the loop below
+      float delta_b = delta, dx_b = dx;
+      asm volatile("" : "+v"(delta_b), "+v"(dx_b));
       static_for<4>([&](auto k4r) {
         constexpr int k4 = 3 - decltype(k4r)::value;
         f32x4 B[NS], C[NS];
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
-          B[i] = *(const f32x4*)(sb + i * 16 * LD + q * 16 + 4 * k4);
-          C[i] = *(const f32x4*)(sc + i * 16 * LD + q * 16 + 4 * k4);
+          B[i] = *(const f32x4*)(sb + i * 16 * kColLd + 4 * k4);
+          C[i] = *(const f32x4*)(sc + i * 16 * kColLd + 4 * k4);
         }
         static_for<4>([&](auto er) {
           constexpr int e = 3 - decltype(er)::value, k = 4 * k4 + e;
-          const float dk = row_bcast<k>(delta), gk = row_bcast<k>(dy);
-          const float of_dy = j == k ? dy : 0.f, of_dx = j == k ? dx : 0.f;
-          p1[k] = p2[k] = 0.f;
+          const float dk = row_bcast<k>(delta_b), gk = row_bcast<k>(dy), xk = row_bcast<k>(dx_b);
+          const float one = one_at<k>(first_one);
+          float p1 = 0.f, p2 = 0.f;
 #pragma unroll
           for (int i = 0; i < NS; ++i) {
-            const float dh = C[i][e] * gk + gr[i];
-            tc[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(of_dy, hh[k][i], tc[i], 0, 0, 0);
-            tb[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(of_dx, dh, tb[i], 0, 0, 0);
+            const float dh = __builtin_fmaf(gk, C[i][e], gr[i]);
+            tc[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(one, gk * hh[k][i], tc[i], 0, 0, 0);
+            tb[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(one, xk * dh, tb[i], 0, 0, 0);
             gr[i] = dh * dd[k][i];
             const float m = gr[i] * (k ? hh[k ? k - 1 : 0][i] : first[i]);
-            p1[k] += m * r.A2[i];
-            p2[k] += dh * B[i][e];
-            dA[i] += m * dk;
+            p1 = i ? p1 + m * r.A2[i] : m * r.A2[i];
+            p2 = i ? p2 + dh * B[i][e] : dh * B[i][e];
+            dA[i] = __builtin_fmaf(dk, m, dA[i]);
           }
+          s1.v[k] = p1;
+          s2.v[k] = p2;
+          s1.template done<k, true>(j);
+          s2.template done<k, true>(j);
         });
+        __builtin_amdgcn_sched_barrier(0);
       });
-      const float s1 = kLn2 * row_sums(p1, j), s2 = row_sums(p2, j);
-      const float ddt = (s1 + cur.x() * s2) * (a.softplus ? sigmoid(v) : 1.f);
+      const float slope = a.softplus ? sigmoid(v) : 1.f;
+      const float ddt = (kLn2 * s1.total + x * s2.total) * slope;
       if (there) {
-        ((T*)g.dx)[(int64_t)tok * a.D + ch.c] = Elem<T>::from_f32(r.skip * dy + delta * s2);
-        ((T*)g.ddt)[(int64_t)tok * a.D + ch.c] = Elem<T>::from_f32(ddt);
-        dskip += dy * cur.x();
+        auto to = [&](void* p) { return (T*)((char*)((T*)p + (int64_t)t * a.D) + l.o); };
+        *to(g.dx) = Elem<T>::from_f32(r.skip * dy + delta * s2.total);
+        *to(g.ddt) = Elem<T>::from_f32(ddt);
+        if (a.has_z) *to(g.dz) = Elem<T>::from_f32(dz);
+        dskip += dy * x;
         dbias += ddt;
       }
       // the workgroup's dB and dC of these tokens, waves in order
@@ -826,22 +886,26 @@ scan_backward(const ScanArgs a, const ScanGrads g, const ScanBwdBuffers w) {
       for (int i = 0; i < NS; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int at = (4 * (lane >> 4) + e) * 16 + j;
-          s.tiles[buf][wave][0][i][at] = tb[i][e];
-          s.tiles[buf][wave][1][i][at] = tc[i][e];
+          tiles[buf][wave][0][i][(4 * (lane >> 4) + e) * 16 + j] = tb[i][e];
+          tiles[buf][wave][1][i][(4 * (lane >> 4) + e) * 16 + j] = tc[i][e];
         }
       __syncthreads();
+      const int64_t row = ((int64_t)in_group * a.tokens + t) * a.G + group;
 #pragma unroll
-      for (int at = threadIdx.x; at < 2 * NS * 256; at += THREADS) {
-        const int which = at / (NS * 256), i = at / 256 % NS, el = at % 256, n = (el & 15) + 16 * i;
-        const int t = t0 + q * 16 + (el >> 4);
+      for (int el = threadIdx.x; el < 2 * NS * 256; el += THREADS) {
+        const int which = el / (NS * 256), i = el / 256 % NS, tk = el / 16 % 16, n = el % 16 + 16 * i;
         float sum = 0.f;
 #pragma unroll
-        for (int wv = 0; wv < WV; ++wv) sum += s.tiles[buf][wv][which][i][el];
-        if (n < a.N && t < end)
-          (which ? w.dc : w.db)[(((int64_t)in_group * a.tokens + t) * a.G + ch.g) * a.N + n] = sum;
+        for (int wv = 0; wv < WV; ++wv) sum += tiles[buf][wv][which][i][el % 256];
+        if (n < a.N && t + tk < end) ((which ? w.dc : w.db) + row * a.N)[(uint32_t)(tk * a.G * a.N + n)] = sum;
       }
       buf ^= 1;
+      if ((q & 3) == 0 && q > 0) {
+        // every wave has read its last of this tile before the barrier above
+        tile.store(a, bc, t - kScanTile, end);
+        __syncthreads();
+      }
+      there = ch.active;
     }
   };
 
@@ -856,15 +920,16 @@ scan_backward(const ScanArgs a, const ScanGrads g, const ScanBwdBuffers w) {
     if (end > lo) {  // entered from an earlier slot
       load_state<NS>(w.hend, slot - 1, a, ch, h);
       leaving(n - 1, end);
-      range(lo, end < hi ? end : hi, h, gr);
+      range(lo, end < hi ? end : hi, groups_at(lo, n - 1, slot), h, gr);
     }
   }
+#pragma unroll
+  for (int i = 0; i < NS; ++i) h[i] = 0.f;
   for (; n < a.n_seqs; ++n) {
     const int start = uniform((int)seqs.start(n)), end = uniform((int)seqs.end(n));
     if (!own.last && start >= hi) break;
-    load_state<NS>(a.h0, n, a, ch, h);
     leaving(n, end);
-    if (start < end) range(start, end < hi ? end : hi, h, gr);
+    if (start < end) range(start, end < hi ? end : hi, groups_at(start, n, slot), h, gr);
     if (g.dh0) store_state<NS>(g.dh0, n, a, ch, gr);
   }
   store_state<NS>(w.da, slot, a, ch, dA);
@@ -926,8 +991,10 @@ scan_sum_channels(const float* __restrict__ db, const float* __restrict__ dc, in
 template <typename F>
 int launch_chain(const ScanArgs& a, F* hend, F* adj, const F* sum, const int* kind, hipStream_t st) {
   const int64_t dn = (int64_t)a.D * a.N;
-  return (int)launch_kernel(scan_chain, dim3((unsigned)ceil_div(dn, 64), adj ? 2 : 1), dim3(64 * kChainWaves), st, a.A,
-                            dn, a.N, a.D, (int)a.n_slots, hend, adj, sum, kind);
+  // loads ahead: four slots while a wave has no more, else sixteen
+  return (int)launch_kernel(a.n_slots <= 4 * kChainWaves ? scan_chain<4> : scan_chain<16>,
+                            dim3((unsigned)ceil_div(dn, 64), adj ? 2 : 1), dim3(64 * kChainWaves), st, a.A, dn, a.N,
+                            a.D, (int)a.n_slots, hend, adj, sum, kind);
 }
 
 template <typename T, int NS>
@@ -1000,22 +1067,25 @@ int backward_t(ScanArgs a, const ScanBwdPlan& p, const ScanGrads& g, void* ws, h
   a.slot = p.slot;
   a.n_slots = p.n_slots;
   float *hend = at(p.hend_off), *adj = at(p.adj_off), *sum = at(p.sum_off);
-  int* kind = (int*)(base + p.kind_off);
-  hipError_t e;
-  if (p.carry) {
+  int* kind = p.carry ? (int*)(base + p.kind_off) : nullptr;
+  const GroupStates groups{at(p.group_off), at(p.group_sum_off)};
+  if (a.tokens > 0) {
     a.blocks_per_group = (int)ceil_div(a.D / a.G, 16 * kScanWaves);
     const int err = dispatch_quads(sizeof(T) == 2, a.N, [&](auto t, auto ns) {
       typedef decltype(t) U;
-      return (int)launch_kernel(scan_backward_carry<U, ns.value>, work_grid(a), dim3(64 * kScanWaves), st, a,
-                                (const U*)g.dout, g.dht, hend, adj, sum, kind);
+      return (int)launch_kernel(scan_backward_states<U, ns.value>, work_grid(a), dim3(64 * kScanWaves), st, a,
+                                (const U*)g.dout, g.dht, hend, adj, sum, kind, groups);
     });
     if (err != 0) return err;
-    const int err2 = launch_chain(a, hend, adj, sum, kind, st);
-    if (err2 != 0) return err2;
+  }
+  if (p.carry) {
+    const int err = launch_chain(a, hend, adj, sum, kind, st);
+    if (err != 0) return err;
   }
   a.blocks_per_group = p.blocks_per_group;
-  const ScanBwdBuffers w{hend, adj, at(p.da_off), at(p.dskip_off), at(p.dbias_off), at(p.db_off), at(p.dc_off)};
-  e = launch_kernel(scan_backward<T, NS>, work_grid(a), dim3(64 * scan_bwd_waves(NS)), st, a, g, w);
+  const ScanBwdBuffers w{hend, adj, groups, at(p.da_off), at(p.dskip_off), at(p.dbias_off), at(p.db_off),
+                         at(p.dc_off)};
+  hipError_t e = launch_kernel(scan_backward<T, NS>, work_grid(a), dim3(64 * kScanBwdWaves), st, a, g, w);
   if (e != hipSuccess) return (int)e;
   const int64_t dn = (int64_t)a.D * a.N, cols = a.tokens * a.G * a.N;
   e = launch_kernel(scan_sum_slots, dim3((unsigned)ceil_div(dn + 2 * (int64_t)a.D, 64)), dim3(1024), st, w.da,
