@@ -199,9 +199,9 @@ struct NormArgs {
   float eps, q_scale;
 };
 
-// Workgroups of the backward pass over one of q and k; each leaves one row
-// of d floats of partial sums of the weight's gradient.
-constexpr int kNormParts = 1024;
+// Workgroups of the backward pass at most (a power of two); each leaves a row
+// of d floats of partial sums for each of the weights' gradients.
+constexpr int kNormParts = 256;
 
 int launch_norm_forward(int is_bf16, const NormArgs& a, void* qo, void* ko, void* stream);
 int launch_norm_backward(int is_bf16, const NormArgs& a, const void* dqo, const void* dko, void* dq, void* dk,

@@ -453,6 +453,8 @@ int check_norm(const kda_qk_norm_desc_t* d, NormSizes* s) {
   s->freq_bytes = (size_t)d->rot / 2 * 4;
   if (d->d % 2 != 0 || d->d > 512) return KDA_ERR_UNSUPPORTED;
   if (d->Hq > 65536 || d->Hk > 65536) return KDA_ERR_UNSUPPORTED;
+  // a wave takes up to 16 heads of a token at least; the kernels count waves in 32 bits
+  if ((double)d->n_tokens * (((double)d->Hq + d->Hk) / 16.0 + 3.0) > 2.0e9) return KDA_ERR_UNSUPPORTED;
   a.n_tokens = d->n_tokens;
   a.Hq = d->Hq;
   a.Hk = d->Hk;
