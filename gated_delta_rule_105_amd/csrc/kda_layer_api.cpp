@@ -112,6 +112,7 @@ int check_conv(const kda_conv_desc_t* d, ConvSizes* s) {
   if (st != KDA_OK) return st;
   if (d->width < 2 || d->width > 4) return KDA_ERR_UNSUPPORTED;
   if (d->D > (1 << 23)) return KDA_ERR_UNSUPPORTED;  // the grid's second dimension
+  if (s->t.n > (size_t)INT32_MAX - 4096) return KDA_ERR_UNSUPPORTED;  // tokens are counted in 32 bits, with a batch ahead
   // the final states add a workgroup per kConvWaves rows to the token tiles
   if (s->t.seqs * (W - 1) + s->t.n / kda::kConvBatch > (size_t)INT32_MAX - 4096) return KDA_ERR_UNSUPPORTED;
   a.n_seqs = (int)s->t.seqs;
@@ -160,6 +161,7 @@ int kda_short_conv_step(const kda_conv_desc_t* d, const void* x, const float* we
   const int st = check_conv(d, &s);
   if (st != KDA_OK) return st;
   if (d->T != 1 || d->n_seqs != 0) return KDA_ERR_INVALID_ARGUMENT;
+  if (s.t.n * (size_t)d->D > (size_t)INT32_MAX) return KDA_ERR_UNSUPPORTED;  // lanes are counted in 32 bits
   if (!x || !weight || !state || !y) return KDA_ERR_INVALID_ARGUMENT;
   Buffers b;
   b.input(x, s.x_bytes, s.esz);
@@ -362,6 +364,7 @@ int kda_selective_scan_step(const kda_scan_desc_t* d, const void* x, const void*
   const int st = check_scan(d, &s);
   if (st != KDA_OK) return st;
   if (d->T != 1 || d->n_seqs != 0) return KDA_ERR_INVALID_ARGUMENT;
+  if (s.t.n * (size_t)d->D * 16 > (size_t)INT32_MAX) return KDA_ERR_UNSUPPORTED;  // lanes are counted in 32 bits
   if (!x || !dt || !A || !Bm || !Cm || !state || !o) return KDA_ERR_INVALID_ARGUMENT;
   Buffers b;
   scan_inputs(&b, s, x, dt, A, Bm, Cm, skip, z, dt_bias);

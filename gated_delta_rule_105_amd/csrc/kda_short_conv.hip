@@ -12,8 +12,8 @@
 // A lane owns one vector of channels (16 bytes forward, 4 channels backward)
 // and walks a tile of tokens with the last W - 1 inputs in registers, so an
 // input is loaded once per tile and the window costs W - 1 extra rows a
-// tile.  Rows are loaded kConvBatch at a time before the first is used.
-// Every wave's token range is uniform: where its sequences begin and end is
+// tile.  Rows come kConvBatch at a time, the next batch's loads issued before
+// this one is used.  Every wave's token range is uniform: where its sequences begin and end is
 // scalar control flow.  A last vector that would pass the end of the row is
 // moved back to end with it; its channels overlap the neighbour's and both
 // write the same values (the step, which updates in place, stores the part
@@ -43,12 +43,12 @@ __device__ __forceinline__ void load_taps(const float* __restrict__ w, const flo
   }
 }
 
-// row r of the sequence [lo, hi) preceded by its initial state (r < 0: the state)
+// row r of a sequence that starts at token lo, preceded by its initial state (r < 0: the state)
 template <typename T, int V, int W>
 __device__ __forceinline__ void load_row(const T* __restrict__ x, int64_t ld, const T* __restrict__ init, int D, int s,
-                                         int64_t lo, int64_t r, int c, float (&v)[V]) {
+                                         int lo, int r, int c, float (&v)[V]) {
   if (r >= 0) {
-    load_vec<T, V>(x + (lo + r) * ld + c, v);
+    load_vec<T, V>(x + (int64_t)(lo + r) * ld + c, v);
   } else if (init) {
     load_vec<T, V>(init + ((int64_t)s * (W - 1) + (W - 1) + r) * D + c, v);
   } else {
@@ -56,6 +56,24 @@ __device__ __forceinline__ void load_row(const T* __restrict__ x, int64_t ld, co
     for (int i = 0; i < V; ++i) v[i] = 0.f;
   }
 }
+
+// Rows t .. t + kConvBatch - 1 of an array as they come from memory (row
+// `last` for those past it): one scalar address each, and the lane's offset.
+template <typename T, int V>
+struct Batch {
+  typename Pack<T, V>::type r[kConvBatch];
+  __device__ __forceinline__ void load(const T* __restrict__ x, int64_t ld, int c, int t, int last) {
+#pragma unroll
+    for (int k = 0; k < kConvBatch; ++k) {
+      const T* row = x + (int64_t)(t + k < last ? t + k : last) * ld;
+      r[k] = *(const typename Pack<T, V>::type*)((const char*)row + (uint32_t)c * (uint32_t)sizeof(T));
+    }
+  }
+  __device__ __forceinline__ float get(int k, int i) const {
+    if constexpr (V == 1) return Elem<T>::to_f32(r[k]);
+    else return Elem<T>::to_f32(r[k][i]);
+  }
+};
 
 template <typename T, int V, int W, bool SILU>
 __global__ void __launch_bounds__(256) conv_forward(const ConvArgs a, T* __restrict__ y, T* __restrict__ fin) {
@@ -70,79 +88,99 @@ __global__ void __launch_bounds__(256) conv_forward(const ConvArgs a, T* __restr
     const int64_t item = (blockIdx.x - a.n_part) * kConvWaves + wave;
     if (item >= (int64_t)a.n_seqs * (W - 1)) return;
     const int s = (int)(item / (W - 1)), p = (int)(item % (W - 1));
-    const int64_t lo = seqs.start(s), len = seqs.end(s) - lo;
+    const int lo = (int)seqs.start(s), len = (int)seqs.end(s) - lo;
     float v[V];
     load_row<T, V, W>(x, a.ld, init, a.D, s, lo, len - (W - 1) + p, c, v);
     store_vec<T, V>(fin + item * a.D + c, v);
     return;
   }
-  int64_t t = ((int64_t)blockIdx.x * kConvWaves + wave) * a.tile;
-  const int64_t t1 = t + a.tile < a.tokens ? t + a.tile : a.tokens;
-  if (t >= t1) return;
+  const int64_t begin = ((int64_t)blockIdx.x * kConvWaves + wave) * a.tile;
+  if (begin >= a.tokens) return;
+  int t = (int)begin;
+  const int t1 = (int)(begin + a.tile < a.tokens ? begin + a.tile : a.tokens);
   float taps[W][V], b[V];
   load_taps<V, W>(a.w, a.bias, c, taps, b);
-  int s = seqs.from(t + 1) - 1;  // the last sequence that starts at t or before
+  int s = uniform(seqs.from(begin + 1)) - 1;  // the last sequence that starts at t or before
   if (s < 0) s = 0;
   for (; s < a.n_seqs && t < t1; ++s) {
-    const int64_t lo = seqs.start(s), hi = seqs.end(s);
+    const int lo = uniform((int)seqs.start(s)), hi = uniform((int)seqs.end(s));
     if (hi <= t) continue;
     if (t < lo) t = lo;
-    const int64_t e = hi < t1 ? hi : t1;
+    const int e = hi < t1 ? hi : t1;
+    Batch<T, V> next;
+    next.load(x, a.ld, c, t, e - 1);
     float win[W - 1][V];
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) load_row<T, V, W>(x, a.ld, init, a.D, s, lo, t - lo - (W - 1) + j, c, win[j]);
-    while (t < e) {
-      float r[kConvBatch][V];
-#pragma unroll
-      for (int k = 0; k < kConvBatch; ++k) load_vec<T, V>(x + (t + k < e ? t + k : e - 1) * a.ld + c, r[k]);
+    for (; t < e; t += kConvBatch) {
+      const Batch<T, V> r = next;
+      if (t + kConvBatch < e) next.load(x, a.ld, c, t + kConvBatch, e - 1);
 #pragma unroll
       for (int k = 0; k < kConvBatch; ++k) {
         float u[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
+          const float v = r.get(k, i);
           u[i] = b[i];
 #pragma unroll
           for (int j = 0; j < W - 1; ++j) u[i] += taps[j][i] * win[j][i];
-          u[i] += taps[W - 1][i] * r[k][i];
+          u[i] += taps[W - 1][i] * v;
           if (SILU) u[i] *= sigmoid(u[i]);
 #pragma unroll
           for (int j = 0; j + 1 < W - 1; ++j) win[j][i] = win[j + 1][i];
-          win[W - 2][i] = r[k][i];
+          win[W - 2][i] = v;
         }
-        if (t + k < e) store_vec<T, V>(y + (t + k) * a.D + c, u);
+        if (t + k < e) store_vec<T, V>(y + (int64_t)(t + k) * a.D + c, u);
       }
-      t += kConvBatch;
     }
     t = e;
   }
 }
 
-// One token: a lane owns V channels of one sequence.
+// One token: a lane owns V channels of kStepSeqs sequences, n_far apart, so
+// that the taps are loaded once for all of them and the rows of all are under
+// way together.
+constexpr int kStepSeqs = 2;
 template <typename T, int V, int W, bool SILU>
 __global__ void __launch_bounds__(256) conv_step(const ConvArgs a, T* __restrict__ state, T* __restrict__ y,
-                                                 int n_vec) {
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t n = id / n_vec;
-  const int c = (int)(id - n * n_vec) * V;
-  if (n >= a.tokens) return;
+                                                 int n_vec, int n_far) {
+  const uint32_t id = blockIdx.x * 256u + threadIdx.x;
+  const int n0 = (int)(id / (uint32_t)n_vec);
+  const int c = (int)(id - (uint32_t)n0 * (uint32_t)n_vec) * V;
+  if (n0 >= n_far) return;
   const T* __restrict__ x = (const T*)a.x;
-  T* __restrict__ st = state + n * (W - 1) * a.D + c;
-  float taps[W][V], b[V], win[W][V];
+  typename Pack<T, V>::type rows[kStepSeqs][W];
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) load_vec<T, V>(st + (int64_t)j * a.D, win[j]);
-  load_vec<T, V>(x + n * a.ld + c, win[W - 1]);
-  load_taps<V, W>(a.w, a.bias, c, taps, b);
-  float u[V];
+  for (int q = 0; q < kStepSeqs; ++q) {
+    const int64_t n = n0 + q * n_far < a.tokens ? n0 + q * n_far : n0;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    u[i] = b[i];
-#pragma unroll
-    for (int j = 0; j < W; ++j) u[i] += taps[j][i] * win[j][i];
-    if (SILU) u[i] *= sigmoid(u[i]);
+    for (int j = 0; j < W - 1; ++j)
+      rows[q][j] = *(const typename Pack<T, V>::type*)(state + (n * (W - 1) + j) * a.D + c);
+    rows[q][W - 1] = *(const typename Pack<T, V>::type*)(x + n * a.ld + c);
   }
+  float taps[W][V], b[V];
+  load_taps<V, W>(a.w, a.bias, c, taps, b);
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) store_vec<T, V>(st + (int64_t)j * a.D, win[j + 1]);
-  store_vec<T, V>(y + n * a.D + c, u);
+  for (int q = 0; q < kStepSeqs; ++q) {
+    const int64_t n = n0 + q * n_far;
+    if (n >= a.tokens) break;
+    float u[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      u[i] = b[i];
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        if constexpr (V == 1) u[i] += taps[j][i] * Elem<T>::to_f32(rows[q][j]);
+        else u[i] += taps[j][i] * Elem<T>::to_f32(rows[q][j][i]);
+      }
+      if (SILU) u[i] *= sigmoid(u[i]);
+    }
+    // the inputs move up a row as they are
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j)
+      *(typename Pack<T, V>::type*)(state + (n * (W - 1) + j) * a.D + c) = rows[q][j + 1];
+    store_vec<T, V>(y + n * a.D + c, u);
+  }
 }
 
 // du from dy and the pre-activation
@@ -169,7 +207,7 @@ conv_backward(const ConvArgs a, const T* __restrict__ dy, const T* __restrict__ 
     const int64_t item = (blockIdx.x - a.n_part) * kConvWaves + wave;
     if (!active || item >= (int64_t)a.n_seqs * (W - 1)) return;
     const int s = (int)(item / (W - 1)), p = (int)(item % (W - 1));
-    const int64_t lo = seqs.start(s), len = seqs.end(s) - lo;
+    const int lo = (int)seqs.start(s), len = (int)seqs.end(s) - lo;
     load_taps<V, W>(a.w, a.bias, c, taps, b);
     float acc[V];
 #pragma unroll
@@ -188,7 +226,7 @@ conv_backward(const ConvArgs a, const T* __restrict__ dy, const T* __restrict__ 
 #pragma unroll
         for (int i = 0; i < V; ++i) u[i] += taps[m][i] * v[i];
       }
-      load_vec<T, V>(dy + (lo + p - j) * a.D + c, g);
+      load_vec<T, V>(dy + (int64_t)(lo + p - j) * a.D + c, g);
 #pragma unroll
       for (int i = 0; i < V; ++i) acc[i] += taps[j][i] * act_grad<SILU>(g[i], u[i]);
     }
@@ -202,18 +240,22 @@ conv_backward(const ConvArgs a, const T* __restrict__ dy, const T* __restrict__ 
 #pragma unroll
     for (int j = 0; j < W; ++j) dw[j][i] = 0.f;
   }
-  int64_t t = ((int64_t)blockIdx.x * kConvWaves + wave) * a.tile;
-  const int64_t t1 = t + a.tile < a.tokens ? t + a.tile : a.tokens;
-  if (active && t < t1) {
+  const int64_t begin = ((int64_t)blockIdx.x * kConvWaves + wave) * a.tile;
+  if (active && begin < a.tokens) {
+    int t = (int)begin;
+    const int t1 = (int)(begin + a.tile < a.tokens ? begin + a.tile : a.tokens);
     load_taps<V, W>(a.w, a.bias, c, taps, b);
-    int s = seqs.from(t + 1) - 1;
+    int s = uniform(seqs.from(begin + 1)) - 1;
     if (s < 0) s = 0;
     for (; s < a.n_seqs && t < t1; ++s) {
-      const int64_t lo = seqs.start(s), hi = seqs.end(s);
+      const int lo = uniform((int)seqs.start(s)), hi = uniform((int)seqs.end(s));
       if (hi <= t) continue;
       if (t < lo) t = lo;
       // tokens [t, e) of this sequence: their dx needs du up to W - 1 tokens further
-      const int64_t first = t, e = hi < t1 ? hi : t1, last = e + W - 1;
+      const int first = t, e = hi < t1 ? hi : t1, last = e + W - 1;
+      Batch<T, V> nx, ng;
+      nx.load(x, a.ld, c, t, hi - 1);
+      ng.load(dy, a.D, c, t, hi - 1);
       float win[W - 1][V], du[W - 1][V];
 #pragma unroll
       for (int j = 0; j < W - 1; ++j) {
@@ -221,31 +263,26 @@ conv_backward(const ConvArgs a, const T* __restrict__ dy, const T* __restrict__ 
 #pragma unroll
         for (int i = 0; i < V; ++i) du[j][i] = 0.f;
       }
-      for (; t < last; t += kConvBatch) {
-        float r[kConvBatch][V], g[kConvBatch][V];
+      // one batch; INSIDE: all of its tokens, and those whose dx they complete, are this wave's own
+      auto batch = [&](const Batch<T, V>& rx, const Batch<T, V>& rg, auto inside) {
+        constexpr bool INSIDE = decltype(inside)::value;
 #pragma unroll
         for (int k = 0; k < kConvBatch; ++k) {
-          const int64_t at = t + k < hi ? t + k : hi - 1;
-          load_vec<T, V>(x + at * a.ld + c, r[k]);
-          load_vec<T, V>(dy + at * a.D + c, g[k]);
-        }
-#pragma unroll
-        for (int k = 0; k < kConvBatch; ++k) {
-          const bool in_seq = t + k < hi, own = t + k < e;
+          const bool in_seq = INSIDE || t + k < hi, own = INSIDE || t + k < e;
           float out[V];
 #pragma unroll
           for (int i = 0; i < V; ++i) {
+            const float v = rx.get(k, i);
             float u = b[i];
 #pragma unroll
             for (int j = 0; j < W - 1; ++j) u += taps[j][i] * win[j][i];
-            u += taps[W - 1][i] * r[k][i];
-            const float d = in_seq ? act_grad<SILU>(g[k][i], u) : 0.f;
-            const float dm = own ? d : 0.f;
-            db[i] += dm;
+            u += taps[W - 1][i] * v;
+            const float d = in_seq ? act_grad<SILU>(rg.get(k, i), u) : 0.f;
             if (own) {
+              db[i] += d;
 #pragma unroll
-              for (int j = 0; j < W - 1; ++j) dw[j][i] += dm * win[j][i];
-              dw[W - 1][i] += dm * r[k][i];
+              for (int j = 0; j < W - 1; ++j) dw[j][i] += d * win[j][i];
+              dw[W - 1][i] += d * v;
             }
             // dx of token t + k - (W - 1)
             out[i] = taps[0][i] * d;
@@ -256,20 +293,31 @@ conv_backward(const ConvArgs a, const T* __restrict__ dy, const T* __restrict__ 
               win[j][i] = win[j + 1][i];
               du[j][i] = du[j + 1][i];
             }
-            win[W - 2][i] = r[k][i];
+            win[W - 2][i] = v;
             du[W - 2][i] = d;
           }
-          const int64_t at = t + k - (W - 1);
-          if (at >= first && at < e) {
-            if (dfin && at >= hi - (W - 1)) {
+          const int at = t + k - (W - 1);
+          if (INSIDE || (at >= first && at < e)) {
+            if (!INSIDE && dfin && at >= hi - (W - 1)) {
               float f[V];
               load_vec<T, V>(dfin + ((int64_t)s * (W - 1) + at - (hi - (W - 1))) * a.D + c, f);
 #pragma unroll
               for (int i = 0; i < V; ++i) out[i] += f[i];
             }
-            store_vec<T, V>(dx + at * a.D + c, out);
+            store_vec<T, V>((T*)((char*)(dx + (int64_t)at * a.D) + (uint32_t)c * (uint32_t)sizeof(T)), out);
           }
         }
+      };
+      for (; t < last; t += kConvBatch) {
+        const Batch<T, V> rx = nx, rg = ng;
+        if (t + kConvBatch < last) {
+          nx.load(x, a.ld, c, t + kConvBatch, hi - 1);
+          ng.load(dy, a.D, c, t + kConvBatch, hi - 1);
+        }
+        if (t - (W - 1) >= first && t + kConvBatch <= e)
+          batch(rx, rg, std::true_type{});
+        else
+          batch(rx, rg, std::false_type{});
       }
       t = e;
     }
@@ -325,8 +373,10 @@ int forward_t(const ConvArgs& a, void* y, void* fin, hipStream_t st) {
 template <typename T, int V, int W, bool SILU>
 int step_t(const ConvArgs& a, void* state, void* y, hipStream_t st) {
   const int n_vec = a.D / V;
-  const dim3 grid((unsigned)ceil_div(a.tokens * n_vec, 256));
-  return (int)launch_kernel(conv_step<T, V, W, SILU>, grid, dim3(256), st, a, (T*)state, (T*)y, n_vec);
+  const int64_t n_far = ceil_div(a.tokens, kStepSeqs), threads = ceil_div(n_far * n_vec, 256) * 256;
+  if (threads > INT32_MAX) return (int)hipErrorInvalidValue;
+  return (int)launch_kernel(conv_step<T, V, W, SILU>, dim3((unsigned)(threads / 256)), dim3(256), st, a, (T*)state,
+                            (T*)y, n_vec, (int)n_far);
 }
 template <typename T, int V, int W, bool SILU>
 int backward_t(const ConvArgs& a, const void* dy, const void* dfin, void* dx, float* dw, float* db, void* dinit,

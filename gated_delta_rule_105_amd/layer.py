@@ -44,13 +44,17 @@ def _code(dtype) -> int:
     raise TypeError(f"unsupported dtype {dtype}; the library takes bfloat16 or float32")
 
 
+def _elsewhere(name, t, dev):
+    return ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+
+
 def _like(name, t, dev, dtype, shape):
-    """Check an optional contiguous tensor; returns its address (None for None)."""
+    """Check an optional contiguous tensor on device number `dev`; returns its address (None for None)."""
     if t is None:
         return None
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, got {t.device}")
-    if t.dtype != dtype:
+    if t.get_device() != dev:
+        raise _elsewhere(name, t, dev)
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -63,9 +67,9 @@ def _rows(name, t, dev, dtype, shape, lead):
     """Check an input whose rows (the dims from `lead` on) are contiguous and a
     fixed distance apart; returns its address and that distance (0: none
     needed, the rows follow one another)."""
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, got {t.device}")
-    if t.dtype != dtype:
+    if t.get_device() != dev:
+        raise _elsewhere(name, t, dev)
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -92,9 +96,10 @@ def _rows(name, t, dev, dtype, shape, lead):
 
 
 def _device(t, name):
+    """The number of the device a call's tensors have to be on."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    return t.device
+    return t.get_device()
 
 
 def _sequences(cu_seqlens, B, T, dev, validate_cu):
@@ -128,23 +133,32 @@ class _On:
         self.contexts = ()
 
     def __enter__(self):
-        cuda = _torch().cuda
+        torch = _torch()
         if self.stream is not None:
-            self.contexts = (cuda.device(self.device),
-                             cuda.stream(cuda.ExternalStream(self.stream, device=self.device)))
-        elif cuda.current_device() != self.device.index:
-            self.contexts = (cuda.device(self.device),)
+            self.contexts = (torch.cuda.device(self.device),
+                             torch.cuda.stream(torch.cuda.ExternalStream(self.stream, device=self.device)))
+        elif torch._C._cuda_getDevice() != self.device:
+            self.contexts = (torch.cuda.device(self.device),)
         for c in self.contexts:
             c.__enter__()
-        return cuda.current_stream(self.device).cuda_stream if self.stream is None else self.stream
+        # the handle alone: torch.cuda.current_stream() would build a Stream around it on every call
+        return torch._C._cuda_getCurrentRawStream(self.device) if self.stream is None else self.stream
 
     def __exit__(self, *exc):
         for c in reversed(self.contexts):
             c.__exit__(*exc)
 
 
+def _new(t, like, name, dev, shape, dtype=None):
+    """A caller's output, checked, or a new one (in `like`'s dtype unless given); and its address."""
+    if t is None:
+        t = like.new_empty(shape) if dtype is None else like.new_empty(shape, dtype=dtype)
+        return t, t.data_ptr()
+    return t, _like(name, t, dev, like.dtype if dtype is None else dtype, shape)
+
+
 def _out(out, name, shape, dtype, dev):
-    """The caller's tensor under `name`, checked, or a new one; and its address."""
+    """The caller's tensor under `name`, checked, or a new one; its address."""
     t = out.get(name)
     if t is None:
         t = _torch().empty(shape, dtype=dtype, device=dev)
@@ -158,8 +172,8 @@ def _workspace(workspace, need, dev):
     torch = _torch()
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
@@ -196,12 +210,11 @@ def short_conv_forward(x, weight, bias=None, *, initial_state=None, cu_seqlens=N
     p0 = _like("initial_state", initial_state, dev, dt, (S, W - 1, D))
     desc = _conv_desc(x, weight, B, T, D, W, n_seqs, activation, ld)
     with _On(dev, stream) as st:
-        if y is None:
-            y = torch.empty((B, T, D), dtype=dt, device=dev)
-        if final_state is None and output_final_state:
-            final_state = torch.empty((S, W - 1, D), dtype=dt, device=dev)
-        layer_call("kda_short_conv_forward", desc, px, pw, pb, p0, cu, _like("y", y, dev, dt, (B, T, D)),
-                   _like("final_state", final_state, dev, dt, (S, W - 1, D)), st)
+        y, py = _new(y, x, "y", dev, (B, T, D))
+        pf = None
+        if final_state is not None or output_final_state:
+            final_state, pf = _new(final_state, x, "final_state", dev, (S, W - 1, D))
+        layer_call("kda_short_conv_forward", desc, px, pw, pb, p0, cu, py, pf, st)
     return y, final_state
 
 
@@ -217,12 +230,11 @@ def short_conv_step(x, weight, state, bias=None, *, activation="silu", y=None, s
     pb = _like("bias", bias, dev, torch.float32, (D,))
     ps = _like("state", state, dev, dt, (N, W - 1, D))
     if N == 0:
-        return torch.empty((0, D), dtype=dt, device=dev) if y is None else y
+        return x.new_empty((0, D)) if y is None else y
     desc = _conv_desc(x, weight, N, 1, D, W, 0, activation, ld)
     with _On(dev, stream) as st:
-        if y is None:
-            y = torch.empty((N, D), dtype=dt, device=dev)
-        layer_call("kda_short_conv_step", desc, px, pw, pb, ps, _like("y", y, dev, dt, (N, D)), st)
+        y, py = _new(y, x, "y", dev, (N, D))
+        layer_call("kda_short_conv_step", desc, px, pw, pb, ps, py, st)
     return y
 
 
@@ -308,13 +320,12 @@ def selective_scan_forward(x, dt, A, B, C, D=None, z=None, dt_bias=None, *, h0=N
     desc = ScanDesc(Bt, T, ch, N, G, n_seqs, _code(ty), dt_softplus, *lds)
     with _On(dev, stream) as st:
         need = layer_workspace_size("kda_selective_scan", desc)
-        if o is None:
-            o = torch.empty((Bt, T, ch), dtype=ty, device=dev)
-        if ht is None and output_final_state:
-            ht = torch.empty((S, ch, N), dtype=torch.float32, device=dev)
+        o, po = _new(o, x, "o", dev, (Bt, T, ch))
+        ph = None
+        if ht is not None or output_final_state:
+            ht, ph = _new(ht, x, "ht", dev, (S, ch, N), torch.float32)
         pws, ws_bytes, workspace = _workspace(workspace, need, dev) if need else (None, 0, None)
-        layer_call("kda_selective_scan_forward", desc, *ptrs, p0, cu, _like("o", o, dev, ty, (Bt, T, ch)),
-                   _like("ht", ht, dev, torch.float32, (S, ch, N)), pws, ws_bytes, st)
+        layer_call("kda_selective_scan_forward", desc, *ptrs, p0, cu, po, ph, pws, ws_bytes, st)
     return o, ht
 
 
@@ -328,12 +339,11 @@ def selective_scan_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, *, 
     S, ch = x.shape
     ps = _like("state", state, dev, torch.float32, (S, ch, N))
     if S == 0:
-        return torch.empty((0, ch), dtype=ty, device=dev) if o is None else o
+        return x.new_empty((0, ch)) if o is None else o
     desc = ScanDesc(S, 1, ch, N, G, 0, _code(ty), dt_softplus, *lds)
     with _On(dev, stream) as st:
-        if o is None:
-            o = torch.empty((S, ch), dtype=ty, device=dev)
-        layer_call("kda_selective_scan_step", desc, *ptrs, ps, _like("o", o, dev, ty, (S, ch)), st)
+        o, po = _new(o, x, "o", dev, (S, ch))
+        layer_call("kda_selective_scan_step", desc, *ptrs, ps, po, st)
     return o
 
 
@@ -421,15 +431,11 @@ def qk_norm_forward(q, k, q_weight=None, k_weight=None, positions=None, inv_freq
     first R channels are turned in pairs by positions * inv_freq; the pairs
     are channels (i, i + R / 2), or (2 i, 2 i + 1) when interleaved.  q_scale
     multiplies q's output.  Returns (q_out, k_out), contiguous."""
-    torch = _torch()
     dev, ty, desc, ptrs = _norm_inputs(q, k, q_weight, k_weight, positions, inv_freq, norm, eps, interleaved, q_scale)
     with _On(dev, stream) as st:
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=ty, device=dev)
-        if k_out is None:
-            k_out = torch.empty(k.shape, dtype=ty, device=dev)
-        layer_call("kda_qk_norm_forward", desc, *ptrs, _like("q_out", q_out, dev, ty, q.shape),
-                   _like("k_out", k_out, dev, ty, k.shape), st)
+        q_out, pq = _new(q_out, q, "q_out", dev, q.shape)
+        k_out, pk = _new(k_out, k, "k_out", dev, k.shape)
+        layer_call("kda_qk_norm_forward", desc, *ptrs, pq, pk, st)
     return q_out, k_out
 
 

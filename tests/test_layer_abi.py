@@ -125,7 +125,7 @@ def test_workspace_sizes():
     # a state of every slot, and its sum of delta
     st, n = size("kda_selective_scan", desc(ScanDesc, B=1, T=65536, D=64, G=1))
     assert st == KDA_OK and n % (64 * 17 * 4) % 256 == 0 and n >= 100 * 64 * 17 * 4
-    assert size("kda_qk_norm_backward", desc(NormDesc)) == (KDA_OK, 2 * 1024 * 128 * 4)
+    assert size("kda_qk_norm_backward", desc(NormDesc)) == (KDA_OK, 2 * 256 * 128 * 4)
 
 
 BAD_CONV = [(dict(B=0), INV), (dict(T=-1), INV), (dict(D=0), INV), (dict(width=0), INV), (dict(width=1), UNS),
