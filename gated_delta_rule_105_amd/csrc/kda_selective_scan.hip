@@ -16,13 +16,13 @@
 // and the sum's product.
 //
 // Layout of the forward scans ("quads").  A wave holds 16 channels, lane l
-// channel l % 16 and the quarter l / 16 of its states (NS of them), so four
-// lanes share a channel.  Tokens come in groups of 16; the four lanes of a
-// channel each prepare four of them (delta, delta x, the gate), which makes
-// that work once per token and channel, and exchange the results by swapping
-// rows of 16 lanes.  A token's sum over the states is the lane's own products
-// and a sum over the four quarters; those of four tokens are taken together
-// (three swaps, three additions) and come out in the lanes that prepared the
+// channel l / 4 and the quarter l % 4 of its states (NS of them), so four
+// neighbour lanes share a channel.  Tokens come in groups of 16; the four
+// lanes of a channel each prepare four of them (delta, delta x, the gate),
+// which makes that work once per token and channel, and read each other's
+// results as an operand modifier.  A token's sum over the states is the
+// lane's own products and a sum over the four quarters; those of four tokens
+// are taken together (fold_quad) and come out in the lanes that prepared the
 // tokens.
 // B and C of 64 tokens are staged in LDS as fp32, [token][state]; a lane
 // reads its quarter, the same address for all 16 channels.
@@ -205,29 +205,23 @@ struct Four {
   }
 };
 
-// v's row k of 16 lanes in every row, for k = 0 .. 3
-__device__ __forceinline__ void spread_rows(float v, float (&out)[4]) {
-  const uint32_t u = __builtin_bit_cast(uint32_t, v);
-  const auto odd = __builtin_amdgcn_permlane16_swap(u, u, false, false);  // rows (0, 0, 2, 2), (1, 1, 3, 3)
-  const auto a = __builtin_amdgcn_permlane32_swap(odd[0], odd[0], false, false);
-  const auto b = __builtin_amdgcn_permlane32_swap(odd[1], odd[1], false, false);
-  out[0] = __builtin_bit_cast(float, (uint32_t)a[0]);
-  out[1] = __builtin_bit_cast(float, (uint32_t)b[0]);
-  out[2] = __builtin_bit_cast(float, (uint32_t)a[1]);
-  out[3] = __builtin_bit_cast(float, (uint32_t)b[1]);
+// lane K's value in all four lanes of a quad
+template <int K>
+__device__ __forceinline__ float quad_bcast(float v) {
+  return dpp<K * 0x55>(v);
 }
-
-// Sums over the four rows of 16 lanes: row k of the result is the sum of
-// p[k]'s rows.  Each swap pairs two values' halves, so that one addition
-// serves both.
-__device__ __forceinline__ float sum_rows(const float (&p)[4]) {
-  auto fold = [](float x, float y, auto swap) {
-    const auto s = swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y));
-    return __builtin_bit_cast(float, (uint32_t)s[0]) + __builtin_bit_cast(float, (uint32_t)s[1]);
-  };
-  auto halves = [](uint32_t x, uint32_t y) { return __builtin_amdgcn_permlane32_swap(x, y, false, false); };
-  auto rows = [](uint32_t x, uint32_t y) { return __builtin_amdgcn_permlane16_swap(x, y, false, false); };
-  return fold(fold(p[0], p[2], halves), fold(p[1], p[3], halves), rows);
+// sum over the quad, in all four lanes
+__device__ __forceinline__ float quad_sum(float v) {
+  v += dpp<kPairSwap>(v);
+  return v + dpp<kQuadSwap>(v);
+}
+// Four sums over the quad, lane k's result that of p[k].  Each fold halves
+// the values a lane answers for and adds its neighbour's share of them.
+__device__ __forceinline__ float fold_quad(const float (&p)[4], int q) {
+  const bool odd = q & 1, upper = q & 2;
+  const float a = (odd ? p[1] : p[0]) + dpp<kPairSwap>(odd ? p[0] : p[1]);
+  const float b = (odd ? p[3] : p[2]) + dpp<kPairSwap>(odd ? p[2] : p[3]);
+  return (upper ? b : a) + dpp<kQuadSwap>(upper ? a : b);
 }
 
 template <int NS>
@@ -270,32 +264,30 @@ __device__ __forceinline__ float scan_group(const ScanArgs& a, const Channel& ch
       v = there ? v : 0.f;
     }
     sum += d;
-    float delta[4], dx[4], dy[4], part[4];
-    spread_rows(d, delta);
-    spread_rows(v, dx);
+    float g = 0.f, part[4];
     if (M == kAdjoint) {
       const float z = Elem<T>::to_f32(in.z_[m]), gate = z * sigmoid(z);
-      float g = Elem<T>::to_f32(in.g_[m]);
-      g *= a.has_z ? gate : 1.f;
-      spread_rows(there ? g : 0.f, dy);
+      g = Elem<T>::to_f32(in.g_[m]) * (a.has_z ? gate : 1.f);
+      g = there ? g : 0.f;
     }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    static_for<4>([&](auto lane) {
+      constexpr int k = decltype(lane)::value;
       float B[NS], C[NS];
       load_lds<NS>(s + (4 * m + k) * NP, B);
       if (M != kState) load_lds<NS>(s + c_off + (4 * m + k) * NP, C);
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
-        const float e = exp2_fast(delta[k] * r.A2[i]);
-        st.h[i] = e * st.h[i] + dx[k] * B[i];
+        const float e = exp2_fast(quad_bcast<k>(d) * r.A2[i]);
+        const float put = quad_bcast<k>(v) * B[i];
+        st.h[i] = __builtin_fmaf(e, st.h[i], put);
         if (M == kOutput) part[k] = i ? part[k] + C[i] * st.h[i] : C[i] * st.h[i];
         if (M == kAdjoint) {
           st.run[i] *= e;
-          st.adj[i] += st.run[i] * (C[i] * dy[k]);
+          st.adj[i] += st.run[i] * (quad_bcast<k>(g) * C[i]);
         }
       }
-    }
-    if (M == kOutput) y[m] = sum_rows(part);
+    });
+    if (M == kOutput) y[m] = fold_quad(part, q);
   }
   if (M == kOutput && ch.active) {
 #pragma unroll
@@ -322,7 +314,7 @@ template <int NS>
 __device__ __forceinline__ void keep_group(const ScanArgs& a, const Channel& ch, const GroupStates& k, int group,
                                            const float (&h)[NS], float sum) {
   store_state<NS>(k.h, group, a, ch, h);
-  const float total = sum_rows({sum, sum, sum, sum});
+  const float total = quad_sum(sum);
   if (ch.active && ch.first == 0) k.sum[(int64_t)group * a.D + ch.c] = total;
 }
 
@@ -381,8 +373,8 @@ struct QuadWork {
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     int block;
     if (!work_of(a, &slot, &block)) return false;
-    q = lane >> 4;
-    ch = channel_of(a, block, wave * 16 + (lane & 15), 16 * kScanWaves, q * NS, 1);
+    q = lane & 3;
+    ch = channel_of(a, block, wave * 16 + (lane >> 2), 16 * kScanWaves, q * NS, 1);
     r.load(a, ch);
     tok = slot_of(a, slot);
     const uint32_t e = (uint32_t)esz;
@@ -420,7 +412,7 @@ scan_forward(const ScanArgs a, float* __restrict__ hend, float* __restrict__ sum
     const float d = scan_range<T, NS, M>(a, w.ch, w.r, w.q, w.l, own ? start : lo, hi, s, st, (T*)nullptr,
                                          (const T*)nullptr);
     store_state<NS>(hend, w.slot, a, w.ch, st.h);
-    const float total = sum_rows({d, d, d, d});
+    const float total = quad_sum(d);
     if (!own && w.ch.active && w.q == 0) sum[(int64_t)w.slot * a.D + w.ch.c] = total;
     return;
   }
@@ -634,7 +626,7 @@ scan_backward_states(const ScanArgs a, const T* __restrict__ dout, const float* 
       for (int i = 0; i < NS; ++i) st.adj[i] += st.run[i] * last[i];
     } else {
       store_state<NS>(hend, w.slot, a, w.ch, st.h);
-      const float total = sum_rows({d, d, d, d});
+      const float total = quad_sum(d);
       if (w.ch.active && w.q == 0) sum[(int64_t)w.slot * a.D + w.ch.c] = total;
     }
     store_state<NS>(adj, w.slot, a, w.ch, st.adj);
@@ -660,10 +652,11 @@ scan_backward_states(const ScanArgs a, const T* __restrict__ dout, const float* 
 // lane k's, broadcast over the row as an operand modifier; the sums over the
 // states of a group's tokens are folded lane by lane (RowSums) as the tokens
 // come.  Sums over channels, of which the backward pass has two per element,
-// are those of the wave's 4 rows: v_mfma_f32_16x16x4f32 with ones in row k of
-// the left operand, zeros in the others, and the products of token k (dh
-// delta x, h dy) on the right, so that a group's 16 tokens accumulate into
-// one [16 tokens][16 states] tile beside the vector unit.  The tiles of the
+// begin with the wave's 4 rows: four tokens' values are added across the rows
+// by three swaps and three additions (fold_rows), which leaves token k's sum
+// in row k, so a group becomes one [16 tokens][16 states] tile in four
+// registers.  (v_mfma_f32_16x16x4f32 with a one-hot left operand does the
+// same, 32 cycles of the matrix pipe each, and was slower.)  The tiles of the
 // waves are added in LDS, those of the workgroups by a later launch.  B and C
 // of 64 tokens are staged as [state][token] with rows of 68 words: four
 // tokens are one 16-byte read, free of bank conflicts.
@@ -726,11 +719,17 @@ struct RowSums {
   }
 };
 
-// 1 in lane K of every row, 0 elsewhere, from the same for lane 0
-template <int K>
-__device__ __forceinline__ float one_at(float first) {
-  if constexpr (K == 0) return first;
-  else return dpp<0x120 + K>(first);  // rotates each row by K lanes
+// Sums over the wave's four rows of 16 lanes: row k of the result is the sum
+// of p[k]'s rows.  Each swap pairs two values' halves, so that one addition
+// serves both.
+__device__ __forceinline__ float fold_rows(const float (&p)[4]) {
+  auto fold = [](float x, float y, auto swap) {
+    const auto s = swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y));
+    return __builtin_bit_cast(float, (uint32_t)s[0]) + __builtin_bit_cast(float, (uint32_t)s[1]);
+  };
+  auto halves = [](uint32_t x, uint32_t y) { return __builtin_amdgcn_permlane32_swap(x, y, false, false); };
+  auto rows = [](uint32_t x, uint32_t y) { return __builtin_amdgcn_permlane16_swap(x, y, false, false); };
+  return fold(fold(p[0], p[2], halves), fold(p[1], p[3], halves), rows);
 }
 
 // What the backward scan reads and writes beside the inputs.
@@ -793,7 +792,6 @@ scan_backward(const ScanArgs a, const ScanGrads g, const ScanBwdBuffers w) {
   const int lo = own.lo, hi = own.hi;
   const T* __restrict__ dout = (const T*)g.dout;
   const LaneOffsets l = lane_offsets(a, j, ch.c, sizeof(T));
-  const float first_one = j == 0 ? 1.f : 0.f;
   float dA[NS], dskip = 0.f, dbias = 0.f;
 #pragma unroll
   for (int i = 0; i < NS; ++i) dA[i] = 0.f;
@@ -855,9 +853,7 @@ scan_backward(const ScanArgs a, const ScanGrads g, const ScanBwdBuffers w) {
       const float dz = dout_j * y * (sg * (1.f + z * (1.f - sg)));
       float dy = dout_j * (a.has_z ? z * sg : 1.f);
       dy = there ? dy : 0.f;
-      f32x4 tb[NS], tc[NS];
-#pragma unroll
-      for (int i = 0; i < NS; ++i) tb[i] = tc[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
+      float tb[NS][4], tc[NS][4];  // dB and dC of tokens 4 e + row
       RowSums s1, s2;
       // other registers to the compiler, which would else keep the 32 values
       // broadcast above for the loop below
@@ -871,16 +867,16 @@ scan_backward(const ScanArgs a, const ScanGrads g, const ScanBwdBuffers w) {
           B[i] = *(const f32x4*)(sb + i * 16 * kColLd + 4 * k4);
           C[i] = *(const f32x4*)(sc + i * 16 * kColLd + 4 * k4);
         }
+        float vb[NS][4], vc[NS][4];
         static_for<4>([&](auto er) {
           constexpr int e = 3 - decltype(er)::value, k = 4 * k4 + e;
           const float dk = row_bcast<k>(delta_b), gk = row_bcast<k>(dy), xk = row_bcast<k>(dx_b);
-          const float one = one_at<k>(first_one);
           float p1 = 0.f, p2 = 0.f;
 #pragma unroll
           for (int i = 0; i < NS; ++i) {
             const float dh = __builtin_fmaf(gk, C[i][e], gr[i]);
-            tc[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(one, gk * hh[k][i], tc[i], 0, 0, 0);
-            tb[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(one, xk * dh, tb[i], 0, 0, 0);
+            vc[i][e] = gk * hh[k][i];
+            vb[i][e] = xk * dh;
             gr[i] = dh * dd[k][i];
             const float m = gr[i] * (k ? hh[k ? k - 1 : 0][i] : first[i]);
             p1 = i ? p1 + m * r.A2[i] : m * r.A2[i];
@@ -892,6 +888,11 @@ scan_backward(const ScanArgs a, const ScanGrads g, const ScanBwdBuffers w) {
           s1.template done<k, true>(j);
           s2.template done<k, true>(j);
         });
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+          tb[i][k4] = fold_rows(vb[i]);
+          tc[i][k4] = fold_rows(vc[i]);
+        }
         __builtin_amdgcn_sched_barrier(0);
       });
       const float slope = a.softplus ? sigmoid(v) : 1.f;
@@ -909,8 +910,8 @@ scan_backward(const ScanArgs a, const ScanGrads g, const ScanBwdBuffers w) {
       for (int i = 0; i < NS; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          tiles[buf][wave][0][i][(4 * (lane >> 4) + e) * 16 + j] = tb[i][e];
-          tiles[buf][wave][1][i][(4 * (lane >> 4) + e) * 16 + j] = tc[i][e];
+          tiles[buf][wave][0][i][(4 * e + (lane >> 4)) * 16 + j] = tb[i][e];
+          tiles[buf][wave][1][i][(4 * e + (lane >> 4)) * 16 + j] = tc[i][e];
         }
       __syncthreads();
       const int64_t row = ((int64_t)in_group * a.tokens + t) * a.G + group;

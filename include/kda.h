@@ -527,10 +527,9 @@ int kda_selective_scan_step(const kda_scan_desc_t* d, const void* x, const void*
  *   dskip, ddt_bias: [D] fp32 or NULL (not written)
  *   dz      : [B, T, D] dtype; required with z, ignored without
  *   dh0     : [S, D, N] fp32 or NULL (not written)
- * The workspace holds partial sums and the states between ranges of tokens.
- * Outputs must not overlap each other, the inputs or the workspace.  A NaN
- * or Inf may reach dB and dC of up to 15 tokens before its own, in the same
- * sequence (their sums over channels are matrix products over 16 tokens).
+ * The workspace holds the state before every 16 tokens (N / 4 bytes per token
+ * and channel), the states between ranges of tokens, and partial sums.
+ * Outputs must not overlap each other, the inputs or the workspace.
  */
 int kda_selective_scan_backward_workspace_size(const kda_scan_desc_t* d, size_t* bytes);
 int kda_selective_scan_backward(const kda_scan_desc_t* d, const void* x, const void* dt, const float* A,

@@ -179,9 +179,8 @@ def test_nan_stays_in_its_sequence_and_channel():
         other = torch.ones(g[key].shape, dtype=torch.bool, device="cuda")
         other[0, 50:350, 7] = False
         assert torch.equal(g2[key][other], g[key][other]), key
-    # tokens of the group of 16 that holds token 200, and earlier ones of its sequence, aside
     for key in ("dB", "dC"):
-        assert torch.equal(g2[key][0, :185], g[key][0, :185]) and torch.equal(g2[key][0, 350:], g[key][0, 350:]), key
+        assert torch.equal(g2[key][0, :200], g[key][0, :200]) and torch.equal(g2[key][0, 350:], g[key][0, 350:]), key
 
 
 def test_slots_do_not_matter():
