@@ -138,8 +138,9 @@ __device__ __forceinline__ float delta_of(const ScanArgs& a, float v) {
 
 // Tiles of B and C: TOK tokens from t0 of group g as [token][NP states],
 // zero past the range's end and past N.  A thread holds element
-// threadIdx.x + k THREADS of the tile.
-template <typename T, int NP, int TOK, int THREADS>
+// threadIdx.x + k THREADS of the tile.  A scan of the state alone has no use
+// for C.
+template <typename T, int NP, int TOK, int THREADS, bool WITH_C>
 struct TileRows {
   static constexpr int PER = TOK * NP / THREADS;
   T b[PER], c[PER];
@@ -151,7 +152,7 @@ struct TileRows {
       const int64_t tok = t < end ? t : end - 1;
       const int at = g * a.N + (n < a.N ? n : a.N - 1);
       b[k] = ((const T*)a.Bm)[tok * a.ld_b + at];
-      c[k] = ((const T*)a.Cm)[tok * a.ld_c + at];
+      if (WITH_C) c[k] = ((const T*)a.Cm)[tok * a.ld_c + at];
     }
   }
   __device__ __forceinline__ void store(const ScanArgs& a, float* s, int t0, int end) const {
@@ -160,7 +161,7 @@ struct TileRows {
       const int el = threadIdx.x + k * THREADS;
       const bool there = el % NP < a.N && t0 + el / NP < end;
       s[el] = there ? Elem<T>::to_f32(b[k]) : 0.f;
-      s[TOK * NP + el] = there ? Elem<T>::to_f32(c[k]) : 0.f;
+      if (WITH_C) s[TOK * NP + el] = there ? Elem<T>::to_f32(c[k]) : 0.f;
     }
   }
 };
@@ -326,7 +327,7 @@ __device__ __forceinline__ float scan_range(const ScanArgs& a, const Channel& ch
                                             T* __restrict__ o, const T* __restrict__ dout, GroupStates keep = {},
                                             int group = 0) {
   constexpr int THREADS = 64 * kScanWaves, NP = 4 * NS, C_OFF = kScanTile * NP, BUF = 2 * C_OFF;
-  TileRows<T, NP, kScanTile, THREADS> tile;
+  TileRows<T, NP, kScanTile, THREADS, M != kState> tile;
   Four<T, M> next;
   float sum = 0.f;
   if (t0 + 16 <= end) next.load(a, dout, l, t0);

@@ -76,6 +76,13 @@ def _rows(name, t, dev, dtype, shape, lead):
     if t.is_contiguous():
         return t.data_ptr(), 0
     size, stride = t.shape, t.stride()
+    # the usual slice, [B, T, row] or [N, row] with rows of one or two dims, without the loops
+    inner = len(size) - lead
+    if stride[-1] == 1 and (inner == 1 or (inner == 2 and stride[-2] == size[-1])) and lead <= 2:
+        row = size[-1] if inner == 1 else size[-1] * size[-2]
+        ld = stride[lead - 1]
+        if ld >= row and size[lead - 1] > 1 and (lead == 1 or size[0] == 1 or stride[0] == ld * size[1]):
+            return t.data_ptr(), ld
     row = 1
     for i in range(t.dim() - 1, lead - 1, -1):
         if size[i] != 1 and stride[i] != row:
