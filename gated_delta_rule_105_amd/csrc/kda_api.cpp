@@ -11,8 +11,8 @@
 
 #include <math.h>
 #include <stdint.h>
+#include <string.h>
 
-#include "kda_check.h"
 #include "kda_launch.h"
 
 static_assert(KDA_NOALLOC_SCRATCH_BYTES == kda::kScratchBytes, "scratch size of the header and the library agree");
@@ -23,7 +23,40 @@ static_assert(KDA_GATE_CHANNEL == kda::kGateChannel && KDA_GATE_HEAD == kda::kGa
 
 namespace {
 
+constexpr size_t kAlign = 16;
+constexpr size_t kWsAlign = 256;
+
+bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+struct Range {
+  uintptr_t lo, hi;  // [lo, hi)
+};
+Range range(const void* p, size_t bytes) { return Range{(uintptr_t)p, (uintptr_t)p + bytes}; }
+bool overlap(Range a, Range b) {
+  if (a.lo == a.hi || b.lo == b.hi || a.lo == 0 || b.lo == 0) return false;
+  return a.lo < b.hi && b.lo < a.hi;
+}
+
+// Multiply non-negative sizes, flagging overflow of size_t.
+bool mul(size_t a, size_t b, size_t* out) {
+  if (a != 0 && b > SIZE_MAX / a) return false;
+  *out = a * b;
+  return true;
+}
+
+// Enum-typed arguments as their int representation: a C caller may store any
+// int in them, and loading a value outside the enumerators through the enum
+// type is undefined in C++, so they are only ever read this way.
+template <typename E>
+int as_int(const E& e) {
+  static_assert(sizeof(E) == sizeof(int), "C enums are int-sized here");
+  int v;
+  memcpy(&v, &e, sizeof v);
+  return v;
+}
 int dtype_of(const kda_chunk_desc_t* d) { return as_int(d->dtype); }
+
+size_t elem_size(int t) { return t == KDA_DTYPE_BF16 ? 2 : 4; }
 
 struct Sizes {
   size_t tokens;      // B * T

@@ -1,5 +1,5 @@
-// Host-side argument checks shared by the C front ends (kda_api.cpp and
-// kda_layer_api.cpp).  Plain C++, internal linkage.
+// Host-side argument checks of the C front end kda_layer_api.cpp (the same
+// rules as kda_api.cpp's own).  Plain C++, internal linkage.
 #pragma once
 
 #include "kda.h"
@@ -9,7 +9,6 @@
 
 namespace {
 
-constexpr size_t kAlign = 16;
 constexpr size_t kWsAlign = 256;
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
