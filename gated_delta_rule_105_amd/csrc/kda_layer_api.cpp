@@ -274,7 +274,8 @@ int check_scan(const kda_scan_desc_t* d, ScanSizes* s) {
   if (groups * (ceil((double)n / 64.0) + (double)s->t.seqs + 8.0) > 2.0e9) return KDA_ERR_UNSUPPORTED;
   // the kernels count tokens in 32 bits and look a tile ahead; a lane's offset inside 16 rows has 32 bits
   if (n > (size_t)INT32_MAX - 4096) return KDA_ERR_UNSUPPORTED;
-  for (int64_t ld : {a.ld_x, a.ld_dt, a.ld_z, (int64_t)d->D})
+  const int64_t rows[] = {a.ld_x, a.ld_dt, a.ld_z, (int64_t)d->D};
+  for (int64_t ld : rows)
     if (ld > (1 << 24)) return KDA_ERR_UNSUPPORTED;
   if ((int64_t)d->D * d->N > (1 << 28)) return KDA_ERR_UNSUPPORTED;  // likewise inside a row of states
   a.n_seqs = (int)s->t.seqs;
