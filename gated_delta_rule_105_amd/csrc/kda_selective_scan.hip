@@ -126,6 +126,11 @@ __device__ __forceinline__ void store_state(float* __restrict__ p, int64_t row, 
   }
 }
 
+// A decay over many tokens times what it carries.  With a growing state
+// (delta A > 0) the decay of a whole range can pass fp32 while the tokens that
+// make it would, one by one, have left a zero a zero.
+__device__ __forceinline__ float carried(float decay, float v) { return v != 0.f ? decay * v : 0.f; }
+
 __device__ __forceinline__ float delta_of(const ScanArgs& a, float v) {
   const float sp = softplus(v);
   return a.softplus ? sp : v;
@@ -284,7 +289,7 @@ __device__ __forceinline__ float scan_group(const ScanArgs& a, const Channel& ch
         if (M == kOutput) part[k] = i ? part[k] + C[i] * st.h[i] : C[i] * st.h[i];
         if (M == kAdjoint) {
           st.run[i] *= e;
-          st.adj[i] += st.run[i] * (quad_bcast<k>(g) * C[i]);
+          st.adj[i] += carried(st.run[i], quad_bcast<k>(g) * C[i]);
         }
       }
     });
@@ -482,7 +487,7 @@ scan_chain(const float* __restrict__ A, int64_t dn, int N, int D, int n_slots, f
         // what the slot holds counts only where a sequence leaves it (back: enters it)
         const bool passed = kd[k] & kPassed, holds = back ? kd[k] & kEntered : kd[k] & (kStarted | kPassed);
         const float e = passed ? exp2_fast(s[k] * A2) : 0.f;
-        h = (passed ? e * h : 0.f) + (holds ? x[k] : 0.f);
+        h = (passed ? carried(e, h) : 0.f) + (holds ? x[k] : 0.f);
         d = passed ? e * d : 0.f;
         unbroken = passed ? unbroken : 0;
         if (write && there) v[(int64_t)(back ? n_slots - 1 - i0 - k : i0 + k) * dn + el] = h;
@@ -496,7 +501,7 @@ scan_chain(const float* __restrict__ A, int64_t dn, int N, int D, int n_slots, f
   through[wave] = unbroken;
   __syncthreads();
   h = 0.f;
-  for (int w = 0; w < wave; ++w) h = (through[w] ? decay[w][lane] * h : 0.f) + state[w][lane];
+  for (int w = 0; w < wave; ++w) h = (through[w] ? carried(decay[w][lane], h) : 0.f) + state[w][lane];
   walk(d, h, true);
 }
 
@@ -624,11 +629,17 @@ scan_backward_states(const ScanArgs a, const T* __restrict__ dout, const float* 
       float last[NS];
       load_state<NS>(dht, n - 1, a, w.ch, last);
 #pragma unroll
-      for (int i = 0; i < NS; ++i) st.adj[i] += st.run[i] * last[i];
+      for (int i = 0; i < NS; ++i) st.adj[i] += carried(st.run[i], last[i]);
     } else {
       store_state<NS>(hend, w.slot, a, w.ch, st.h);
       const float total = quad_sum(d);
       if (w.ch.active && w.q == 0) sum[(int64_t)w.slot * a.D + w.ch.c] = total;
+    }
+    const float all = quad_sum(d);
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {  // a NaN decay reaches back through any gradient
+      const float e = exp2_fast(all * w.r.A2[i]);
+      st.adj[i] = e != e ? e : st.adj[i];
     }
     store_state<NS>(adj, w.slot, a, w.ch, st.adj);
   }
@@ -825,7 +836,7 @@ scan_backward(const ScanArgs a, const ScanGrads g, const ScanBwdBuffers w) {
       const float dx = there ? delta * x : 0.f;
       float first[NS], hh[16][NS], dd[16][NS];
 #pragma unroll
-      for (int i = 0; i < NS; ++i) first[i] = cur.h_[i] + exp2_fast(cur.sum_ * r.A2[i]) * h[i];
+      for (int i = 0; i < NS; ++i) first[i] = cur.h_[i] + carried(exp2_fast(cur.sum_ * r.A2[i]), h[i]);
       RowSums ys;
       static_for<4>([&](auto k4) {
         f32x4 B[NS], C[NS];

@@ -160,6 +160,50 @@ def test_extreme_rates_and_steps():
     check("ht", ht, rht, mht, n)
 
 
+@pytest.mark.parametrize("lengths", [None, [3, 600, 0, 37]])
+def test_growing_states(lengths):
+    """Rates above zero: a state that nothing has entered yet, and a gradient
+    that nothing follows, stay zero however far the ranges between grow.  A
+    step multiplies by e^3.2, whose argument's 4 roundings weigh 3.2 each: 20
+    roundings a step at most, twice that with the gradient, over 16 tokens."""
+    p, q, u, _ = inputs(1, 640, 16, 16, "f32", lengths=lengths, softplus=False, bias=False, state=False, seed=9)
+    note(f"selective_scan growing states {lengths}")
+    p["dt"].fill_(0.8)
+    p["A"][:, ::2] = 4.0
+    lo, hi = (0, 640) if lengths is None else (3, 603)
+    p["x"][:, : hi - 16] = 0.0
+    p["x"][:, hi:] = 0.0
+    u["do"][:, :lo] = 0.0
+    u["do"][:, lo + 16:] = 0.0
+    o, ht = kda.selective_scan_forward(**p, **q, dt_softplus=False)
+    g = kda.selective_scan_backward(**p, **q, **u, dt_softplus=False,
+                                    out=dict(dh0=torch.empty(ht.shape, device="cuda")))
+    torch.cuda.synchronize()
+    ro, rht, mo, mht = ref.scan(**p, cu=q["cu_seqlens"], softplus=False)
+    check("o", o, ro, mo, 64 + 20 * 16)
+    check("ht", ht, rht, mht, 64 + 20 * 16)
+    zeros = torch.zeros(ht.shape, device="cuda")
+    rg, rm = ref.scan_grad(**p, **u, h0=zeros, cu=q["cu_seqlens"], softplus=False)
+    for key in ("dx", "ddt", "dA", "dB", "dC", "dD", "dz", "dh0"):
+        assert torch.isfinite(g[key]).all(), key
+        check(key, g[key], rg[key], rm[key], 128 + 40 * 16 + 640)
+
+
+def test_nan_step_reaches_back():
+    """A NaN step size makes NaN of every earlier gradient of its channel's state, whatever follows it."""
+    p, q, u, _ = inputs(1, 700, 8, 4, "f32", seed=10)
+    note("selective_scan nan step")
+    p["dt"][0, 650, 3] = float("nan")
+    u["do"][0, 640:] = 0.0
+    u["dht"].zero_()
+    g = kda.selective_scan_backward(**p, **q, **u)
+    torch.cuda.synchronize()
+    hit = torch.zeros(8, dtype=torch.bool, device="cuda")
+    hit[3] = True
+    assert torch.isnan(g["dh0"][0][hit]).all() and torch.isfinite(g["dh0"][0][~hit]).all()
+    assert torch.isnan(g["dx"][0, :651, hit]).all() and torch.isfinite(g["dx"][0][:, ~hit]).all()
+
+
 def test_nan_stays_in_its_sequence_and_channel():
     p, q, u, _ = inputs(1, 0, 20, 16, "f32", lengths=[50, 300, 40], seed=5)
     note("selective_scan nan")
