@@ -44,6 +44,13 @@ def _code(dtype) -> int:
     raise TypeError(f"unsupported dtype {dtype}; the library takes bfloat16 or float32")
 
 
+def _ints(*lengths):
+    """`lengths`, which the descriptors hold in 32 bits (ctypes would wrap longer ones)."""
+    if max(lengths) > 0x7fffffff:
+        raise ValueError(f"lengths are limited to 2^31 - 1, got {max(lengths)}")
+    return lengths
+
+
 def _elsewhere(name, t, dev):
     return ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
 
@@ -192,7 +199,7 @@ def _activation(name):
 
 
 def _conv_desc(x, weight, B, T, D, W, n_seqs, activation, ld):
-    return ConvDesc(B, T, D, W, n_seqs, _code(x.dtype), _activation(activation), ld)
+    return ConvDesc(*_ints(B, T, D, W, n_seqs), _code(x.dtype), _activation(activation), ld)
 
 
 def short_conv_forward(x, weight, bias=None, *, initial_state=None, cu_seqlens=None, activation="silu", y=None,
@@ -302,7 +309,7 @@ def _scan_inputs(x, dt, A, B, C, D, z, dt_bias, lead):
 
 def selective_scan_workspace_bytes(B: int, T: int, D: int, N: int, dtype, G: int = 1, n_seqs: int = 0) -> int:
     """Device workspace one selective_scan_forward call of this shape needs."""
-    return layer_workspace_size("kda_selective_scan", ScanDesc(B, T, D, N, G, n_seqs, _code(dtype), 1))
+    return layer_workspace_size("kda_selective_scan", ScanDesc(*_ints(B, T, D, N, G, n_seqs), _code(dtype), 1))
 
 
 def selective_scan_forward(x, dt, A, B, C, D=None, z=None, dt_bias=None, *, h0=None, cu_seqlens=None,
@@ -324,7 +331,7 @@ def selective_scan_forward(x, dt, A, B, C, D=None, z=None, dt_bias=None, *, h0=N
     Bt, T, ch = x.shape
     n_seqs, S, cu = _sequences(cu_seqlens, Bt, T, dev, validate_cu)
     p0 = _like("h0", h0, dev, torch.float32, (S, ch, N))
-    desc = ScanDesc(Bt, T, ch, N, G, n_seqs, _code(ty), dt_softplus, *lds)
+    desc = ScanDesc(*_ints(Bt, T, ch, N, G, n_seqs), _code(ty), dt_softplus, *lds)
     with _On(dev, stream) as st:
         need = layer_workspace_size("kda_selective_scan", desc)
         o, po = _new(o, x, "o", dev, (Bt, T, ch))
@@ -347,7 +354,7 @@ def selective_scan_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, *, 
     ps = _like("state", state, dev, torch.float32, (S, ch, N))
     if S == 0:
         return x.new_empty((0, ch)) if o is None else o
-    desc = ScanDesc(S, 1, ch, N, G, 0, _code(ty), dt_softplus, *lds)
+    desc = ScanDesc(*_ints(S, 1, ch, N, G, 0), _code(ty), dt_softplus, *lds)
     with _On(dev, stream) as st:
         o, po = _new(o, x, "o", dev, (S, ch))
         layer_call("kda_selective_scan_step", desc, *ptrs, ps, po, st)
@@ -370,7 +377,7 @@ def selective_scan_backward(x, dt, A, B, C, do, D=None, z=None, dt_bias=None, *,
     p0 = _like("h0", h0, dev, f32, (S, ch, N))
     pdo = _like("do", do, dev, ty, (Bt, T, ch))
     pdht = _like("dht", dht, dev, f32, (S, ch, N))
-    desc = ScanDesc(Bt, T, ch, N, G, n_seqs, _code(ty), dt_softplus, *lds)
+    desc = ScanDesc(*_ints(Bt, T, ch, N, G, n_seqs), _code(ty), dt_softplus, *lds)
     need = layer_workspace_size("kda_selective_scan_backward", desc)
     out = dict(out or {})
     with _On(dev, stream) as st:
@@ -420,7 +427,7 @@ def _norm_inputs(q, k, q_weight, k_weight, positions, inv_freq, norm, eps, inter
     tokens = 1
     for s in rows:
         tokens *= s
-    desc = NormDesc(tokens, Hq, Hk, d, rot, _code(ty), _NORMS[norm], interleaved, eps, q_scale, ld_q, ld_k)
+    desc = NormDesc(*_ints(tokens, Hq, Hk, d, rot), _code(ty), _NORMS[norm], interleaved, eps, q_scale, ld_q, ld_k)
     return dev, ty, desc, (pq, pk, _like("q_weight", q_weight, dev, f32, (d,)),
                            _like("k_weight", k_weight, dev, f32, (d,)), pp, pf)
 

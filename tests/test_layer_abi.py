@@ -187,3 +187,14 @@ def test_binding_refuses_host_tensors():
         kda.selective_scan_forward(x, x, torch.zeros(8, 2), torch.zeros(1, 4, 1, 2), torch.zeros(1, 4, 1, 2))
     with pytest.raises(ValueError, match="device tensor"):
         kda.qk_norm_forward(x.view(1, 4, 1, 8), x.view(1, 4, 1, 8))
+
+
+def test_binding_refuses_lengths_past_32_bits():
+    """The descriptors' lengths are 32-bit; a longer one would wrap to a short call."""
+    torch = pytest.importorskip("torch")
+    import gated_delta_rule_105_amd as kda
+    with pytest.raises(ValueError, match="2\\^31"):
+        kda.selective_scan_workspace_bytes(1, 2 ** 32 + 64, 64, 16, torch.bfloat16)
+    meta = torch.empty(1, 2 ** 32 + 5, 1, device="meta")
+    with pytest.raises(ValueError, match="2\\^31"):
+        kda.layer._conv_desc(meta, None, 1, meta.shape[1], 1, 4, 0, "silu", 0)
