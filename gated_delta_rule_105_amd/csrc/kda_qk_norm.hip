@@ -19,13 +19,22 @@
 // fp32 would lose the angle of a far position (2^-24 of a million is 0.06
 // revolutions).  Heads are loaded kNormBatch groups at a time before the
 // first is used.
+//
+// Measured: unit vectors of 4096 tokens, 16 + 16 heads of 128, bf16, 12.8 us
+// (67.1 MB, 5.2 TB/s); 8192 tokens of 32 + 8 heads of 128, half rotated, 31 us
+// (167.8 MB, 5.4 TB/s; a large copy reaches 4.9 beyond the last-level cache);
+// 8 tokens 4.8 us, which is the launch and one token's chain of loads, angles
+// and sums; backward 8192 tokens of 16 + 4 heads of 64, fp32, 31.8 us and 4
+// for the weights' sums (125.8 MB).
 #include "kda_layer_device.h"
 
 namespace kda {
 
 namespace {
 
-constexpr int kNormBatch = 4;  // groups of heads (forward; half backward) a wave loads at a time
+// groups of heads (forward; half backward) a wave loads at a time: rotated
+// forward 33.0 us with 4, 34.9 with 2, 38.3 with 8 (registers)
+constexpr int kNormBatch = 4;
 
 // PV pairs (a, b) in each of NC chunks, LPH lanes apart.
 template <int PV, int NC>
@@ -352,7 +361,9 @@ norm_params(const float* __restrict__ part, int n_part, int d, float* __restrict
   out[c] = v;
 }
 
-// Groups of heads a wave takes of a token: up to 16, while `waves` waves are left.
+// Groups of heads a wave takes of a token: up to 16 (its angles serve them
+// all: rotated forward 33.0 us with 16, 38.9 with 8, 41.1 with 4), while
+// `waves` waves are left.
 inline int norm_steps(int n_tokens, int groups, int64_t waves) {
   int steps = groups < 16 ? groups : 16;
   while (steps > 1 && n_tokens * ceil_div(groups, steps) < waves) steps = (steps + 1) / 2;
