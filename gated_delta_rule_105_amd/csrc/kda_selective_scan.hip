@@ -17,11 +17,11 @@
 // two to four of the others.
 //
 // Measured in bf16 at 16 states.  1 x 4096 tokens of 4096 channels: 135 us,
-// of which the states of the slots 60, the chain 8 and the outputs 70 to 85;
+// of which the states of the slots 50 to 60, the chain 9 and the outputs 70 to 85;
 // 28 us would move the bytes (135 MB), and the two scans issue vector
-// instructions in 68 and 77 % of their cycles.  8 x 2048 tokens of the same,
+// instructions in 75 and 81 % of their cycles.  8 x 2048 tokens of the same,
 // whose rows need no slots: 334 us.  Backward 2 x 2048 tokens of 2048
-// channels: 240 us, states 67, chain 8, main 168 (85 % vector issue), sums
+// channels: 233 us, states 60, chain 8, main 168 (84 % vector issue), sums
 // 15; 24 us would move the bytes.
 //
 // Layout of the forward scans ("quads").  A wave holds 16 channels, lane l
@@ -263,8 +263,9 @@ struct Scanned {
 
 // One group of 16 tokens from token t.  WHOLE: all of them are before `end`.
 // s: this lane's quarter of the group's first token of B; C is `c_off` floats
-// further.  Returns this lane's sum of delta.
-template <typename T, int NS, Mode M, bool WHOLE>
+// further.  GROWS: a decay may be above 1 (see carried).  Returns this lane's
+// sum of delta.
+template <typename T, int NS, Mode M, bool WHOLE, bool GROWS = false>
 __device__ __forceinline__ float scan_group(const ScanArgs& a, const Channel& ch, const Rates<NS>& r, int q,
                                             const Four<T, M>& in, const LaneOffsets& l, int t, int end,
                                             const float* s, int c_off, Scanned<NS>& st, T* __restrict__ o) {
@@ -298,7 +299,8 @@ __device__ __forceinline__ float scan_group(const ScanArgs& a, const Channel& ch
         if (M == kOutput) part[k] = i ? part[k] + C[i] * st.h[i] : C[i] * st.h[i];
         if (M == kAdjoint) {
           st.run[i] *= e;
-          st.adj[i] += carried(st.run[i], quad_bcast<k>(g) * C[i]);
+          const float back = quad_bcast<k>(g) * C[i];
+          st.adj[i] += GROWS ? carried(st.run[i], back) : st.run[i] * back;
         }
       }
     });
@@ -344,6 +346,20 @@ __device__ __forceinline__ float scan_range(const ScanArgs& a, const Channel& ch
   TileRows<T, NP, kScanTile, THREADS, M != kState> tile;
   Four<T, M> next;
   float sum = 0.f;
+  // Decays are at most 1 when delta is a softplus and no rate is above zero,
+  // and the products of them then need no care: 60 us for the backward
+  // pass's states in place of 67 (2 x 2048 tokens of 2048 channels, bf16).
+  bool grows = false;
+  if (M == kAdjoint) {
+#pragma unroll
+    for (int i = 0; i < NS; ++i) grows = grows || r.A2[i] > 0.f;
+    grows = __any(grows || !a.softplus);
+  }
+  auto group_of = [&](const Four<T, M>& in, int u, const float* at, auto whole) {
+    if (M == kAdjoint && grows)
+      return scan_group<T, NS, M, whole.value, true>(a, ch, r, q, in, l, u, end, at, C_OFF, st, o);
+    return scan_group<T, NS, M, whole.value>(a, ch, r, q, in, l, u, end, at, C_OFF, st, o);
+  };
   if (t0 + 16 <= end) next.load(a, dout, l, t0);
   tile.load(a, ch.g, t0, end);
   __syncthreads();  // the range before may still be reading
@@ -359,13 +375,13 @@ __device__ __forceinline__ float scan_range(const ScanArgs& a, const Channel& ch
       const Four<T, M> cur = next;
       if (u + 32 <= end) next.load(a, dout, l, u + 16);
       if (KEEP) keep_group<NS>(a, ch, keep, group++, st.h, sum);
-      sum += scan_group<T, NS, M, true>(a, ch, r, q, cur, l, u, end, sq + (u - t) * NP, C_OFF, st, o);
+      sum += group_of(cur, u, sq + (u - t) * NP, std::true_type{});
     }
     if (u < end && u < t + kScanTile) {
       Four<T, M> cur;
       cur.load(a, dout, ch, u, q, end);
       if (KEEP) keep_group<NS>(a, ch, keep, group++, st.h, sum);
-      sum += scan_group<T, NS, M, false>(a, ch, r, q, cur, l, u, end, sq + (u - t) * NP, C_OFF, st, o);
+      sum += group_of(cur, u, sq + (u - t) * NP, std::false_type{});
     }
     if (more) {
       buf ^= 1;
