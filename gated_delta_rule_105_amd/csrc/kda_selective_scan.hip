@@ -21,7 +21,7 @@
 // 28 us would move the bytes (135 MB), and the two scans issue vector
 // instructions in 75 and 81 % of their cycles.  8 x 2048 tokens of the same,
 // whose rows need no slots: 334 us.  Backward 2 x 2048 tokens of 2048
-// channels: 233 us, states 60, chain 8, main 168 (84 % vector issue), sums
+// channels: 234 us, states 60, chain 8, main 168 (84 % vector issue), sums
 // 15; 24 us would move the bytes.
 //
 // Layout of the forward scans ("quads").  A wave holds 16 channels, lane l

@@ -13,8 +13,8 @@
 // fp32, 10.2 us (4.0 TB/s: some 1300 waves, one batch each); one token for
 // 256 sequences of 6144 channels 8.4 us (3.0 TB/s, one load's latency and the
 // launch); backward 2 x 4096 tokens of 4096 channels, bf16, 46 us and 4.6 for
-// the parameters' sums (201.5 MB, 4.1 TB/s: 12 % more is read than that, the
-// batches that run past a tile).
+// the parameters' sums (201.5 MB necessary, 224 moved: batches that run past
+// a tile are read twice).
 //
 // A lane owns one vector of channels (16 bytes forward, 4 channels backward)
 // and walks a tile of tokens with the last W - 1 inputs in registers, so an
