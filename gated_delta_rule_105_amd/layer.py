@@ -15,6 +15,12 @@ and ``selective_scan`` are the same as differentiable PyTorch operations.
 x, dt, z, B, C, q and k may be column slices of a wider tensor (rows a fixed
 distance apart); everything else must be contiguous.  Activations are bfloat16
 or float32, all of one dtype; parameters and states of the scan are float32.
+
+In a captured graph pass ``validate_cu=False`` (the check reads the offsets on
+the host).  To capture a training step, call the ``*_backward`` functions: a
+captured ``.backward()`` must not meet leaves whose earlier autograd graph,
+made outside the capture, is still alive (PyTorch would tie the capture to
+the stream of that graph).
 """
 from __future__ import annotations
 
