@@ -198,8 +198,8 @@ int kda_short_conv_backward(const kda_conv_desc_t* d, const void* x, const float
   ConvSizes s;
   int st = check_conv(d, &s);
   if (st != KDA_OK) return st;
-  if (s.t.n > 0 && (!x || !weight || !dy || !dx)) return KDA_ERR_INVALID_ARGUMENT;
-  if (!dweight) return KDA_ERR_INVALID_ARGUMENT;
+  if (s.t.n > 0 && (!x || !dy || !dx)) return KDA_ERR_INVALID_ARGUMENT;
+  if (!weight || !dweight) return KDA_ERR_INVALID_ARGUMENT;  // dinitial's workgroups read the taps of empty sequences too
   if ((d->n_seqs > 0) != (cu_seqlens != nullptr)) return KDA_ERR_INVALID_ARGUMENT;
   const size_t need = conv_ws_bytes(d, s);
   if ((st = check_workspace(workspace, workspace_bytes, need)) != KDA_OK) return st;
@@ -341,7 +341,8 @@ int kda_selective_scan_forward(const kda_scan_desc_t* d, const void* x, const vo
   ScanSizes s;
   int st = check_scan(d, &s);
   if (st != KDA_OK) return st;
-  if (s.t.n > 0 && (!x || !dt || !A || !Bm || !Cm || !o)) return KDA_ERR_INVALID_ARGUMENT;
+  if (s.t.n > 0 && (!x || !dt || !Bm || !Cm || !o)) return KDA_ERR_INVALID_ARGUMENT;
+  if (!A) return KDA_ERR_INVALID_ARGUMENT;  // read for the final states of empty sequences too
   if ((d->n_seqs > 0) != (cu_seqlens != nullptr)) return KDA_ERR_INVALID_ARGUMENT;
   const kda::ScanPlan p = scan_plan(d, s);
   if ((st = check_workspace(workspace, workspace_bytes, p.ws_bytes)) != KDA_OK) return st;
