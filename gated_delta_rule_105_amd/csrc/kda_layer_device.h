@@ -1,10 +1,10 @@
 // Device-side helpers of the operators around the recurrence: element-aligned
-// vector loads, the sequences of a batch, exchanges inside rows of 16 lanes,
-// and the activations.
+// vector loads, exchanges inside rows of 16 lanes, and the activations.
 #pragma once
 
 #include "kda_device.h"
 #include "kda_layer.h"
+#include "kda_seqs.h"
 
 namespace kda {
 
@@ -50,40 +50,6 @@ template <typename T>
 __device__ __forceinline__ float load_f32(const T* p) {
   return Elem<T>::to_f32(*p);
 }
-
-// ---- sequences -------------------------------------------------------------
-// The sequences of a batch, as ranges of its tokens: rows of T tokens, or
-// packed ones between the offsets cu (kept inside the batch whatever they
-// hold, so that wrong offsets give wrong results and no wild access).
-struct Seqs {
-  const int32_t* cu;
-  int n;
-  int64_t T, tokens;
-
-  __device__ __forceinline__ int64_t start(int s) const {
-    if (!cu) return s * T;
-    const int64_t c = cu[s];
-    return c < 0 ? 0 : c > tokens ? tokens : c;
-  }
-  __device__ __forceinline__ int64_t end(int s) const { return start(s + 1); }
-  // first sequence that starts at token t or later (n if none does)
-  __device__ __forceinline__ int from(int64_t t) const {
-    if (!cu) {
-      if (T == 0) return t > 0 ? n : 0;
-      const int64_t s = (t + T - 1) / T;
-      return s < n ? (int)s : n;
-    }
-    int lo = 0, hi = n;
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (start(mid) >= t)
-        hi = mid;
-      else
-        lo = mid + 1;
-    }
-    return lo;
-  }
-};
 
 // A value that every lane of the wave holds alike, in a scalar register.
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }

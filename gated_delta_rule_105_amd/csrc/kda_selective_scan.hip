@@ -447,10 +447,11 @@ scan_forward(const ScanArgs a, float* __restrict__ hend, float* __restrict__ sum
     if (!own && w.ch.active && w.q == 0) sum[(int64_t)w.slot * a.D + w.ch.c] = total;
     return;
   }
-  int n = uniform(seqs.from(lo));
+  int n = uniform(seqs.from(lo)), at = lo;
   if (n > 0) {
     const int end = uniform((int)seqs.end(n - 1));
     if (end > lo) {  // a sequence that entered from an earlier slot
+      at = end;
       load_state<NS>(hend, w.slot - 1, a, w.ch, st.h);
       scan_range<T, NS, M>(a, w.ch, w.r, w.q, w.l, lo, end < hi ? end : hi, s, st, o, (const T*)nullptr);
       if (ht && end <= hi) store_state<NS>(ht, n - 1, a, w.ch, st.h);
@@ -458,7 +459,8 @@ scan_forward(const ScanArgs a, float* __restrict__ hend, float* __restrict__ sum
   }
   // those that start here; the last slot also has the empty ones behind the last token
   for (; n < a.n_seqs; ++n) {
-    const int start = uniform((int)seqs.start(n)), end = uniform((int)seqs.end(n));
+    const Span range = seqs.next(n, &at);
+    const int start = uniform(range.start), end = uniform(range.end);
     if (!w.tok.last && start >= hi) break;
     load_state<NS>(a.h0, n, a, w.ch, st.h);
     if (start < end)
@@ -640,7 +642,7 @@ scan_backward_states(const ScanArgs a, const T* __restrict__ dout, const float* 
   Scanned<NS> st;
   int n = uniform(seqs.from(lo));
   const int before = n > 0 ? uniform((int)seqs.end(n - 1)) : lo;
-  int found = kNothing;
+  int found = kNothing, at = before > lo ? before : lo;
   if (before > lo) {  // entered from an earlier slot
     found = kEntered | (before > hi ? kPassed : 0);
 #pragma unroll
@@ -669,7 +671,8 @@ scan_backward_states(const ScanArgs a, const T* __restrict__ dout, const float* 
     store_state<NS>(adj, w.slot, a, w.ch, st.adj);
   }
   for (; n < a.n_seqs; ++n) {
-    const int start = uniform((int)seqs.start(n)), end = uniform((int)seqs.end(n));
+    const Span range = seqs.next(n, &at);
+    const int start = uniform(range.start), end = uniform(range.end);
     if (start >= hi) break;
     if (start >= end) continue;
     load_state<NS>(a.h0, n, a, w.ch, st.h);
@@ -975,10 +978,11 @@ scan_backward(const ScanArgs a, const ScanGrads g, const ScanBwdBuffers w) {
   auto leaving = [&](int n, int end) {
     load_state<NS>(end <= hi ? g.dht : w.adj, end <= hi ? n : slot + 1, a, ch, gr);
   };
-  int n = uniform(seqs.from(lo));
+  int n = uniform(seqs.from(lo)), at = lo;
   if (n > 0) {
     const int end = uniform((int)seqs.end(n - 1));
     if (end > lo) {  // entered from an earlier slot
+      at = end;
       load_state<NS>(w.hend, slot - 1, a, ch, h);
       leaving(n - 1, end);
       range(lo, end < hi ? end : hi, groups_at(lo, n - 1, slot), h, gr);
@@ -987,7 +991,8 @@ scan_backward(const ScanArgs a, const ScanGrads g, const ScanBwdBuffers w) {
 #pragma unroll
   for (int i = 0; i < NS; ++i) h[i] = 0.f;
   for (; n < a.n_seqs; ++n) {
-    const int start = uniform((int)seqs.start(n)), end = uniform((int)seqs.end(n));
+    const Span tok = seqs.next(n, &at);
+    const int start = uniform(tok.start), end = uniform(tok.end);
     if (!own.last && start >= hi) break;
     leaving(n, end);
     if (start < end) range(start, end < hi ? end : hi, groups_at(start, n, slot), h, gr);
