@@ -11,6 +11,9 @@ namespace kda {
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// A launch has less than 2^32 threads along its first dimension.
+inline bool grid_fits(int64_t groups, int64_t threads) { return groups <= (int64_t)UINT32_MAX / threads; }
+
 // ---- short convolution ---------------------------------------------------
 // One wave owns 64 vectors of channels and `tile` tokens, one workgroup
 // kConvWaves such tiles in a row.
@@ -187,6 +190,21 @@ inline ScanBwdPlan plan_scan_backward(int64_t tokens, int rows, int D, int N, in
   return p;
 }
 
+// Workgroups of a scan's launches: the forward scans and the backward pass's
+// states, 16 channels a wave; the backward pass's own.
+inline int64_t scan_groups(int64_t n_slots, int D, int G) {
+  return n_slots * G * ceil_div(D / G, 16 * kScanWaves);
+}
+inline bool scan_fits(const ScanPlan& p, int D, int G) {
+  return grid_fits(scan_groups(p.n_slots, D, G) + 7, 64 * kScanWaves);
+}
+inline bool scan_backward_fits(const ScanBwdPlan& p, int64_t tokens, int D, int N, int G) {
+  return grid_fits(scan_groups(p.n_slots, D, G) + 7, 64 * kScanWaves) &&
+         grid_fits(p.n_slots * G * p.blocks_per_group + 7, 64 * kScanBwdWaves) &&
+         grid_fits(ceil_div((int64_t)D * N + 2 * (int64_t)D, 64), 1024) &&  // sums over the slots
+         grid_fits(ceil_div(tokens * G * N, 256), 256);                     // and over the channels
+}
+
 struct ScanGrads {
   const void* dout;
   const float* dht;
@@ -209,6 +227,37 @@ struct NormArgs {
   float sum_factor;  // 1 (unit) or 1 / d (rms)
   float eps, q_scale;
 };
+
+// Four pairs a lane when neither the head nor its rotated part ends inside
+// such a group, else single pairs; lanes per head the power of two that
+// covers the head (64 at most: single pairs of wide heads then come in chunks).
+inline bool norm_four_pairs(int d, int rot) { return d % 8 == 0 && rot % 8 == 0; }
+inline int norm_head_lanes(int d, int rot) {
+  const int wanted = norm_four_pairs(d, rot) ? d / 8 : d / 2;
+  int lanes = norm_four_pairs(d, rot) ? 4 : 16;
+  while (lanes < 64 && lanes < wanted) lanes *= 2;
+  return lanes;
+}
+// groups of heads, a wave each at a time, that a token has: those of q, then those of k
+inline int norm_groups(int Hq, int Hk, int head_lanes) {
+  const int per = 64 / head_lanes;
+  return (Hq + per - 1) / per + (Hk + per - 1) / per;
+}
+// Groups of heads a wave takes of a token: up to 16 (its angles serve them
+// all: rotated forward 33.0 us with 16, 38.9 with 8, 41.1 with 4), while
+// `waves` waves are left.
+inline int norm_steps(int n_tokens, int groups, int64_t waves) {
+  int steps = groups < 16 ? groups : 16;
+  while (steps > 1 && n_tokens * ceil_div(groups, steps) < waves) steps = (steps + 1) / 2;
+  return steps;
+}
+constexpr int kNormMinWaves = 4096;
+constexpr int kNormForwardWaves = 4;  // waves per workgroup (forward)
+inline bool norm_forward_fits(const NormArgs& a) {
+  const int groups = norm_groups(a.Hq, a.Hk, norm_head_lanes(a.d, a.rot));
+  const int64_t per_token = ceil_div(groups, norm_steps(a.n_tokens, groups, kNormMinWaves));
+  return grid_fits(ceil_div(a.n_tokens * per_token, kNormForwardWaves), 64 * kNormForwardWaves);
+}
 
 // Workgroups of the backward pass at most (a power of two); each leaves a row
 // of d floats of partial sums for each of the weights' gradients.  One on

@@ -113,13 +113,19 @@ int check_conv(const kda_conv_desc_t* d, ConvSizes* s) {
   if (d->width < 2 || d->width > 4) return KDA_ERR_UNSUPPORTED;
   if (d->D > (1 << 23)) return KDA_ERR_UNSUPPORTED;  // the grid's second dimension
   if (s->t.n > (size_t)INT32_MAX - 4096) return KDA_ERR_UNSUPPORTED;  // tokens are counted in 32 bits, with a batch ahead
-  // the final states add a workgroup per kConvWaves rows to the token tiles
-  if (s->t.seqs * (W - 1) + s->t.n / kda::kConvBatch > (size_t)INT32_MAX - 4096) return KDA_ERR_UNSUPPORTED;
   a.n_seqs = (int)s->t.seqs;
   a.T = d->T;
   a.tokens = (int64_t)s->t.n;
   a.D = d->D;
   return KDA_OK;
+}
+
+// The launch over `tile` tokens a wave, and a workgroup per kConvWaves rows of the states with `states`.
+bool conv_fits(ConvSizes* s, int width, int tile, bool states) {
+  s->a.tile = tile;
+  s->a.n_part = kda::conv_parts(s->a.tokens, tile);
+  const int64_t rows = states ? (int64_t)s->t.seqs * (width - 1) : 0;
+  return kda::grid_fits(s->a.n_part + kda::ceil_div(rows, kda::kConvWaves), 64 * kda::kConvWaves);
 }
 
 }  // namespace
@@ -134,6 +140,8 @@ int kda_short_conv_forward(const kda_conv_desc_t* d, const void* x, const float*
   if (st != KDA_OK) return st;
   if (s.t.n > 0 && (!x || !weight || !y)) return KDA_ERR_INVALID_ARGUMENT;
   if ((d->n_seqs > 0) != (cu_seqlens != nullptr)) return KDA_ERR_INVALID_ARGUMENT;
+  if (!conv_fits(&s, d->width, kda::conv_forward_tile(s.bf16, s.a.tokens, s.a.D), final_state != nullptr))
+    return KDA_ERR_UNSUPPORTED;
   Buffers b;
   b.input(x, s.x_bytes, s.esz);
   b.input(weight, s.w_bytes, 4);
@@ -150,8 +158,6 @@ int kda_short_conv_forward(const kda_conv_desc_t* d, const void* x, const float*
   a.bias = bias;
   a.init = initial_state;
   a.cu = cu_seqlens;
-  a.tile = kda::conv_forward_tile(s.bf16, a.tokens, a.D);
-  a.n_part = kda::conv_parts(a.tokens, a.tile);
   return hip_status(kda::launch_conv_forward(s.bf16, d->width, s.silu, a, y, final_state, stream));
 }
 
@@ -201,6 +207,8 @@ int kda_short_conv_backward(const kda_conv_desc_t* d, const void* x, const float
   if (s.t.n > 0 && (!x || !dy || !dx)) return KDA_ERR_INVALID_ARGUMENT;
   if (!weight || !dweight) return KDA_ERR_INVALID_ARGUMENT;  // dinitial's workgroups read the taps of empty sequences too
   if ((d->n_seqs > 0) != (cu_seqlens != nullptr)) return KDA_ERR_INVALID_ARGUMENT;
+  if (!conv_fits(&s, d->width, kda::conv_backward_tile(s.a.tokens, s.a.D), dinitial != nullptr))
+    return KDA_ERR_UNSUPPORTED;
   const size_t need = conv_ws_bytes(d, s);
   if ((st = check_workspace(workspace, workspace_bytes, need)) != KDA_OK) return st;
   Buffers b;
@@ -223,8 +231,6 @@ int kda_short_conv_backward(const kda_conv_desc_t* d, const void* x, const float
   a.bias = bias;
   a.init = initial_state;
   a.cu = cu_seqlens;
-  a.tile = kda::conv_backward_tile(a.tokens, a.D);
-  a.n_part = kda::conv_parts(a.tokens, a.tile);
   return hip_status(kda::launch_conv_backward(s.bf16, d->width, s.silu, a, dy, dfinal, dx, dweight, dbias, dinitial,
                                               (float*)workspace, stream));
 }
@@ -330,7 +336,9 @@ int kda_selective_scan_workspace_size(const kda_scan_desc_t* d, size_t* bytes) {
   ScanSizes s;
   const int st = check_scan(d, &s);
   if (st != KDA_OK) return st;
-  *bytes = scan_plan(d, s).ws_bytes;
+  const kda::ScanPlan p = scan_plan(d, s);
+  if (!kda::scan_fits(p, d->D, d->G)) return KDA_ERR_UNSUPPORTED;
+  *bytes = p.ws_bytes;
   return KDA_OK;
 }
 
@@ -345,6 +353,7 @@ int kda_selective_scan_forward(const kda_scan_desc_t* d, const void* x, const vo
   if (!A) return KDA_ERR_INVALID_ARGUMENT;  // read for the final states of empty sequences too
   if ((d->n_seqs > 0) != (cu_seqlens != nullptr)) return KDA_ERR_INVALID_ARGUMENT;
   const kda::ScanPlan p = scan_plan(d, s);
+  if (!kda::scan_fits(p, d->D, d->G)) return KDA_ERR_UNSUPPORTED;
   if ((st = check_workspace(workspace, workspace_bytes, p.ws_bytes)) != KDA_OK) return st;
   Buffers b;
   scan_inputs(&b, s, x, dt, A, Bm, Cm, skip, z, dt_bias);
@@ -382,7 +391,9 @@ int kda_selective_scan_backward_workspace_size(const kda_scan_desc_t* d, size_t*
   ScanSizes s;
   const int st = check_scan(d, &s);
   if (st != KDA_OK) return st;
-  *bytes = kda::plan_scan_backward(s.a.tokens, s.a.n_seqs, d->D, d->N, d->G).ws_bytes;
+  const kda::ScanBwdPlan p = kda::plan_scan_backward(s.a.tokens, s.a.n_seqs, d->D, d->N, d->G);
+  if (!kda::scan_backward_fits(p, s.a.tokens, d->D, d->N, d->G)) return KDA_ERR_UNSUPPORTED;
+  *bytes = p.ws_bytes;
   return KDA_OK;
 }
 
@@ -401,6 +412,7 @@ int kda_selective_scan_backward(const kda_scan_desc_t* d, const void* x, const v
   if (!A || !dA) return KDA_ERR_INVALID_ARGUMENT;
   if ((d->n_seqs > 0) != (cu_seqlens != nullptr)) return KDA_ERR_INVALID_ARGUMENT;
   const kda::ScanBwdPlan p = kda::plan_scan_backward(s.a.tokens, s.a.n_seqs, d->D, d->N, d->G);
+  if (!kda::scan_backward_fits(p, s.a.tokens, d->D, d->N, d->G)) return KDA_ERR_UNSUPPORTED;
   if ((st = check_workspace(workspace, workspace_bytes, p.ws_bytes)) != KDA_OK) return st;
   Buffers b;
   scan_inputs(&b, s, x, dt, A, Bm, Cm, skip, z, dt_bias);
@@ -514,6 +526,7 @@ int kda_qk_norm_forward(const kda_qk_norm_desc_t* d, const void* q, const void* 
   b.output(k_out, s.ko_bytes, s.esz);
   if (!b.valid()) return KDA_ERR_INVALID_ARGUMENT;
   if (d->n_tokens == 0) return KDA_OK;
+  if (!kda::norm_forward_fits(s.a)) return KDA_ERR_UNSUPPORTED;
   norm_args(&s.a, q, k, q_weight, k_weight, positions, inv_freq);
   return hip_status(kda::launch_norm_forward(s.bf16, s.a, q_out, k_out, stream));
 }

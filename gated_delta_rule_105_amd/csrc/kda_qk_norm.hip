@@ -163,16 +163,16 @@ __device__ __forceinline__ float inv_norm(float ss, float f, float eps) { return
 template <int HPW>
 struct Groups {
   int q, all;
-  __host__ __device__ explicit Groups(const NormArgs& a) : q((a.Hq + HPW - 1) / HPW), all(q + (a.Hk + HPW - 1) / HPW) {}
+  __device__ explicit Groups(const NormArgs& a) : q((a.Hq + HPW - 1) / HPW), all(q + (a.Hk + HPW - 1) / HPW) {}
 };
 
 // Forward: a wave takes `steps` groups of heads of one token.
 template <typename T, int PV, int NC, int LPH, bool WIDE>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(64 * kNormForwardWaves)
 norm_forward(const NormArgs a, T* __restrict__ qo, T* __restrict__ ko, int steps, int waves_per_token) {
   constexpr int HPW = 64 / LPH, U = kNormBatch / NC > 0 ? kNormBatch / NC : 1;
   const int lane = threadIdx.x & 63, sub = lane % LPH, head_in = lane / LPH;
-  const int id = (int)blockIdx.x * 4 + uniform(threadIdx.x >> 6);
+  const int id = (int)blockIdx.x * kNormForwardWaves + uniform(threadIdx.x >> 6);
   const int tok = id / waves_per_token;
   if (tok >= a.n_tokens) return;
   const Groups<HPW> groups(a);
@@ -361,29 +361,19 @@ norm_params(const float* __restrict__ part, int n_part, int d, float* __restrict
   out[c] = v;
 }
 
-// Groups of heads a wave takes of a token: up to 16 (its angles serve them
-// all: rotated forward 33.0 us with 16, 38.9 with 8, 41.1 with 4), while
-// `waves` waves are left.
-inline int norm_steps(int n_tokens, int groups, int64_t waves) {
-  int steps = groups < 16 ? groups : 16;
-  while (steps > 1 && n_tokens * ceil_div(groups, steps) < waves) steps = (steps + 1) / 2;
-  return steps;
-}
-
 template <typename T, int PV, int NC, int LPH, bool WIDE>
 int forward_t(const NormArgs& a, void* qo, void* ko, hipStream_t st) {
-  const int groups = Groups<64 / LPH>(a).all, steps = norm_steps(a.n_tokens, groups, 4096);
+  const int groups = norm_groups(a.Hq, a.Hk, LPH), steps = norm_steps(a.n_tokens, groups, kNormMinWaves);
   const int per_token = (int)ceil_div(groups, steps);
-  const int64_t blocks = ceil_div((int64_t)a.n_tokens * per_token, 4);
-  if (blocks * 4 > INT32_MAX) return (int)hipErrorInvalidValue;
-  return (int)launch_kernel(norm_forward<T, PV, NC, LPH, WIDE>, dim3((unsigned)blocks), dim3(256), st, a, (T*)qo,
-                            (T*)ko, steps, per_token);
+  const int64_t blocks = ceil_div((int64_t)a.n_tokens * per_token, kNormForwardWaves);
+  return (int)launch_kernel(norm_forward<T, PV, NC, LPH, WIDE>, dim3((unsigned)blocks), dim3(64 * kNormForwardWaves),
+                            st, a, (T*)qo, (T*)ko, steps, per_token);
 }
 template <typename T, int PV, int NC, int LPH, bool WIDE>
 int backward_t(const NormArgs& a, const void* dqo, const void* dko, void* dq, void* dk, float* dwq, float* dwk,
                float* part, hipStream_t st) {
-  const int groups = Groups<64 / LPH>(a).all;
-  int steps = norm_steps(a.n_tokens, groups, 4096), per_token = (int)ceil_div(groups, steps);
+  const int groups = norm_groups(a.Hq, a.Hk, LPH);
+  int steps = norm_steps(a.n_tokens, groups, kNormMinWaves), per_token = (int)ceil_div(groups, steps);
   // a token's waves divide the grid's, so that a wave keeps its place in the token
   while (per_token & (per_token - 1)) ++per_token;
   if (per_token > kNormParts * kNormWaves) per_token = kNormParts * kNormWaves;
@@ -406,23 +396,21 @@ template <int PV_, int NC_, int LPH_> struct Shape {
   static constexpr int PV = PV_, NC = NC_, LPH = LPH_;
 };
 
-// Four pairs a lane when neither the head nor its rotated part ends inside
-// such a group, else single pairs; lanes per head the power of two that
-// covers the head.
+// the shape that norm_four_pairs and norm_head_lanes choose
 template <typename T, typename F>
 int dispatch_t(int d, int rot, F&& f) {
-  const int pairs = d / 2;
-  if (d % 8 == 0 && rot % 8 == 0) {
-    if (pairs <= 16) return f(T{}, Shape<4, 1, 4>{});
-    if (pairs <= 32) return f(T{}, Shape<4, 1, 8>{});
-    if (pairs <= 64) return f(T{}, Shape<4, 1, 16>{});
-    if (pairs <= 128) return f(T{}, Shape<4, 1, 32>{});
+  const int lanes = norm_head_lanes(d, rot);
+  if (norm_four_pairs(d, rot)) {
+    if (lanes == 4) return f(T{}, Shape<4, 1, 4>{});
+    if (lanes == 8) return f(T{}, Shape<4, 1, 8>{});
+    if (lanes == 16) return f(T{}, Shape<4, 1, 16>{});
+    if (lanes == 32) return f(T{}, Shape<4, 1, 32>{});
     return f(T{}, Shape<4, 1, 64>{});
   }
-  if (pairs <= 16) return f(T{}, Shape<1, 1, 16>{});
-  if (pairs <= 32) return f(T{}, Shape<1, 1, 32>{});
-  if (pairs <= 64) return f(T{}, Shape<1, 1, 64>{});
-  if (pairs <= 128) return f(T{}, Shape<1, 2, 64>{});
+  if (lanes == 16) return f(T{}, Shape<1, 1, 16>{});
+  if (lanes == 32) return f(T{}, Shape<1, 1, 32>{});
+  if (d <= 128) return f(T{}, Shape<1, 1, 64>{});
+  if (d <= 256) return f(T{}, Shape<1, 2, 64>{});
   return f(T{}, Shape<1, 4, 64>{});
 }
 template <typename F>
