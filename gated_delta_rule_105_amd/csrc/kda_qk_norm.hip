@@ -292,7 +292,8 @@ norm_backward(const NormArgs a, const T* __restrict__ dqo, const T* __restrict__
             along += gr.a[i][e] * (q ? wq.a[i][e] : wk.a[i][e]) * v.a[i][e] +
                      gr.b[i][e] * (q ? wq.b[i][e] : wk.b[i][e]) * v.b[i][e];
           }
-        const float r = inv_norm(head_sum<LPH>(ss), a.sum_factor, a.eps);
+        // lanes beyond the last head hold zeros, whose norm without an epsilon is none
+        const float norm = inv_norm(head_sum<LPH>(ss), a.sum_factor, a.eps), r = there ? norm : 0.f;
         const float back = head_sum<LPH>(along) * a.sum_factor * r;
 #pragma unroll
         for (int i = 0; i < NC; ++i)
