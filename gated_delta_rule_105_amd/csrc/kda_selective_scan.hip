@@ -114,6 +114,16 @@ struct Rates {
   }
 };
 
+// A decay of the wave's channels may be above 1: not when delta is a softplus
+// and no rate is above zero, and the products of decays then need no care.
+template <int NS>
+__device__ __forceinline__ bool may_grow(const ScanArgs& a, const Rates<NS>& r) {
+  bool above = !a.softplus;
+#pragma unroll
+  for (int i = 0; i < NS; ++i) above = above || r.A2[i] > 0.f;
+  return __any(above);
+}
+
 // One row [D, N] of states (zeros where p is null and past N).
 template <int NS>
 __device__ __forceinline__ void load_state(const float* __restrict__ p, int64_t row, const ScanArgs& a,
@@ -135,10 +145,15 @@ __device__ __forceinline__ void store_state(float* __restrict__ p, int64_t row, 
   }
 }
 
-// A decay over many tokens times what it carries.  With a growing state
-// (delta A > 0) the decay of a whole range can pass fp32 while the tokens that
-// make it would, one by one, have left a zero a zero.
-__device__ __forceinline__ float carried(float decay, float v) { return v != 0.f ? decay * v : 0.f; }
+// 2^x v: a decay over many tokens times what it carries.  Where steps of
+// either sign or rates above zero make states grow and shrink again, the decay
+// of a whole range can pass fp32 although no token's result does, so its whole
+// part is added to v's exponent.  (The rest is above 1/2 and at most 1: the
+// product stays in range before that.)
+__device__ __forceinline__ float scaled(float x, float v) {
+  const float t = __builtin_amdgcn_fmed3f(x, -1e30f, 1e30f), whole = __builtin_ceilf(t);
+  return __builtin_amdgcn_ldexpf(v * exp2_fast(t - whole), (int)whole);
+}
 
 __device__ __forceinline__ float delta_of(const ScanArgs& a, float v) {
   const float sp = softplus(v);
@@ -255,22 +270,35 @@ __device__ __forceinline__ void load_lds(const float* p, float (&v)[NS]) {
 }
 
 // State of one scan: the state itself, and for kAdjoint the gradient sent
-// back and the product of the decays so far.
+// back.
 template <int NS>
 struct Scanned {
-  float h[NS], adj[NS], run[NS];
+  float h[NS], adj[NS];
 };
 
 // One group of 16 tokens from token t.  WHOLE: all of them are before `end`.
 // s: this lane's quarter of the group's first token of B; C is `c_off` floats
-// further.  GROWS: a decay may be above 1 (see carried).  Returns this lane's
-// sum of delta.
+// further.  kAdjoint sums what the group's tokens send to the state before it,
+// with the product of the decays so far, and sends that back through the
+// range's tokens before the group, whose sum of delta is `before`.  GROWS: a
+// decay may be above 1; the product then keeps its exponent apart.  Returns
+// this lane's sum of delta.
 template <typename T, int NS, Mode M, bool WHOLE, bool GROWS = false>
 __device__ __forceinline__ float scan_group(const ScanArgs& a, const Channel& ch, const Rates<NS>& r, int q,
                                             const Four<T, M>& in, const LaneOffsets& l, int t, int end,
-                                            const float* s, int c_off, Scanned<NS>& st, T* __restrict__ o) {
+                                            const float* s, int c_off, float before, Scanned<NS>& st,
+                                            T* __restrict__ o) {
   constexpr int NP = 4 * NS;
-  float y[4], sum = 0.f;
+  float y[4], sum = 0.f, adj[NS], run[NS];
+  int exponent[NS];
+  if (M == kAdjoint) {
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      adj[i] = 0.f;
+      run[i] = 1.f;
+      exponent[i] = 0;
+    }
+  }
 #pragma unroll
   for (int m = 0; m < 4; ++m) {
     const bool there = WHOLE || t + 4 * m + q < end;
@@ -298,13 +326,26 @@ __device__ __forceinline__ float scan_group(const ScanArgs& a, const Channel& ch
         st.h[i] = __builtin_fmaf(e, st.h[i], put);
         if (M == kOutput) part[k] = i ? part[k] + C[i] * st.h[i] : C[i] * st.h[i];
         if (M == kAdjoint) {
-          st.run[i] *= e;
+          run[i] *= e;
           const float back = quad_bcast<k>(g) * C[i];
-          st.adj[i] += GROWS ? carried(st.run[i], back) : st.run[i] * back;
+          if (GROWS) {
+            exponent[i] += __builtin_amdgcn_frexp_expf(run[i]);
+            run[i] = __builtin_amdgcn_frexp_mantf(run[i]);
+            adj[i] += __builtin_amdgcn_ldexpf(run[i] * back, exponent[i]);
+          } else {
+            adj[i] += run[i] * back;
+          }
         }
       }
     });
     if (M == kOutput) y[m] = fold_quad(part, q);
+  }
+  if (M == kAdjoint) {
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      const float x = before * r.A2[i];
+      st.adj[i] += GROWS ? scaled(x, adj[i]) : exp2_fast(x) * adj[i];
+    }
   }
   if (M == kOutput && ch.active) {
 #pragma unroll
@@ -329,10 +370,9 @@ __device__ __forceinline__ int groups_at(int t0, int seq, int slot) { return t0 
 
 template <int NS>
 __device__ __forceinline__ void keep_group(const ScanArgs& a, const Channel& ch, const GroupStates& k, int group,
-                                           const float (&h)[NS], float sum) {
+                                           const float (&h)[NS], float before) {
   store_state<NS>(k.h, group, a, ch, h);
-  const float total = quad_sum(sum);
-  if (ch.active && ch.first == 0) k.sum[(int64_t)group * a.D + ch.c] = total;
+  if (ch.active && ch.first == 0) k.sum[(int64_t)group * a.D + ch.c] = before;
 }
 
 // Scans tokens [t0, end) of one sequence.  Returns the lane's sum of delta.
@@ -346,19 +386,13 @@ __device__ __forceinline__ float scan_range(const ScanArgs& a, const Channel& ch
   TileRows<T, NP, kScanTile, THREADS, M != kState> tile;
   Four<T, M> next;
   float sum = 0.f;
-  // Decays are at most 1 when delta is a softplus and no rate is above zero,
-  // and the products of them then need no care: 60 us for the backward
-  // pass's states in place of 67 (2 x 2048 tokens of 2048 channels, bf16).
-  bool grows = false;
-  if (M == kAdjoint) {
-#pragma unroll
-    for (int i = 0; i < NS; ++i) grows = grows || r.A2[i] > 0.f;
-    grows = __any(grows || !a.softplus);
-  }
+  const bool grows = M == kAdjoint && may_grow(a, r);
   auto group_of = [&](const Four<T, M>& in, int u, const float* at, auto whole) {
+    const float before = KEEP ? quad_sum(sum) : 0.f;
+    if (KEEP) keep_group<NS>(a, ch, keep, group++, st.h, before);
     if (M == kAdjoint && grows)
-      return scan_group<T, NS, M, whole.value, true>(a, ch, r, q, in, l, u, end, at, C_OFF, st, o);
-    return scan_group<T, NS, M, whole.value>(a, ch, r, q, in, l, u, end, at, C_OFF, st, o);
+      return scan_group<T, NS, M, whole.value, true>(a, ch, r, q, in, l, u, end, at, C_OFF, before, st, o);
+    return scan_group<T, NS, M, whole.value>(a, ch, r, q, in, l, u, end, at, C_OFF, before, st, o);
   };
   if (t0 + 16 <= end) next.load(a, dout, l, t0);
   tile.load(a, ch.g, t0, end);
@@ -374,13 +408,11 @@ __device__ __forceinline__ float scan_range(const ScanArgs& a, const Channel& ch
     for (; u + 16 <= end && u < t + kScanTile; u += 16) {
       const Four<T, M> cur = next;
       if (u + 32 <= end) next.load(a, dout, l, u + 16);
-      if (KEEP) keep_group<NS>(a, ch, keep, group++, st.h, sum);
       sum += group_of(cur, u, sq + (u - t) * NP, std::true_type{});
     }
     if (u < end && u < t + kScanTile) {
       Four<T, M> cur;
       cur.load(a, dout, ch, u, q, end);
-      if (KEEP) keep_group<NS>(a, ch, keep, group++, st.h, sum);
       sum += group_of(cur, u, sq + (u - t) * NP, std::false_type{});
     }
     if (more) {
@@ -475,7 +507,7 @@ scan_forward(const ScanArgs a, float* __restrict__ hend, float* __restrict__ sum
 //   h_i <- h_i + exp(A sum_i) h_{i-1},   g_i <- g_i + exp(A sum_i) g_{i+1}
 // for the slots that a sequence passes through.  A lane takes one state of
 // one channel; the 8 waves of a workgroup take an eighth of the slots each,
-// first composing it to (product of the decays, state), then again from the
+// first composing it to (exponent of the decays, state), then again from the
 // state that the waves before hand on, so that the chain is an eighth as
 // long.  Loads go ahead of it in batches.
 constexpr int kChainWaves = 8;
@@ -497,15 +529,15 @@ scan_chain(const float* __restrict__ A, int64_t dn, int N, int D, int n_slots, f
   // positions along the chain: slot i, or n_slots - 1 - i going back
   const int first = wave * per, last = first + per < n_slots ? first + per : n_slots;
   int unbroken = 1;
-  auto walk = [&](float& d, float& h, bool write) {
+  auto walk = [&](float& x, float& h, bool write) {
     for (int i0 = first; i0 < last; i0 += BATCH) {
-      float s[BATCH], x[BATCH];
+      float s[BATCH], made[BATCH];
       int kd[BATCH];
 #pragma unroll
       for (int k = 0; k < BATCH; ++k) {
         const int i = i0 + k < last ? i0 + k : last - 1, slot = back ? n_slots - 1 - i : i;
         s[k] = sum[(int64_t)slot * D + c];
-        x[k] = v[(int64_t)slot * dn + el];
+        made[k] = v[(int64_t)slot * dn + el];
         kd[k] = kind[slot];
       }
 #pragma unroll
@@ -513,23 +545,23 @@ scan_chain(const float* __restrict__ A, int64_t dn, int N, int D, int n_slots, f
         if (i0 + k >= last) break;
         // what the slot holds counts only where a sequence leaves it (back: enters it)
         const bool passed = kd[k] & kPassed, holds = back ? kd[k] & kEntered : kd[k] & (kStarted | kPassed);
-        const float e = passed ? exp2_fast(s[k] * A2) : 0.f;
-        h = (passed ? carried(e, h) : 0.f) + (holds ? x[k] : 0.f);
-        d = passed ? e * d : 0.f;
+        const float by = __builtin_amdgcn_fmed3f(s[k] * A2, -1e30f, 1e30f);
+        h = (passed ? scaled(by, h) : 0.f) + (holds ? made[k] : 0.f);
+        x += by;  // of use where all of the wave's slots are passed
         unbroken = passed ? unbroken : 0;
         if (write && there) v[(int64_t)(back ? n_slots - 1 - i0 - k : i0 + k) * dn + el] = h;
       }
     }
   };
-  float d = 1.f, h = 0.f;
-  walk(d, h, false);
-  decay[wave][lane] = d;
+  float x = 0.f, h = 0.f;
+  walk(x, h, false);
+  decay[wave][lane] = x;
   state[wave][lane] = h;
   through[wave] = unbroken;
   __syncthreads();
   h = 0.f;
-  for (int w = 0; w < wave; ++w) h = (through[w] ? carried(decay[w][lane], h) : 0.f) + state[w][lane];
-  walk(d, h, true);
+  for (int w = 0; w < wave; ++w) h = (through[w] ? scaled(decay[w][lane], h) : 0.f) + state[w][lane];
+  walk(x, h, true);
 }
 
 // ---- one token ---------------------------------------------------------------
@@ -630,7 +662,7 @@ scan_step(const ScanArgs a, float* __restrict__ state, T* __restrict__ o, int n_
 // walks the groups of every slot back, redoing each group's recurrence in
 // registers.  The last two add the partial sums.
 template <typename T, int NS>
-__global__ void __launch_bounds__(64 * kScanWaves, 2)
+__global__ void __launch_bounds__(64 * kScanWaves, NS <= 4 ? 3 : 2)
 scan_backward_states(const ScanArgs a, const T* __restrict__ dout, const float* __restrict__ dht,
                      float* __restrict__ hend, float* __restrict__ adj, float* __restrict__ sum,
                      int* __restrict__ kind, const GroupStates keep) {
@@ -648,25 +680,23 @@ scan_backward_states(const ScanArgs a, const T* __restrict__ dout, const float* 
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
       st.h[i] = st.adj[i] = 0.f;
-      st.run[i] = 1.f;
     }
     const float d = scan_range<T, NS, kAdjoint, true>(a, w.ch, w.r, w.q, w.l, lo, before < hi ? before : hi, s, st,
                                                       (T*)nullptr, dout, keep, groups_at(lo, n - 1, w.slot));
+    const float all = quad_sum(d);
     if (before <= hi) {
       float last[NS];
       load_state<NS>(dht, n - 1, a, w.ch, last);
 #pragma unroll
-      for (int i = 0; i < NS; ++i) st.adj[i] += carried(st.run[i], last[i]);
+      for (int i = 0; i < NS; ++i) st.adj[i] += scaled(all * w.r.A2[i], last[i]);
     } else {
       store_state<NS>(hend, w.slot, a, w.ch, st.h);
-      const float total = quad_sum(d);
-      if (w.ch.active && w.q == 0) sum[(int64_t)w.slot * a.D + w.ch.c] = total;
+      if (w.ch.active && w.q == 0) sum[(int64_t)w.slot * a.D + w.ch.c] = all;
     }
-    const float all = quad_sum(d);
 #pragma unroll
     for (int i = 0; i < NS; ++i) {  // a NaN decay reaches back through any gradient
-      const float e = exp2_fast(all * w.r.A2[i]);
-      st.adj[i] = e != e ? e : st.adj[i];
+      const float x = all * w.r.A2[i];
+      st.adj[i] = x != x ? x : st.adj[i];
     }
     store_state<NS>(adj, w.slot, a, w.ch, st.adj);
   }
@@ -864,7 +894,7 @@ scan_backward(const ScanArgs a, const ScanGrads g, const ScanBwdBuffers w) {
       const float dx = there ? delta * x : 0.f;
       float first[NS], hh[16][NS], dd[16][NS];
 #pragma unroll
-      for (int i = 0; i < NS; ++i) first[i] = cur.h_[i] + carried(exp2_fast(cur.sum_ * r.A2[i]), h[i]);
+      for (int i = 0; i < NS; ++i) first[i] = cur.h_[i] + scaled(cur.sum_ * r.A2[i], h[i]);
       RowSums ys;
       static_for<4>([&](auto k4) {
         f32x4 B[NS], C[NS];

@@ -28,3 +28,60 @@ def test_norm_gradient_without_epsilon(Hq, Hk, d, rot, kind):
         dx, dw, mx, mw = ref.norm_grad(x, dout, w, p["pos"], p["freq"], kind, 0.0)
         check("d" + n, g["d" + n], dx, mx, 128)
         check(f"d{n}_weight", g[f"d{n}_weight"], dw, mw, 128 + x.numel() // d)
+
+
+# ---------------------------------------------------------------- states that grow and shrink
+def swinging(lengths, seed):
+    """64-token stretches with steps of either sign: half of the states (tiny ones, with tiny B and C) grow by e^102 in
+    a stretch and shrink back in the next, the others swing the other way by e^-26."""
+    gen = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=gen).cuda()  # noqa: E731
+    T, D, N = 384, 10, 6
+    S = 1 if lengths is None else len(lengths)
+    cu = None if lengths is None else torch.tensor([sum(lengths[:i]) for i in range(S + 1)], dtype=torch.int32).cuda()
+    size = torch.ones(N).cuda()
+    size[::2] = 1e-20
+    dt = torch.tensor([0.0, 0.8, -0.8, 0.75, -0.75, 0.1]).repeat_interleave(64).cuda()
+    A = torch.full((D, N), -0.5).cuda()
+    A[:, ::2] = 2.0
+    p = dict(x=r(1, T, D), dt=dt[None, :, None].expand(1, T, D).contiguous(), A=A, B=r(1, T, 1, N) * size,
+             C=r(1, T, 1, N) * size, D=r(D), z=r(1, T, D))
+    return p, r(S, D, N) * size, cu, r(1, T, D), r(S, D, N) * size
+
+
+@pytest.mark.parametrize("lengths", [None, [70, 0, 314], [1, 383]])
+def test_states_that_swing(lengths):
+    """Every state stays inside fp32 token by token, so composing stretches must not overflow either.  A step
+    multiplies by e^1.6, off by under 7 roundings; a stretch of 64 composed at once is off by its sum of delta (16
+    additions a lane and 2 more, 9 roundings at half their weight) times its exponent of 103: under 1024 roundings, 16
+    a token.  The gradient has two such recurrences."""
+    p, h0, cu, do, dht = swinging(lengths, 50)
+    note(f"selective_scan swinging states {lengths}")
+    o, ht = kda.selective_scan_forward(**p, h0=h0, cu_seqlens=cu, dt_softplus=False)
+    g = kda.selective_scan_backward(**p, do=do, h0=h0, dht=dht, cu_seqlens=cu, dt_softplus=False)
+    torch.cuda.synchronize()
+    ro, rht, mo, mht = ref.scan(**p, h0=h0, cu=cu, softplus=False)
+    check("o", o, ro, mo, 64 + 16 * 384)
+    check("ht", ht, rht, mht, 64 + 16 * 384)
+    rg, rm = ref.scan_grad(**p, do=do, h0=h0, dht=dht, cu=cu, softplus=False)
+    for key in ("dx", "ddt", "dA", "dB", "dC", "dD", "dz", "dh0"):
+        check(key, g[key], rg[key], rm[key], 128 + 32 * 384 + 384)
+
+
+def test_a_state_that_vanishes_and_grows():
+    """Stretches that decay by 2^-550 and then grow by as much leave what fp32 leaves of a state, never a NaN."""
+    p, h0, _, do, dht = swinging(None, 51)
+    note("selective_scan vanishing states")
+    long = lambda t: t.repeat(1, 4, *[1] * (t.dim() - 2))  # noqa: E731
+    p = {k: (long(v) if k in ("x", "B", "C", "z") else v) for k, v in p.items()}
+    p["dt"] = torch.tensor([-3.0, 3.0] * 12).repeat_interleave(64).cuda()[None, :, None].expand(1, 1536, 10).contiguous()
+    p["B"][..., ::2] = 0.0
+    p["A"][:, 1::2] = -0.01
+    o, ht = kda.selective_scan_forward(**p, h0=h0, dt_softplus=False)
+    do = long(do)
+    p["C"][..., ::2] = 0.0
+    g = kda.selective_scan_backward(**p, do=do, h0=h0, dt_softplus=False)
+    torch.cuda.synchronize()
+    assert torch.isfinite(o).all() and torch.isfinite(ht).all()
+    for key in ("dx", "ddt", "dA", "dB", "dC", "dD", "dz", "dh0"):
+        assert torch.isfinite(g[key]).all(), key
