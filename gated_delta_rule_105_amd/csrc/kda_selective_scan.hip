@@ -281,9 +281,9 @@ struct Scanned {
 // further.  kAdjoint sums what the group's tokens send to the state before it,
 // with the product of the decays so far, and sends that back through the
 // range's tokens before the group, whose sum of delta is `before`.  GROWS: a
-// decay may be above 1; the product then keeps its exponent apart.  Returns
-// this lane's sum of delta.
-template <typename T, int NS, Mode M, bool WHOLE, bool GROWS = false>
+// decay may be above 1; the product then keeps its exponent apart.  WILD:
+// states past N are kept zero whatever comes.  Returns this lane's sum of delta.
+template <typename T, int NS, Mode M, bool WHOLE, bool GROWS = false, bool WILD = false>
 __device__ __forceinline__ float scan_group(const ScanArgs& a, const Channel& ch, const Rates<NS>& r, int q,
                                             const Four<T, M>& in, const LaneOffsets& l, int t, int end,
                                             const float* s, int c_off, float before, Scanned<NS>& st,
@@ -324,6 +324,7 @@ __device__ __forceinline__ float scan_group(const ScanArgs& a, const Channel& ch
         const float e = exp2_fast(quad_bcast<k>(d) * r.A2[i]);
         const float put = quad_bcast<k>(v) * B[i];
         st.h[i] = __builtin_fmaf(e, st.h[i], put);
+        if (WILD) st.h[i] = ch.first + i < a.N ? st.h[i] : 0.f;
         if (M == kOutput) part[k] = i ? part[k] + C[i] * st.h[i] : C[i] * st.h[i];
         if (M == kAdjoint) {
           run[i] *= e;
@@ -342,10 +343,7 @@ __device__ __forceinline__ float scan_group(const ScanArgs& a, const Channel& ch
   }
   if (M == kAdjoint) {
 #pragma unroll
-    for (int i = 0; i < NS; ++i) {
-      const float x = before * r.A2[i];
-      st.adj[i] += GROWS ? scaled(x, adj[i]) : exp2_fast(x) * adj[i];
-    }
+    for (int i = 0; i < NS; ++i) st.adj[i] += scaled(before * r.A2[i], adj[i]);
   }
   if (M == kOutput && ch.active) {
 #pragma unroll
@@ -377,7 +375,12 @@ __device__ __forceinline__ void keep_group(const ScanArgs& a, const Channel& ch,
 
 // Scans tokens [t0, end) of one sequence.  Returns the lane's sum of delta.
 // KEEP: leaves what GroupStates says from group `group` on.
-template <typename T, int NS, Mode M, bool KEEP = false>
+// PADS: some lanes hold states past N, the last state of a channel's last lane
+// among them.  They read zeros for B and C and stay zero, unless an infinite
+// delta x makes NaN of them.  A tile of tokens that ends so is scanned again
+// with them kept zero (20011 tokens of 771 channels, 12 states, fp32: 169 us; a
+// look at every group's inputs beforehand 175).
+template <typename T, int NS, Mode M, bool KEEP = false, bool PADS = false>
 __device__ __forceinline__ float scan_range(const ScanArgs& a, const Channel& ch, const Rates<NS>& r, int q,
                                             const LaneOffsets& l, int t0, int end, float* s, Scanned<NS>& st,
                                             T* __restrict__ o, const T* __restrict__ dout, GroupStates keep = {},
@@ -394,6 +397,7 @@ __device__ __forceinline__ float scan_range(const ScanArgs& a, const Channel& ch
       return scan_group<T, NS, M, whole.value, true>(a, ch, r, q, in, l, u, end, at, C_OFF, before, st, o);
     return scan_group<T, NS, M, whole.value>(a, ch, r, q, in, l, u, end, at, C_OFF, before, st, o);
   };
+  __shared__ float entered[PADS ? NS : 1][THREADS];  // the states that entered the tile
   if (t0 + 16 <= end) next.load(a, dout, l, t0);
   tile.load(a, ch.g, t0, end);
   __syncthreads();  // the range before may still be reading
@@ -405,6 +409,10 @@ __device__ __forceinline__ float scan_range(const ScanArgs& a, const Channel& ch
     if (more) tile.load(a, ch.g, t + kScanTile, end);
     const float* sq = s + buf * BUF + q * NS;
     int u = t;
+    if (PADS) {
+#pragma unroll
+      for (int i = 0; i < NS; ++i) entered[i][threadIdx.x] = st.h[i];
+    }
     for (; u + 16 <= end && u < t + kScanTile; u += 16) {
       const Four<T, M> cur = next;
       if (u + 32 <= end) next.load(a, dout, l, u + 16);
@@ -414,6 +422,15 @@ __device__ __forceinline__ float scan_range(const ScanArgs& a, const Channel& ch
       Four<T, M> cur;
       cur.load(a, dout, ch, u, q, end);
       sum += group_of(cur, u, sq + (u - t) * NP, std::false_type{});
+    }
+    if (PADS && __any(q == 3 && st.h[NS - 1] != 0.f)) {
+#pragma unroll
+      for (int i = 0; i < NS; ++i) st.h[i] = ch.first + i < a.N ? entered[i][threadIdx.x] : 0.f;
+      for (u = t; u < end && u < t + kScanTile; u += 16) {
+        Four<T, M> cur;
+        cur.load(a, dout, ch, u, q, end);
+        scan_group<T, NS, M, false, false, true>(a, ch, r, q, cur, l, u, end, sq + (u - t) * NP, C_OFF, 0.f, st, o);
+      }
     }
     if (more) {
       buf ^= 1;
@@ -454,7 +471,7 @@ enum SlotKind { kNothing = 0, kStarted = 1, kPassed = 2, kEntered = 4 };
 
 // Forward.  M = kState: the first launch, over what a slot leaves unfinished;
 // kOutput: the last one, hend then holding the states at the slots' ends.
-template <typename T, int NS, Mode M>
+template <typename T, int NS, Mode M, bool PADS>
 __global__ void __launch_bounds__(64 * kScanWaves, 2)
 scan_forward(const ScanArgs a, float* __restrict__ hend, float* __restrict__ sum, int* __restrict__ kind,
              T* __restrict__ o, float* __restrict__ ht) {
@@ -485,7 +502,7 @@ scan_forward(const ScanArgs a, float* __restrict__ hend, float* __restrict__ sum
     if (end > lo) {  // a sequence that entered from an earlier slot
       at = end;
       load_state<NS>(hend, w.slot - 1, a, w.ch, st.h);
-      scan_range<T, NS, M>(a, w.ch, w.r, w.q, w.l, lo, end < hi ? end : hi, s, st, o, (const T*)nullptr);
+      scan_range<T, NS, M, false, PADS>(a, w.ch, w.r, w.q, w.l, lo, end < hi ? end : hi, s, st, o, (const T*)nullptr);
       if (ht && end <= hi) store_state<NS>(ht, n - 1, a, w.ch, st.h);
     }
   }
@@ -496,7 +513,8 @@ scan_forward(const ScanArgs a, float* __restrict__ hend, float* __restrict__ sum
     if (!w.tok.last && start >= hi) break;
     load_state<NS>(a.h0, n, a, w.ch, st.h);
     if (start < end)
-      scan_range<T, NS, M>(a, w.ch, w.r, w.q, w.l, start, end < hi ? end : hi, s, st, o, (const T*)nullptr);
+      scan_range<T, NS, M, false, PADS>(a, w.ch, w.r, w.q, w.l, start, end < hi ? end : hi, s, st, o,
+                                        (const T*)nullptr);
     if (ht && end <= hi) store_state<NS>(ht, n, a, w.ch, st.h);
   }
 }
@@ -844,12 +862,20 @@ __device__ __forceinline__ LaneOffsets lane_offsets(const ScanArgs& a, int token
                      e * (uint32_t)(token * a.ld_z + c), e * (uint32_t)(token * (int64_t)a.D + c)};
 }
 
-template <typename T, int NS>
+// CARE: some lanes have no state or no channel, or a range's end may cut a
+// group short.  Such lanes read zeros for B and C, or have zeros for delta,
+// delta x and dy, and stay zero; tokens past the end have a delta of zero.  Only
+// an infinity (of an input, or of a product) makes NaN of a lane's zeros or of
+// dA's products with such a delta; a group that ends so is walked again with
+// both left out (a call over 4096 tokens of 2048 channels in 40 sequences, bf16,
+// 16 states: 277 us, 271 without care; 24 states 236 and 221).
+template <typename T, int NS, bool CARE>
 __global__ void __launch_bounds__(64 * kScanBwdWaves, NS == 1 ? 3 : 1)
 scan_backward(const ScanArgs a, const ScanGrads g, const ScanBwdBuffers w) {
   constexpr int WV = kScanBwdWaves, THREADS = 64 * WV;
   __shared__ __align__(16) float bc[2 * NS * 16 * kColLd];  // B, C of a tile
   __shared__ float tiles[2][WV][2][NS][256];                // dB, dC of a group, per wave
+  __shared__ float before[3][CARE ? NS : 1][THREADS];       // a lane's states, gradients and dA before a group
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), j = lane & 15;
   int slot, block;
   if (!work_of(a, &slot, &block)) return;
@@ -866,6 +892,9 @@ scan_backward(const ScanArgs a, const ScanGrads g, const ScanBwdBuffers w) {
 #pragma unroll
   for (int i = 0; i < NS; ++i) dA[i] = 0.f;
   int buf = 0;
+  bool real[NS];  // a state, and a channel, that there is
+#pragma unroll
+  for (int i = 0; i < NS; ++i) real[i] = ch.active && j + 16 * i < a.N;
 
   // tokens [t0, end) of one sequence, whose groups are `at`, at + 1, ...: h
   // the state that entered the range (zero when the groups' states have it),
@@ -876,12 +905,12 @@ scan_backward(const ScanArgs a, const ScanGrads g, const ScanBwdBuffers w) {
     TileCols<T, NS, THREADS> tile;
     tile.load(a, group, t0 + (q & ~3) * 16, end);
     Token<T, NS> next;
-    const int left = end - t0 - 16 * q;  // tokens of the last group
-    next.load(a, dout, w.groups, ch, lane_offsets(a, j < left ? j : left - 1, ch.c, sizeof(T)), t0 + 16 * q, at + q);
+    int tokens = end - t0 - 16 * q;  // of the last group, then 16
+    next.load(a, dout, w.groups, ch, lane_offsets(a, j < tokens ? j : tokens - 1, ch.c, sizeof(T)), t0 + 16 * q, at + q);
     __syncthreads();  // the range before may still be reading
     tile.store(a, bc, t0 + (q & ~3) * 16, end);
     __syncthreads();
-    bool there = ch.active && j < left;
+    bool there = ch.active && j < tokens;
     for (; q >= 0; --q) {
       const Token<T, NS> cur = next;
       const int t = t0 + 16 * q;
@@ -895,76 +924,107 @@ scan_backward(const ScanArgs a, const ScanGrads g, const ScanBwdBuffers w) {
       float first[NS], hh[16][NS], dd[16][NS];
 #pragma unroll
       for (int i = 0; i < NS; ++i) first[i] = cur.h_[i] + scaled(cur.sum_ * r.A2[i], h[i]);
-      RowSums ys;
-      static_for<4>([&](auto k4) {
-        f32x4 B[NS], C[NS];
-#pragma unroll
-        for (int i = 0; i < NS; ++i) {
-          B[i] = *(const f32x4*)(sb + i * 16 * kColLd + 4 * k4);
-          C[i] = *(const f32x4*)(sc + i * 16 * kColLd + 4 * k4);
-        }
-        static_for<4>([&](auto e) {
-          constexpr int k = 4 * decltype(k4)::value + decltype(e)::value;
-          const float dk = row_bcast<k>(delta), xk = row_bcast<k>(dx);
-          float y = 0.f;
-#pragma unroll
-          for (int i = 0; i < NS; ++i) {
-            dd[k][i] = exp2_fast(dk * r.A2[i]);
-            const float put = xk * B[i][decltype(e)::value];
-            hh[k][i] = __builtin_fmaf(dd[k][i], k ? hh[k ? k - 1 : 0][i] : first[i], put);
-            y = i ? y + C[i][decltype(e)::value] * hh[k][i] : C[i][decltype(e)::value] * hh[k][i];
-          }
-          ys.v[k] = y;
-          ys.template done<k, false>(j);
-        });
-        __builtin_amdgcn_sched_barrier(0);
-      });
-      const float z = cur.z(), dout_j = cur.dout(), sg = sigmoid(z), y = ys.total + r.skip * x;
-      const float dz = dout_j * y * (sg * (1.f + z * (1.f - sg)));
-      float dy = dout_j * (a.has_z ? z * sg : 1.f);
-      dy = there ? dy : 0.f;
+      RowSums ys, s1, s2;
+      float dy, dz;
       float tb[NS][4], tc[NS][4];  // dB and dC of tokens 4 e + row
-      RowSums s1, s2;
-      // other registers to the compiler, which would else keep the 32 values
-      // broadcast above for the loop below
-      float delta_b = delta, dx_b = dx;
-      asm volatile("" : "+v"(delta_b), "+v"(dx_b));
-      static_for<4>([&](auto k4r) {
-        constexpr int k4 = 3 - decltype(k4r)::value;
-        f32x4 B[NS], C[NS];
-#pragma unroll
-        for (int i = 0; i < NS; ++i) {
-          B[i] = *(const f32x4*)(sb + i * 16 * kColLd + 4 * k4);
-          C[i] = *(const f32x4*)(sc + i * 16 * kColLd + 4 * k4);
-        }
-        float vb[NS][4], vc[NS][4];
-        static_for<4>([&](auto er) {
-          constexpr int e = 3 - decltype(er)::value, k = 4 * k4 + e;
-          const float dk = row_bcast<k>(delta_b), gk = row_bcast<k>(dy), xk = row_bcast<k>(dx_b);
-          float p1 = 0.f, p2 = 0.f;
+      // the group's tokens forward, then back
+      auto walk = [&](auto care) {
+        static_for<4>([&](auto k4) {
+          f32x4 B[NS], C[NS];
 #pragma unroll
           for (int i = 0; i < NS; ++i) {
-            const float dh = __builtin_fmaf(gk, C[i][e], gr[i]);
-            vc[i][e] = gk * hh[k][i];
-            vb[i][e] = xk * dh;
-            gr[i] = dh * dd[k][i];
-            const float m = gr[i] * (k ? hh[k ? k - 1 : 0][i] : first[i]);
-            p1 = i ? p1 + m * r.A2[i] : m * r.A2[i];
-            p2 = i ? p2 + dh * B[i][e] : dh * B[i][e];
-            dA[i] = __builtin_fmaf(dk, m, dA[i]);
+            B[i] = *(const f32x4*)(sb + i * 16 * kColLd + 4 * k4);
+            C[i] = *(const f32x4*)(sc + i * 16 * kColLd + 4 * k4);
           }
-          s1.v[k] = p1;
-          s2.v[k] = p2;
-          s1.template done<k, true>(j);
-          s2.template done<k, true>(j);
+          static_for<4>([&](auto e) {
+            constexpr int k = 4 * decltype(k4)::value + decltype(e)::value;
+            const float dk = row_bcast<k>(delta), xk = row_bcast<k>(dx);
+            float y = 0.f;
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+              dd[k][i] = exp2_fast(dk * r.A2[i]);
+              const float put = xk * B[i][decltype(e)::value];
+              hh[k][i] = __builtin_fmaf(dd[k][i], k ? hh[k ? k - 1 : 0][i] : first[i], put);
+              if (care) hh[k][i] = real[i] ? hh[k][i] : 0.f;
+              y = i ? y + C[i][decltype(e)::value] * hh[k][i] : C[i][decltype(e)::value] * hh[k][i];
+            }
+            ys.v[k] = y;
+            ys.template done<k, false>(j);
+          });
+          __builtin_amdgcn_sched_barrier(0);
         });
+        const float z = cur.z(), dout_j = cur.dout(), sg = sigmoid(z), y = ys.total + r.skip * x;
+        dz = dout_j * y * (sg * (1.f + z * (1.f - sg)));
+        dy = dout_j * (a.has_z ? z * sg : 1.f);
+        dy = there ? dy : 0.f;
+        // other registers to the compiler, which would else keep the 32 values
+        // broadcast above for the loop below
+        float delta_b = delta, dx_b = dx;
+        asm volatile("" : "+v"(delta_b), "+v"(dx_b));
+        static_for<4>([&](auto k4r) {
+          constexpr int k4 = 3 - decltype(k4r)::value;
+          f32x4 B[NS], C[NS];
+#pragma unroll
+          for (int i = 0; i < NS; ++i) {
+            B[i] = *(const f32x4*)(sb + i * 16 * kColLd + 4 * k4);
+            C[i] = *(const f32x4*)(sc + i * 16 * kColLd + 4 * k4);
+          }
+          float vb[NS][4], vc[NS][4];
+          static_for<4>([&](auto er) {
+            constexpr int e = 3 - decltype(er)::value, k = 4 * k4 + e;
+            const float dk = row_bcast<k>(delta_b), gk = row_bcast<k>(dy), xk = row_bcast<k>(dx_b);
+            float p1 = 0.f, p2 = 0.f;
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+              float dh = __builtin_fmaf(gk, C[i][e], gr[i]);
+              if (care) dh = real[i] ? dh : 0.f;
+              vc[i][e] = gk * hh[k][i];
+              vb[i][e] = xk * dh;
+              gr[i] = dh * dd[k][i];
+              if (care) gr[i] = real[i] ? gr[i] : 0.f;
+              const float m = gr[i] * (k ? hh[k ? k - 1 : 0][i] : first[i]);
+              p1 = i ? p1 + m * r.A2[i] : m * r.A2[i];
+              p2 = i ? p2 + dh * B[i][e] : dh * B[i][e];
+              if (!care || k < tokens) dA[i] = __builtin_fmaf(dk, m, dA[i]);
+            }
+            s1.v[k] = p1;
+            s2.v[k] = p2;
+            s1.template done<k, true>(j);
+            s2.template done<k, true>(j);
+          });
+#pragma unroll
+          for (int i = 0; i < NS; ++i) {
+            tb[i][k4] = fold_rows(vb[i]);
+            tc[i][k4] = fold_rows(vc[i]);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        });
+      };
+      if (CARE) {
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
-          tb[i][k4] = fold_rows(vb[i]);
-          tc[i][k4] = fold_rows(vc[i]);
+          first[i] = real[i] ? first[i] : 0.f;
+          before[0][i][threadIdx.x] = first[i];
+          before[1][i][threadIdx.x] = gr[i];
+          before[2][i][threadIdx.x] = dA[i];
         }
-        __builtin_amdgcn_sched_barrier(0);
-      });
+      }
+      walk(std::false_type{});
+      if (CARE) {
+        bool again = false;
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+          again = again || (!real[i] && (hh[15][i] != 0.f || gr[i] != 0.f)) || (tokens < 16 && dA[i] != dA[i]);
+        if (__any(again)) {
+#pragma unroll
+          for (int i = 0; i < NS; ++i) {
+            first[i] = before[0][i][threadIdx.x];
+            gr[i] = before[1][i][threadIdx.x];
+            dA[i] = before[2][i][threadIdx.x];
+          }
+          walk(std::true_type{});
+        }
+      }
       const float slope = a.softplus ? sigmoid(v) : 1.f;
       const float ddt = (kLn2 * s1.total + x * s2.total) * slope;
       if (there) {
@@ -1000,6 +1060,7 @@ scan_backward(const ScanArgs a, const ScanGrads g, const ScanBwdBuffers w) {
         __syncthreads();
       }
       there = ch.active;
+      tokens = 16;
     }
   };
 
@@ -1105,14 +1166,14 @@ int forward_t(ScanArgs a, const ScanPlan& p, void* o, float* ht, void* ws, hipSt
     hend = (float*)((char*)ws + p.hend_off);
     sum = (float*)((char*)ws + p.sum_off);
     kind = (int*)((char*)ws + p.kind_off);
-    const hipError_t e = launch_kernel(scan_forward<T, NS, kState>, work_grid(a), dim3(64 * kScanWaves), st, a, hend,
-                                       sum, kind, (T*)nullptr, (float*)nullptr);
+    const hipError_t e = launch_kernel(scan_forward<T, NS, kState, false>, work_grid(a), dim3(64 * kScanWaves), st, a,
+                                       hend, sum, kind, (T*)nullptr, (float*)nullptr);
     if (e != hipSuccess) return (int)e;
     const int err = launch_chain(a, hend, (float*)nullptr, sum, kind, st);
     if (err != 0) return err;
   }
-  return (int)launch_kernel(scan_forward<T, NS, kOutput>, work_grid(a), dim3(64 * kScanWaves), st, a, hend, sum, kind,
-                            (T*)o, ht);
+  return (int)launch_kernel(a.N < 4 * NS ? scan_forward<T, NS, kOutput, true> : scan_forward<T, NS, kOutput, false>,
+                            work_grid(a), dim3(64 * kScanWaves), st, a, hend, sum, kind, (T*)o, ht);
 }
 
 template <typename T>
@@ -1187,7 +1248,9 @@ int backward_t(ScanArgs a, const ScanBwdPlan& p, const ScanGrads& g, void* ws, h
   a.blocks_per_group = p.blocks_per_group;
   const ScanBwdBuffers w{hend, adj, groups, at(p.da_off), at(p.dskip_off), at(p.dbias_off), at(p.db_off),
                          at(p.dc_off)};
-  hipError_t e = launch_kernel(scan_backward<T, NS>, work_grid(a), dim3(64 * kScanBwdWaves), st, a, g, w);
+  const bool whole = a.N == 16 * NS && a.D / a.G % 16 == 0 && !a.cu && a.T % 16 == 0;
+  auto* kernel = whole ? scan_backward<T, NS, false> : scan_backward<T, NS, true>;
+  hipError_t e = launch_kernel(kernel, work_grid(a), dim3(64 * kScanBwdWaves), st, a, g, w);
   if (e != hipSuccess) return (int)e;
   const int64_t dn = (int64_t)a.D * a.N, cols = a.tokens * a.G * a.N;
   e = launch_kernel(scan_sum_slots, dim3((unsigned)ceil_div(dn + 2 * (int64_t)a.D, 64)), dim3(1024), st, w.da,

@@ -85,3 +85,51 @@ def test_a_state_that_vanishes_and_grows():
     assert torch.isfinite(o).all() and torch.isfinite(ht).all()
     for key in ("dx", "ddt", "dA", "dB", "dC", "dD", "dz", "dh0"):
         assert torch.isfinite(g[key]).all(), key
+
+
+# ---------------------------------------------------------------- infinities beside lanes without a state or channel
+def positive(D, N, dtype, seed, T=150):
+    """Positive inputs and slow decays: an infinity stays one of its sign through every sum."""
+    gen = torch.Generator().manual_seed(seed)
+    r = lambda *s: 0.1 + torch.rand(*s, generator=gen)  # noqa: E731
+    c = lambda *s: r(*s).to(dtype).cuda()  # noqa: E731
+    p = dict(x=c(1, T, D), dt=(r(1, T, D) - 2).to(dtype).cuda(), A=(-0.01 * r(D, N)).cuda(), B=c(1, T, 1, N),
+             C=c(1, T, 1, N), D=r(D).cuda(), z=c(1, T, D))
+    return p, r(1, D, N).cuda(), c(1, T, D), r(1, D, N).cuda()
+
+
+def same_kind(name, got, want):
+    """NaN, infinities and their signs where the definition has them."""
+    got, want = got.detach().cpu().double(), want
+    for kind, a, b in (("nan", got.isnan(), want.isnan()), ("inf", got == float("inf"), want == float("inf")),
+                       ("-inf", got == -float("inf"), want == -float("inf"))):
+        assert torch.equal(a, b), f"{name}: {int((a != b).sum())} of {a.numel()} elements differ in being {kind}"
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("D,N", [(18, 1), (18, 3), (16, 4), (18, 6), (20, 12), (18, 16), (16, 17), (18, 24), (18, 33),
+                                 (17, 48)])
+@pytest.mark.parametrize("where", ["x", "B", "C", "h0", "dht", "do"])
+def test_infinities_next_to_padding(where, D, N, dtype):
+    """N and D that leave lanes without a state or a channel: an infinity gives what the definition gives."""
+    p, h0, do, dht = positive(D, N, dtype, 60 + N)
+    note(f"selective_scan infinity in {where} D={D} N={N} {dtype}")
+    t = dict(p, h0=h0, do=do, dht=dht)[where]
+    t.reshape(-1)[(70 * t[0, 0].numel() if t.dim() > 2 and t.shape[1] == 150 else 0) + t[0, 0].numel() - 1] = float("inf")
+    if where in ("h0", "dht"):
+        t.zero_()[0, D - 1, N - 1] = float("inf")
+    o, ht = kda.selective_scan_forward(**p, h0=h0)
+    g = kda.selective_scan_backward(**p, do=do, h0=h0, dht=dht)
+    torch.cuda.synchronize()
+    ro, rht, _, _ = ref.scan(**p, h0=h0)
+    same_kind("o", o, ro)
+    same_kind("ht", ht, rht)
+    rg, _ = ref.scan_grad(**p, do=do, h0=h0, dht=dht)
+    for key in ("dx", "ddt", "dA", "dB", "dC", "dD", "dz", "dh0"):
+        same_kind(key, g[key], rg[key])
+    state = h0.clone()
+    for i in range(150):
+        tok = {k: (v[:, i] if k in ("x", "dt", "z", "B", "C") else v) for k, v in p.items()}
+        oi = kda.selective_scan_step(state=state, **tok)
+        if 68 <= i < 74:
+            same_kind(f"step {i}", oi, ro[:, i])
