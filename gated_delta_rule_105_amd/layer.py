@@ -17,7 +17,11 @@ distance apart); everything else must be contiguous.  Activations are bfloat16
 or float32, all of one dtype; parameters and states of the scan are float32.
 
 In a captured graph pass ``validate_cu=False`` (the check reads the offsets on
-the host).  To capture a training step, call the ``*_backward`` functions: a
+the host).  Offsets that then end before the batch does leave rows behind the
+last sequence, which no call writes: tensors that a call makes hold there what
+the memory held, tensors handed in keep what they had, and the differentiable
+forms, which would hand such rows on as gradients, fill their own with zeros.
+To capture a training step, call the ``*_backward`` functions: a
 captured ``.backward()`` must not meet leaves whose earlier autograd graph,
 made outside the capture, is still alive (PyTorch would tie the capture to
 the stream of that graph).
@@ -496,6 +500,11 @@ def _functions():
         return _FUNCTIONS
     torch = _torch()
 
+    def cleared(cu, validated, **like):
+        # rows behind offsets that nobody checked are not written: zeros for them
+        return {} if cu is None or validated else {
+            k: torch.zeros_like(t, memory_format=torch.contiguous_format) for k, t in like.items() if t is not None}
+
     def full(g, like):
         return torch.zeros_like(like, memory_format=torch.contiguous_format) if g is None else g.contiguous()
 
@@ -503,9 +512,10 @@ def _functions():
         @staticmethod
         def forward(ctx, x, weight, bias, initial_state, cu_seqlens, activation, validate_cu):
             y, final = short_conv_forward(x, weight, bias, initial_state=initial_state, cu_seqlens=cu_seqlens,
-                                          activation=activation, validate_cu=validate_cu)
+                                          activation=activation, validate_cu=validate_cu,
+                                          **cleared(cu_seqlens, validate_cu, y=x))
             ctx.save_for_backward(x, weight, bias, initial_state, cu_seqlens)
-            ctx.activation = activation
+            ctx.activation, ctx.validated = activation, validate_cu
             ctx.set_materialize_grads(False)
             return y, final
 
@@ -515,16 +525,17 @@ def _functions():
             x, weight, bias, init, cu = ctx.saved_tensors
             g = short_conv_backward(x, weight, full(dy, x), bias, initial_state=init,
                                     dfinal=None if dfinal is None else dfinal.contiguous(), cu_seqlens=cu,
-                                    activation=ctx.activation, validate_cu=False)
+                                    activation=ctx.activation, validate_cu=False, out=cleared(cu, ctx.validated, dx=x))
             return g["dx"], g["dweight"], g["dbias"], g["dinitial"], None, None, None
 
     class SelectiveScan(torch.autograd.Function):
         @staticmethod
         def forward(ctx, x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, dt_softplus, validate_cu):
             o, ht = selective_scan_forward(x, dt, A, B, C, D, z, dt_bias, h0=h0, cu_seqlens=cu_seqlens,
-                                           dt_softplus=dt_softplus, validate_cu=validate_cu)
+                                           dt_softplus=dt_softplus, validate_cu=validate_cu,
+                                           **cleared(cu_seqlens, validate_cu, o=x))
             ctx.save_for_backward(x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens)
-            ctx.dt_softplus = dt_softplus
+            ctx.dt_softplus, ctx.validated = dt_softplus, validate_cu
             ctx.set_materialize_grads(False)
             return o, ht
 
@@ -534,7 +545,8 @@ def _functions():
             x, dt, A, B, C, D, z, dt_bias, h0, cu = ctx.saved_tensors
             g = selective_scan_backward(x, dt, A, B, C, full(do, x), D, z, dt_bias, h0=h0,
                                         dht=None if dht is None else dht.contiguous(), cu_seqlens=cu,
-                                        dt_softplus=ctx.dt_softplus, validate_cu=False)
+                                        dt_softplus=ctx.dt_softplus, validate_cu=False,
+                                        out=cleared(cu, ctx.validated, dx=x, ddt=dt, dB=B, dC=C, dz=z))
             return (g["dx"], g["ddt"], g["dA"], g["dB"], g["dC"], g["dD"], g["dz"], g["ddt_bias"], g["dh0"], None,
                     None, None)
 

@@ -133,3 +133,50 @@ def test_infinities_next_to_padding(where, D, N, dtype):
         oi = kda.selective_scan_step(state=state, **tok)
         if 68 <= i < 74:
             same_kind(f"step {i}", oi, ro[:, i])
+
+
+# ---------------------------------------------------------------- rows behind the last sequence
+def soiled(*shape, dtype):
+    """Leaves NaN in the memory that the next tensor of this size is made of."""
+    torch.full(shape, float("nan"), dtype=dtype, device="cuda")
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rows_behind_the_last_sequence(dtype):
+    """Offsets that nobody checks (as in a captured graph) and that end before the batch does: the differentiable
+    forms give zeros there, and gradients of zero, in place of what the memory held."""
+    gen = torch.Generator().manual_seed(70)
+    r = lambda *s: torch.randn(*s, generator=gen).to(dtype).cuda()  # noqa: E731
+    T, end, D, N = 190, 131, 24, 8
+    cu = torch.tensor([0, 40, end], dtype=torch.int32).cuda()
+    f = lambda *s: torch.randn(*s, generator=gen).cuda()  # noqa: E731
+    note(f"rows behind the last sequence {dtype}")
+    for _ in range(8):
+        soiled(1, T, D, dtype=dtype)
+        soiled(1, T, 1, N, dtype=dtype)
+    x, w, dy = r(1, T, D), f(D, 4), r(1, T, D)
+    lead = lambda t: t[:, :end].contiguous()  # noqa: E731
+    xl = x.clone().requires_grad_()
+    y, _ = kda.short_conv(xl, w, cu_seqlens=cu, validate_cu=False)
+    y.backward(dy)
+    ys, _ = kda.short_conv_forward(lead(x), w, cu_seqlens=cu)
+    gs = kda.short_conv_backward(lead(x), w, lead(dy), cu_seqlens=cu)
+    for got, want in ((y, ys), (xl.grad, gs["dx"])):
+        assert torch.equal(got[:, :end], want) and not got[:, end:].any()
+    p = dict(x=r(1, T, D), dt=r(1, T, D), A=-torch.exp(f(D, N)), B=r(1, T, 1, N), C=r(1, T, 1, N), D=f(D), z=r(1, T, D),
+             dt_bias=f(D))
+    do = r(1, T, D)
+    leaves = {k: v.clone().requires_grad_() for k, v in p.items()}
+    o, _ = kda.selective_scan(**leaves, cu_seqlens=cu, validate_cu=False)
+    o.backward(do)
+    torch.cuda.synchronize()
+    cut = {k: (lead(v) if k in ("x", "dt", "B", "C", "z") else v) for k, v in p.items()}
+    ro, _, mo, _ = ref.scan(**cut, cu=cu)
+    check("o", o[:, :end], ro, mo, 64 + 8 * end)
+    assert not o[:, end:].any()
+    rg, rm = ref.scan_grad(**cut, do=lead(do), cu=cu)
+    for key in ("x", "dt", "B", "C", "z"):
+        check("d" + key, leaves[key].grad[:, :end], rg["d" + key], rm["d" + key], 128 + 16 * end)
+        assert not leaves[key].grad[:, end:].any(), key
+    for key in ("A", "D", "dt_bias"):
+        check("d" + key, leaves[key].grad, rg["d" + key], rm["d" + key], 128 + 17 * end)
