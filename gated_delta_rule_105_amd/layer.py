@@ -173,12 +173,20 @@ class _On:
             c.__exit__(*exc)
 
 
+def _written(t):
+    """Tell autograd that a caller's tensor is written, which it cannot see: a gradient that still needs what the
+    tensor held is then an error."""
+    _torch().autograd.graph.increment_version(t)
+
+
 def _new(t, like, name, dev, shape, dtype=None):
     """A caller's output, checked, or a new one (in `like`'s dtype unless given); and its address."""
     if t is None:
         t = like.new_empty(shape) if dtype is None else like.new_empty(shape, dtype=dtype)
         return t, t.data_ptr()
-    return t, _like(name, t, dev, like.dtype if dtype is None else dtype, shape)
+    address = _like(name, t, dev, like.dtype if dtype is None else dtype, shape)
+    _written(t)
+    return t, address
 
 
 def _out(out, name, shape, dtype, dev):
@@ -188,7 +196,9 @@ def _out(out, name, shape, dtype, dev):
         t = _torch().empty(shape, dtype=dtype, device=dev)
         out[name] = t
         return t.data_ptr()
-    return _like(name, t, dev, dtype, shape)
+    address = _like(name, t, dev, dtype, shape)
+    _written(t)
+    return address
 
 
 def _workspace(workspace, need, dev):
@@ -259,6 +269,7 @@ def short_conv_step(x, weight, state, bias=None, *, activation="silu", y=None, s
     with _On(dev, stream) as st:
         y, py = _new(y, x, "y", dev, (N, D))
         layer_call("kda_short_conv_step", desc, px, pw, pb, ps, py, st)
+    _written(state)
     return y
 
 
@@ -368,6 +379,7 @@ def selective_scan_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, *, 
     with _On(dev, stream) as st:
         o, po = _new(o, x, "o", dev, (S, ch))
         layer_call("kda_selective_scan_step", desc, *ptrs, ps, po, st)
+    _written(state)
     return o
 
 

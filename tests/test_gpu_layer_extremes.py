@@ -180,3 +180,39 @@ def test_rows_behind_the_last_sequence(dtype):
         assert not leaves[key].grad[:, end:].any(), key
     for key in ("A", "D", "dt_bias"):
         check("d" + key, leaves[key].grad, rg["d" + key], rm["d" + key], 128 + 17 * end)
+
+
+# ---------------------------------------------------------------- states updated in place
+def test_updates_in_place_are_seen_by_autograd():
+    """A state that a gradient still needs and that a step then overwrites is an error, as with any operation in
+    place, and not a wrong gradient; so is an output written over an input that was kept."""
+    gen = torch.Generator().manual_seed(80)
+    r = lambda *s: torch.randn(*s, generator=gen).cuda()  # noqa: E731
+    D, N, T = 8, 4, 20
+    note("updates in place")
+    w, x = r(D, 4).requires_grad_(), r(1, T, D)
+    conv = r(1, 3, D)
+    y, _ = kda.short_conv(x, w, initial_state=conv)
+    kda.short_conv_step(x[:, 0], w, conv)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+    A, B, C, h = (-torch.exp(r(D, N))).requires_grad_(), r(1, T, 1, N), r(1, T, 1, N), r(1, D, N)
+    o, _ = kda.selective_scan(x, x, A, B, C, h0=h)
+    kda.selective_scan_step(x[:, 0], x[:, 0], A, B[:, 0], C[:, 0], h)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        o.sum().backward()
+    q = r(2, 5, 2, 32)
+    k, wq = r(2, 5, 2, 32), r(32).requires_grad_()
+    out, _ = kda.qk_norm(q, k, wq)
+    kda.qk_norm_forward(k, k, q_out=q)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        out.sum().backward()
+    out, _ = kda.qk_norm(q, k, wq)
+    kda.qk_norm_backward(k, k, k, k, out=dict(dq=q))
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        out.sum().backward()
+    with torch.inference_mode():  # tensors that have no version
+        conv, h = r(1, 3, D), r(1, D, N)
+        y = kda.short_conv_step(x[:, 0], w, conv)
+        kda.selective_scan_step(y, y, A, B[:, 0], C[:, 0], h)
+    torch.cuda.synchronize()
