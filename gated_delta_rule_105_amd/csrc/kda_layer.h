@@ -135,6 +135,15 @@ inline ScanPlan plan_scan(int64_t tokens, int rows, int64_t T, bool packed, int 
 int launch_scan_forward(int is_bf16, const ScanArgs& a, const ScanPlan& p, void* o, float* ht, void* ws, void* stream);
 int launch_scan_step(int is_bf16, const ScanArgs& a, float* state, void* o, void* stream);
 
+// One token: lanes of a channel, four states each, and sequences a lane:
+// several, whose rates are then loaded once, where that leaves 16 waves a
+// compute unit.
+constexpr int kScanStepSeqs = 3;
+inline int scan_step_lanes(int N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
+inline int scan_step_seqs(int64_t tokens, int D, int N) {
+  return tokens * D * scan_step_lanes(N) >= (int64_t)kScanStepSeqs * 256 * 16 * 64 ? kScanStepSeqs : 1;
+}
+
 // Waves per workgroup of the backward scan; each workgroup leaves dB and dC of
 // its 16 channels as one row of partial sums.  (8 waves leave half the rows,
 // but measured 13 % slower: the barrier of every 16 tokens then holds up

@@ -591,7 +591,6 @@ scan_chain(const float* __restrict__ A, int64_t dn, int N, int D, int n_slots, f
 // 26.6 with four, 32 with one; 28.8 with loads and stores that bypass the
 // caches, with four).  Without VEC (N no multiple of 4) the same states are
 // loaded one by one.
-constexpr int kStepSeqs = 3;
 template <typename T, int LPC, bool VEC, int SEQS>
 __global__ void __launch_bounds__(256)
 scan_step(const ScanArgs a, float* __restrict__ state, T* __restrict__ o, int n_far) {
@@ -1183,17 +1182,16 @@ int step_t(const ScanArgs& a, float* state, void* o, hipStream_t st) {
     return (int)launch_kernel(scan_step<T, lpc.value, vec.value, seqs.value>, dim3((unsigned)blocks), dim3(256), st, a,
                               state, (T*)o, (int)n_far);
   };
-  // several sequences a lane once that leaves 16 waves a compute unit: the rates are then loaded once for them
+  const int per_channel = scan_step_lanes(a.N);
   auto shape = [&](auto lpc, auto vec) {
-    return a.tokens * a.D * lpc.value >= (int64_t)kStepSeqs * 256 * 16 * 64
-               ? go(lpc, vec, std::integral_constant<int, kStepSeqs>{})
-               : go(lpc, vec, std::integral_constant<int, 1>{});
+    return scan_step_seqs(a.tokens, a.D, a.N) > 1 ? go(lpc, vec, std::integral_constant<int, kScanStepSeqs>{})
+                                                  : go(lpc, vec, std::integral_constant<int, 1>{});
   };
   auto lanes = [&](auto vec) {
-    if (a.N <= 4) return shape(std::integral_constant<int, 1>{}, vec);
-    if (a.N <= 8) return shape(std::integral_constant<int, 2>{}, vec);
-    if (a.N <= 16) return shape(std::integral_constant<int, 4>{}, vec);
-    if (a.N <= 32) return shape(std::integral_constant<int, 8>{}, vec);
+    if (per_channel == 1) return shape(std::integral_constant<int, 1>{}, vec);
+    if (per_channel == 2) return shape(std::integral_constant<int, 2>{}, vec);
+    if (per_channel == 4) return shape(std::integral_constant<int, 4>{}, vec);
+    if (per_channel == 8) return shape(std::integral_constant<int, 8>{}, vec);
     return shape(std::integral_constant<int, 16>{}, vec);
   };
   return a.N % 4 == 0 ? lanes(std::true_type{}) : lanes(std::false_type{});

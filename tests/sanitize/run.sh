@@ -16,4 +16,4 @@ export ASAN_OPTIONS=detect_leaks=0:abort_on_error=1
 export UBSAN_OPTIONS=print_stacktrace=1:halt_on_error=1
 export KDA_LIBRARY="$O/libkda.so" KDA_ORACLE_LIBRARY="$O/libkda_oracle.so"
 cd "$R"
-python -m pytest tests/test_abi.py tests/test_layer_abi.py tests/test_oracle_pins.py tests/test_oracle_bwd_pins.py -q -s -m "not gpu" -p no:cacheprovider
+python -m pytest tests/test_abi.py tests/test_layer_abi.py tests/test_layer_abi_limits.py tests/test_oracle_pins.py tests/test_oracle_bwd_pins.py -q -s -m "not gpu" -p no:cacheprovider
