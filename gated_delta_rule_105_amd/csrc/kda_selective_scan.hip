@@ -151,7 +151,7 @@ __device__ __forceinline__ void store_state(float* __restrict__ p, int64_t row, 
 // part is added to v's exponent.  (The rest is above 1/2 and at most 1: the
 // product stays in range before that.)
 __device__ __forceinline__ float scaled(float x, float v) {
-  const float t = __builtin_amdgcn_fmed3f(x, -1e30f, 1e30f), whole = __builtin_ceilf(t);
+  const float t = __builtin_amdgcn_fmed3f(x, -1e9f, 1e9f), whole = __builtin_ceilf(t);
   return __builtin_amdgcn_ldexpf(v * exp2_fast(t - whole), (int)whole);
 }
 
