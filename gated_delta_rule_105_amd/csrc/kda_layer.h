@@ -103,8 +103,13 @@ inline ScanPlan plan_scan(int64_t tokens, int rows, int64_t T, bool packed, int 
   if (tokens == 0) {
     p.slot = 1;
     p.n_slots = 1;
-  } else if (!packed && waves * rows >= 6 * cus) {
-    p.slot = T;  // the rows alone put a wave on every SIMD: no slots to chain, a token is scanned once
+  } else if (!packed && waves * rows >= 4 * cus) {
+    // The rows alone put a wave on every SIMD: no slots to chain, a token is
+    // scanned once.  Rows of 2048 tokens of 2048 channels, bf16, as slots and
+    // cut: 6 of them (3 waves a compute unit) 226 and 191 us, 8 (4) 226 and 237,
+    // 16 332 and 428; rows of 1000 tokens of 4096: 3 of them (3) 111 and 105, 6
+    // (6) 167 and 193.
+    p.slot = T;
     p.n_slots = rows;
   } else {
     // waves for 32 a compute unit, twice what it holds at once.  1 x 4096
