@@ -216,3 +216,26 @@ def test_updates_in_place_are_seen_by_autograd():
         y = kda.short_conv_step(x[:, 0], w, conv)
         kda.selective_scan_step(y, y, A, B[:, 0], C[:, 0], h)
     torch.cuda.synchronize()
+
+
+# ---------------------------------------------------------------- angles beside a quarter turn's multiples
+def test_angles_beside_quarter_turns():
+    """fp32 angles next to multiples of a quarter turn: the small one of cosine and sine keeps its relative accuracy.
+    The unit vector (1, 0) gives both as they are.  The product and the turn are off by a few 2^-53 of the angle, the
+    rest of the turn is rounded once (2^-24 of itself), cosine and sine take under 4 roundings each."""
+    note("qk_norm quarter turns")
+    gen = torch.Generator().manual_seed(90)
+    quarter = torch.tensor(torch.pi / 2).float()
+    freq = quarter * torch.tensor([1.0, 2.0, 3.0, 5.0, 0.25]) * (1 + torch.randint(-4, 5, (5,), generator=gen) * 2.0 ** -23)
+    pos = torch.tensor([0, 1, 2, 3, 4, 5, 6, 7, 100, 4099, -3, -1026], dtype=torch.int32)
+    outs = []
+    for i in range(5):  # one pair at a time, so that the vector is a unit
+        x = torch.zeros(len(pos), 1, 10)
+        x[..., i] = 1.0
+        outs.append(kda.qk_norm_forward(x.cuda(), x.cuda(), None, None, pos.cuda(), freq.cuda(), eps=0.0)[0].cpu())
+    angle = pos.double()[:, None] * freq.double()
+    room = 8 * 2.0 ** -53 * angle.abs()
+    for i in range(5):
+        for at, want in ((i, torch.cos(angle[:, i])), (5 + i, torch.sin(angle[:, i]))):
+            got = outs[i][:, 0, at].double()
+            assert ((got - want).abs() <= 6 * 2.0 ** -24 * want.abs() + room[:, i]).all(), (i, at)
