@@ -182,6 +182,37 @@ def test_rows_behind_the_last_sequence(dtype):
         check("d" + key, leaves[key].grad, rg["d" + key], rm["d" + key], 128 + 17 * end)
 
 
+def test_rows_behind_the_last_sequence_in_a_graph():
+    """One captured call serves batches of other lengths: the offsets are rewritten between replays, and each replay
+    gives what an eager call gives, zeros behind the last sequence among it."""
+    gen = torch.Generator().manual_seed(71)
+    r = lambda *s: torch.randn(*s, generator=gen).cuda()  # noqa: E731
+    T, D, N = 300, 40, 12
+    cu = torch.tensor([0, 100, 300], dtype=torch.int32).cuda()
+    x, dt, z, w = r(1, T, D), r(1, T, D), r(1, T, D), r(D, 4)
+    A, B, C = -torch.exp(r(D, N)), r(1, T, 1, N), r(1, T, 1, N)
+    note("rows behind the last sequence in a graph")
+
+    def call():
+        y, conv = kda.short_conv(x, w, cu_seqlens=cu, validate_cu=False)
+        o, h = kda.selective_scan(y, dt, A, B, C, None, z, cu_seqlens=cu, validate_cu=False)
+        return y, conv, o, h
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call()
+    for ends in ([0, 100, 300], [0, 7, 90], [0, 0, 0], [0, 299, 300]):
+        cu.copy_(torch.tensor(ends, dtype=torch.int32))
+        x.copy_(r(1, T, D))
+        want = [t.clone() for t in call()]
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want)), ends
+        assert not out[0][:, ends[-1]:].any() and not out[2][:, ends[-1]:].any(), ends
+
+
 # ---------------------------------------------------------------- states updated in place
 def test_updates_in_place_are_seen_by_autograd():
     """A state that a gradient still needs and that a step then overwrites is an error, as with any operation in
