@@ -23,8 +23,8 @@
 // this one is used.  Every wave's token range is uniform: where its sequences
 // begin and end is scalar control flow.  A last vector that would pass the end
 // of the row is moved back to end with it; its channels overlap the
-// neighbour's and both write the same values (the step, which updates in
-// place, takes single channels instead when vectors do not divide the row).
+// neighbour's and both write the same values.  The step, which updates in
+// place, takes single channels.
 #include "kda_layer_device.h"
 
 namespace kda {
@@ -144,49 +144,41 @@ __global__ void __launch_bounds__(256) conv_forward(const ConvArgs a, T* __restr
   }
 }
 
-// One token: a lane owns V channels of kStepSeqs sequences, n_far apart, so
-// that the taps are loaded once for all of them and the rows of all are under
-// way together (one or four sequences a lane measure the same within 3 %).
+// One token: a lane owns a channel of kStepSeqs sequences, n_far apart, so that
+// the taps are loaded once for all of them and the rows of all are under way
+// together (4096 sequences of 6144 channels, 4 taps: bf16 77 us with two, 91 with
+// one, 77 with four; fp32 142, 136, 149).  Vectors of channels, 16 bytes a lane,
+// measured 105 and 148 us there, 16.5 against 17.6 with 2 taps in fp32 for 1024
+// sequences, and the same 8.5 for 256 sequences in bf16.
 constexpr int kStepSeqs = 2;
-template <typename T, int V, int W, bool SILU>
-__global__ void __launch_bounds__(256) conv_step(const ConvArgs a, T* __restrict__ state, T* __restrict__ y,
-                                                 int n_vec, int n_far) {
+template <typename T, int W, bool SILU>
+__global__ void __launch_bounds__(256) conv_step(const ConvArgs a, T* __restrict__ state, T* __restrict__ y, int n_far) {
   const uint32_t id = blockIdx.x * 256u + threadIdx.x;
-  const int n0 = (int)(id / (uint32_t)n_vec);
-  const int c = (int)(id - (uint32_t)n0 * (uint32_t)n_vec) * V;
+  const int n0 = (int)(id / (uint32_t)a.D), c = (int)(id - (uint32_t)n0 * (uint32_t)a.D);
   if (n0 >= n_far) return;
   const T* __restrict__ x = (const T*)a.x;
-  typename Pack<T, V>::type rows[kStepSeqs][W];
+  T rows[kStepSeqs][W];
 #pragma unroll
   for (int q = 0; q < kStepSeqs; ++q) {
     const int64_t n = n0 + q * n_far < a.tokens ? n0 + q * n_far : n0;
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j)
-      rows[q][j] = *(const typename Pack<T, V>::type*)(state + (n * (W - 1) + j) * a.D + c);
-    rows[q][W - 1] = *(const typename Pack<T, V>::type*)(x + n * a.ld + c);
+    for (int j = 0; j < W - 1; ++j) rows[q][j] = state[(n * (W - 1) + j) * a.D + c];
+    rows[q][W - 1] = x[n * a.ld + c];
   }
-  float taps[W][V], b[V];
-  load_taps<V, W>(a.w, a.bias, c, taps, b);
+  float taps[W][1], b[1];
+  load_taps<1, W>(a.w, a.bias, c, taps, b);
 #pragma unroll
   for (int q = 0; q < kStepSeqs; ++q) {
     const int64_t n = n0 + q * n_far;
     if (n >= a.tokens) break;
-    float u[V];
+    float u = b[0];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      u[i] = b[i];
-#pragma unroll
-      for (int j = 0; j < W; ++j) {
-        if constexpr (V == 1) u[i] += taps[j][i] * Elem<T>::to_f32(rows[q][j]);
-        else u[i] += taps[j][i] * Elem<T>::to_f32(rows[q][j][i]);
-      }
-      if (SILU) u[i] *= sigmoid(u[i]);
-    }
+    for (int j = 0; j < W; ++j) u += taps[j][0] * Elem<T>::to_f32(rows[q][j]);
+    if (SILU) u *= sigmoid(u);
     // the inputs move up a row as they are
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j)
-      *(typename Pack<T, V>::type*)(state + (n * (W - 1) + j) * a.D + c) = rows[q][j + 1];
-    store_vec<T, V>(y + n * a.D + c, u);
+    for (int j = 0; j < W - 1; ++j) state[(n * (W - 1) + j) * a.D + c] = rows[q][j + 1];
+    y[n * a.D + c] = Elem<T>::from_f32(u);
   }
 }
 
@@ -377,13 +369,11 @@ int forward_t(const ConvArgs& a, void* y, void* fin, hipStream_t st) {
   const dim3 grid((unsigned)(a.n_part + states), (unsigned)ceil_div(ceil_div(a.D, V), 64));
   return (int)launch_kernel(conv_forward<T, V, W, SILU>, grid, dim3(256), st, a, (T*)y, (T*)fin);
 }
-template <typename T, int V, int W, bool SILU>
+template <typename T, int W, bool SILU>
 int step_t(const ConvArgs& a, void* state, void* y, hipStream_t st) {
-  const int n_vec = a.D / V;
-  const int64_t n_far = ceil_div(a.tokens, kStepSeqs), threads = ceil_div(n_far * n_vec, 256) * 256;
-  if (threads > INT32_MAX) return (int)hipErrorInvalidValue;
-  return (int)launch_kernel(conv_step<T, V, W, SILU>, dim3((unsigned)(threads / 256)), dim3(256), st, a, (T*)state,
-                            (T*)y, n_vec, (int)n_far);
+  const int64_t n_far = ceil_div(a.tokens, kStepSeqs), groups = ceil_div(n_far * a.D, 256);
+  return (int)launch_kernel(conv_step<T, W, SILU>, dim3((unsigned)groups), dim3(256), st, a, (T*)state, (T*)y,
+                            (int)n_far);
 }
 template <typename T, int V, int W, bool SILU>
 int backward_t(const ConvArgs& a, const void* dy, const void* dfin, void* dx, float* dw, float* db, void* dinit,
@@ -400,9 +390,8 @@ int backward_t(const ConvArgs& a, const void* dy, const void* dfin, void* dx, fl
 }
 
 // Chooses the instance: type, taps, activation, and vectors of VEC channels
-// or single ones when a row has fewer than VEC (or, with EXACT, when VEC does
-// not divide the row).
-template <typename T, int VEC, bool EXACT, typename F>
+// or single ones when a row has fewer than VEC.
+template <typename T, int VEC, typename F>
 int dispatch_t(int width, int silu, int D, F&& f) {
   auto w = [&](auto vec) {
     auto act = [&](auto taps) {
@@ -412,30 +401,28 @@ int dispatch_t(int width, int silu, int D, F&& f) {
            : width == 3 ? act(std::integral_constant<int, 3>{})
                         : act(std::integral_constant<int, 4>{});
   };
-  return D < VEC || (EXACT && D % VEC != 0) ? w(std::integral_constant<int, 1>{})
-                                            : w(std::integral_constant<int, VEC>{});
+  return D < VEC ? w(std::integral_constant<int, 1>{}) : w(std::integral_constant<int, VEC>{});
 }
-template <bool BACKWARD, bool EXACT, typename F>
+template <int VEC_BF16, int VEC_F32, typename F>
 int dispatch(int is_bf16, int width, int silu, int D, F&& f) {
-  return is_bf16 ? dispatch_t<bf16_t, conv_vec(true, BACKWARD), EXACT>(width, silu, D, f)
-                 : dispatch_t<float, conv_vec(false, BACKWARD), EXACT>(width, silu, D, f);
+  return is_bf16 ? dispatch_t<bf16_t, VEC_BF16>(width, silu, D, f) : dispatch_t<float, VEC_F32>(width, silu, D, f);
 }
 
 }  // namespace
 
 int launch_conv_forward(int is_bf16, int width, int silu, const ConvArgs& a, void* y, void* fin, void* stream) {
-  return dispatch<false, false>(is_bf16, width, silu, a.D, [&](auto t, auto vec, auto taps, auto act) {
+  return dispatch<conv_vec(true, false), conv_vec(false, false)>(is_bf16, width, silu, a.D, [&](auto t, auto vec, auto taps, auto act) {
     return forward_t<decltype(t), vec.value, taps.value, act.value>(a, y, fin, (hipStream_t)stream);
   });
 }
 int launch_conv_step(int is_bf16, int width, int silu, const ConvArgs& a, void* state, void* y, void* stream) {
-  return dispatch<false, true>(is_bf16, width, silu, a.D, [&](auto t, auto vec, auto taps, auto act) {
-    return step_t<decltype(t), vec.value, taps.value, act.value>(a, state, y, (hipStream_t)stream);
+  return dispatch<1, 1>(is_bf16, width, silu, a.D, [&](auto t, auto, auto taps, auto act) {
+    return step_t<decltype(t), taps.value, act.value>(a, state, y, (hipStream_t)stream);
   });
 }
 int launch_conv_backward(int is_bf16, int width, int silu, const ConvArgs& a, const void* dy, const void* dfin,
                          void* dx, float* dw, float* db, void* dinit, float* part, void* stream) {
-  return dispatch<true, false>(is_bf16, width, silu, a.D, [&](auto t, auto vec, auto taps, auto act) {
+  return dispatch<conv_vec(true, true), conv_vec(false, true)>(is_bf16, width, silu, a.D, [&](auto t, auto vec, auto taps, auto act) {
     return backward_t<decltype(t), vec.value, taps.value, act.value>(a, dy, dfin, dx, dw, db, dinit, part,
                                                                      (hipStream_t)stream);
   });
