@@ -17,16 +17,17 @@
 // A wave keeps the cosines and sines of a token while it goes through the
 // token's heads: they are taken in quarter turns, reduced in 64 bits, because
 // fp32 would lose the angle of a far position (2^-24 of a million is 0.06
-// revolutions); the rest, an eighth of a turn at most, is rounded to
-// fp32 once, 2^-24 of itself.  Heads are loaded kNormBatch groups at a time before the
-// first is used.
+// revolutions); the rest, an eighth of a turn at most, is rounded to fp32
+// once, 2^-24 of itself.  Heads are loaded kNormBatch groups at a time before
+// the first is used.
 //
 // Measured: unit vectors of 4096 tokens, 16 + 16 heads of 128, bf16, 12.8 us
 // (67.1 MB, 5.2 TB/s); 8192 tokens of 32 + 8 heads of 128, half rotated, 31 us
 // (167.8 MB, 5.4 TB/s; a large copy reaches 4.9 beyond the last-level cache);
 // 8 tokens 4.8 us, which is the launch and one token's chain of loads, angles
-// and sums; backward 8192 tokens of 16 + 4 heads of 64, fp32, 31.8 us and 4
-// for the weights' sums (125.8 MB).
+// and sums; backward 8192 tokens of 16 + 4 heads of 64, 32 us in fp32 (125.8
+// MB) and 23.6 in bf16 (62.9), which waits for its loads (34 and 48 % vector
+// issue), and 4 for the weights' sums.
 #include "kda_layer_device.h"
 
 namespace kda {

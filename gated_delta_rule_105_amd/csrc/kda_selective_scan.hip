@@ -17,12 +17,12 @@
 // two to four of the others.
 //
 // Measured in bf16 at 16 states.  1 x 4096 tokens of 4096 channels: 135 us,
-// of which the states of the slots 50 to 60, the chain 9 and the outputs 70 to 85;
-// 28 us would move the bytes (135 MB), and the two scans issue vector
-// instructions in 75 and 81 % of their cycles.  8 x 2048 tokens of the same,
-// whose rows need no slots: 334 us.  Backward 2 x 2048 tokens of 2048
-// channels: 234 us, states 60, chain 8, main 168 (84 % vector issue), sums
-// 15; 24 us would move the bytes.
+// of which (under the profiler, which adds a sixth) the states of the slots 62,
+// the chain 9 and the outputs 86; 28 us would move the bytes (135 MB), and the
+// two scans issue vector instructions in 76 and 82 % of their cycles.  8 x 2048
+// tokens of the same, whose rows need no slots: 334 us.  Backward 2 x 2048
+// tokens of 2048 channels: 239 us, of which (likewise) states 67 (65 % vector
+// issue), chain 9, main 180 (84 %), sums 15; 24 us would move the bytes.
 //
 // Layout of the forward scans ("quads").  A wave holds 16 channels, lane l
 // channel l / 4 and the quarter l % 4 of its states (NS of them), so four
@@ -587,10 +587,9 @@ scan_chain(const float* __restrict__ A, int64_t dn, int N, int D, int n_slots, f
 // lane owns 4 consecutive states (16 bytes) of a channel in SEQS sequences,
 // n_far apart, LPC lanes a channel, so that the rates are loaded once for the
 // sequences and the loads of all are under way together (256 sequences, 4096
-// channels, 16 states: 24.3 us with three sequences a lane, 26.0 with two,
-// 26.6 with four, 32 with one; 28.8 with loads and stores that bypass the
-// caches, with four).  Without VEC (N no multiple of 4) the same states are
-// loaded one by one.
+// channels, 16 states: 22.0 us, 142.9 MB; loads and stores that bypass the
+// caches cost 8 % more).  Without VEC (N no multiple of 4) the same states are
+// loaded one by one, which takes the same call 52 us.
 template <typename T, int LPC, bool VEC, int SEQS>
 __global__ void __launch_bounds__(256)
 scan_step(const ScanArgs a, float* __restrict__ state, T* __restrict__ o, int n_far) {

@@ -402,9 +402,19 @@ int kda_decode_step_gated(int N, int H, int d_k, int d_v, kda_dtype_t dtype, kda
  *     one distance serves every batch row.  A row itself is contiguous.
  *   - Inputs and outputs need the alignment of their elements only (a slice
  *     starts anywhere); the workspace needs 256 bytes.
- *   - There is no floor and no sign rule on any input.
+ *   - There is no floor and no sign rule on any input.  The scan's states may
+ *     grow as well as shrink (rates above zero, steps of either sign): they
+ *     are what the recurrence gives while that stays inside fp32.
  *   - Packed batches: cu_seqlens as kda_chunk_forward.  Sequences may be
- *     empty (their final state is their initial state).
+ *     empty (their final state is their initial state).  Offsets that break
+ *     those rules give wrong results, but no access outside the arrays; rows
+ *     behind an offset cu[n_seqs] < T are not written.
+ *   - Parameters (weight, A) are read, and not NULL, also without tokens.
+ *   - KDA_ERR_UNSUPPORTED: 2^31 - 4096 tokens or more; what the descriptors
+ *     state; more than 2^23 channels of a convolution; rows of x, dt or z
+ *     more than 2^24 elements apart, or D N above 2^28, in a scan; a step of
+ *     2^31 elements (convolution) or 2^27 channels (scan) or more; a batch
+ *     that needs 2^32 threads or more along a launch's first dimension.
  *   - Sums, states and statistics are held in fp32, outputs are rounded once.
  *     Results do not depend on the launch: no atomics, every sum has a fixed
  *     order.
@@ -528,7 +538,10 @@ int kda_selective_scan_step(const kda_scan_desc_t* d, const void* x, const void*
  *   dz      : [B, T, D] dtype; required with z, ignored without
  *   dh0     : [S, D, N] fp32 or NULL (not written)
  * The workspace holds the state before every 16 tokens (N / 4 bytes per token
- * and channel), the states between ranges of tokens, and partial sums.
+ * and channel), the dB and dC of every 16 channels in fp32 (N / 2 bytes per
+ * token and channel), the states between ranges of tokens, and smaller sums:
+ * some 3/4 N bytes per token and channel, 100 MB for 2 x 2048 tokens of 2048
+ * channels with 16 states.  Long sequences are not cut into windows.
  * Outputs must not overlap each other, the inputs or the workspace.
  */
 int kda_selective_scan_backward_workspace_size(const kda_scan_desc_t* d, size_t* bytes);
