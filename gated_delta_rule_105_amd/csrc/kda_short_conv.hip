@@ -11,8 +11,9 @@
 // Measured: forward 4096 tokens of 6144 channels, bf16, 20.5 us (100.8 MB,
 // 4.9 TB/s, what a large copy reaches); 5003 packed tokens of 1011 channels,
 // fp32, 10.2 us (4.0 TB/s: some 1300 waves, one batch each); one token for
-// 256 sequences of 6144 channels 8.4 us (3.0 TB/s, one load's latency and the
-// launch); backward 2 x 4096 tokens of 4096 channels, bf16, 46 us and 4.6 for
+// 256 sequences of 6144 channels 6.4 us (3.9 TB/s, one load's latency and the
+// launch; 8.5 between calls that follow one another, which is the host's);
+// backward 2 x 4096 tokens of 4096 channels, bf16, 46 us and 4.6 for
 // the parameters' sums (201.5 MB necessary, 224 moved: batches that run past
 // a tile are read twice).
 //
@@ -149,7 +150,7 @@ __global__ void __launch_bounds__(256) conv_forward(const ConvArgs a, T* __restr
 // together (4096 sequences of 6144 channels, 4 taps: bf16 77 us with two, 91 with
 // one, 77 with four; fp32 142, 136, 149).  Vectors of channels, 16 bytes a lane,
 // measured 105 and 148 us there, 16.5 against 17.6 with 2 taps in fp32 for 1024
-// sequences, and the same 8.5 for 256 sequences in bf16.
+// sequences, and 8.6 against 6.4 for 256 sequences in bf16.
 constexpr int kStepSeqs = 2;
 template <typename T, int W, bool SILU>
 __global__ void __launch_bounds__(256) conv_step(const ConvArgs a, T* __restrict__ state, T* __restrict__ y, int n_far) {
