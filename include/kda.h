@@ -542,6 +542,9 @@ int kda_selective_scan_step(const kda_scan_desc_t* d, const void* x, const void*
  * token and channel), the states between ranges of tokens, and smaller sums:
  * some 3/4 N bytes per token and channel, 100 MB for 2 x 2048 tokens of 2048
  * channels with 16 states.  Long sequences are not cut into windows.
+ * An infinity among dout reaches the earlier tokens of its sequence as an
+ * infinity or, where the decays of 16 tokens together fall below 2^-126, as a
+ * NaN.
  * Outputs must not overlap each other, the inputs or the workspace.
  */
 int kda_selective_scan_backward_workspace_size(const kda_scan_desc_t* d, size_t* bytes);
