@@ -13,6 +13,9 @@ missing library raises.
 The operators around the recurrence in a layer (layer.py) are the short causal
 convolution (short_conv*), the norm of queries and keys with the position
 rotation (qk_norm*) and the selective state space scan (selective_scan*).
+Those of block.py are linear attention with a decay for each head
+(linear_attn*), the norm of a block's heads with the output gate (gated_norm*)
+and the residual sum with the norm before the next block (residual_norm*).
 
 g selects the gate: [.., H, d] one log-decay per key channel (KDA), [.., H]
 one per head (Gated DeltaNet), None no decay (DeltaNet).
@@ -39,7 +42,11 @@ __all__ = ["chunk_forward", "chunk_forward_noalloc", "chunk_forward_states", "ch
            "short_conv", "short_conv_forward", "short_conv_step", "short_conv_backward",
            "selective_scan", "selective_scan_forward", "selective_scan_step", "selective_scan_backward",
            "selective_scan_workspace_bytes",
-           "qk_norm", "qk_norm_forward", "qk_norm_backward"]
+           "qk_norm", "qk_norm_forward", "qk_norm_backward",
+           "linear_attn", "linear_attn_forward", "linear_attn_step", "linear_attn_backward",
+           "linear_attn_workspace_bytes",
+           "gated_norm", "gated_norm_forward", "gated_norm_backward",
+           "residual_norm", "residual_norm_forward", "residual_norm_backward"]
 
 
 def _torch():
@@ -465,3 +472,6 @@ from .layer import (qk_norm, qk_norm_backward, qk_norm_forward, selective_scan, 
                     selective_scan_backward, selective_scan_forward, selective_scan_step,
                     selective_scan_workspace_bytes, short_conv, short_conv_backward, short_conv_forward,
                     short_conv_step)
+from .block import (gated_norm, gated_norm_backward, gated_norm_forward, linear_attn,  # noqa: E402
+                    linear_attn_backward, linear_attn_forward, linear_attn_step, linear_attn_workspace_bytes,
+                    residual_norm, residual_norm_backward, residual_norm_forward)

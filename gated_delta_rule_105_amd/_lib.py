@@ -26,8 +26,12 @@ KDA_GATE_HEAD = 1      # g [.., H]: Gated DeltaNet
 KDA_GATE_NONE = 2      # no g: DeltaNet
 KDA_ACT_NONE = 0
 KDA_ACT_SILU = 1
+KDA_ACT_SIGMOID = 2
 KDA_NORM_UNIT = 0
 KDA_NORM_RMS = 1
+KDA_DECAY_NONE = 0
+KDA_DECAY_HEAD = 1
+KDA_DECAY_TOKEN = 2
 
 # Every symbol include/kda.h declares.
 EXPORTS = ("kda_status_string", "kda_version", "kda_chunk_forward_workspace_size",
@@ -39,7 +43,11 @@ EXPORTS = ("kda_status_string", "kda_version", "kda_chunk_forward_workspace_size
            "kda_short_conv_forward", "kda_short_conv_step", "kda_short_conv_backward_workspace_size",
            "kda_short_conv_backward", "kda_selective_scan_workspace_size", "kda_selective_scan_forward",
            "kda_selective_scan_step", "kda_selective_scan_backward_workspace_size", "kda_selective_scan_backward",
-           "kda_qk_norm_forward", "kda_qk_norm_backward_workspace_size", "kda_qk_norm_backward")
+           "kda_qk_norm_forward", "kda_qk_norm_backward_workspace_size", "kda_qk_norm_backward",
+           "kda_linear_attn_workspace_size", "kda_linear_attn_forward", "kda_linear_attn_step",
+           "kda_linear_attn_backward_workspace_size", "kda_linear_attn_backward",
+           "kda_gated_norm_forward", "kda_gated_norm_backward_workspace_size", "kda_gated_norm_backward",
+           "kda_residual_norm_forward", "kda_residual_norm_backward_workspace_size", "kda_residual_norm_backward")
 
 # Launches of one kda_chunk_forward call, in stream order (kda_chunk_forward_timed):
 # the map sweep and the output sweep are the two instances of kda_chunk_sweep.
@@ -86,6 +94,21 @@ class NormDesc(ctypes.Structure):
                        (("eps", ctypes.c_float), ("q_scale", ctypes.c_float)), "ld_q ld_k")
 
 
+class LinearDesc(ctypes.Structure):
+    """Mirror of kda_linear_desc_t."""
+    _fields_ = _fields("B T Hq H d_k d_v n_seqs dtype decay", (("scale", ctypes.c_float),), "ld_q ld_k ld_v ld_g")
+
+
+class GatedNormDesc(ctypes.Structure):
+    """Mirror of kda_gated_norm_desc_t."""
+    _fields_ = _fields("n_tokens H d dtype activation", (("eps", ctypes.c_float),), "ld_x ld_gate")
+
+
+class ResidualNormDesc(ctypes.Structure):
+    """Mirror of kda_residual_norm_desc_t."""
+    _fields_ = _fields("n_tokens D dtype", (("scale", ctypes.c_float), ("eps", ctypes.c_float)), "ld_x ld_residual")
+
+
 # Pointer arguments of the operators around the recurrence, each call being
 # (descriptor, pointers ..., [workspace, workspace bytes,] stream).
 LAYER_CALLS = {
@@ -97,6 +120,16 @@ LAYER_CALLS = {
     "kda_selective_scan_backward": (ScanDesc, 21, True),
     "kda_qk_norm_forward": (NormDesc, 8, False),
     "kda_qk_norm_backward": (NormDesc, 12, True),
+}
+# The same of linear attention and of the norms at a block's end.
+BLOCK_CALLS = {
+    "kda_linear_attn_forward": (LinearDesc, 8, True),
+    "kda_linear_attn_step": (LinearDesc, 6, False),
+    "kda_linear_attn_backward": (LinearDesc, 13, True),
+    "kda_gated_norm_forward": (GatedNormDesc, 4, False),
+    "kda_gated_norm_backward": (GatedNormDesc, 7, True),
+    "kda_residual_norm_forward": (ResidualNormDesc, 6, False),
+    "kda_residual_norm_backward": (ResidualNormDesc, 10, True),
 }
 
 
@@ -155,12 +188,14 @@ def load(path: str = LIBRARY) -> ctypes.CDLL:
                                           ctypes.c_int, ctypes.c_int, ctypes.c_float, vp, vp, vp, vp, vp, vp, vp,
                                           vp]
     lib.kda_decode_step_gated.restype = ctypes.c_int
-    for name, (desc, n_ptr, ws) in LAYER_CALLS.items():
+    for name, (desc, n_ptr, ws) in (*LAYER_CALLS.items(), *BLOCK_CALLS.items()):
         fn = getattr(lib, name)
         fn.argtypes = [ctypes.POINTER(desc)] + [vp] * n_ptr + ([vp, sz] if ws else []) + [vp]
         fn.restype = ctypes.c_int
     for name, desc in (("kda_short_conv_backward", ConvDesc), ("kda_selective_scan", ScanDesc),
-                       ("kda_selective_scan_backward", ScanDesc), ("kda_qk_norm_backward", NormDesc)):
+                       ("kda_selective_scan_backward", ScanDesc), ("kda_qk_norm_backward", NormDesc),
+                       ("kda_linear_attn", LinearDesc), ("kda_linear_attn_backward", LinearDesc),
+                       ("kda_gated_norm_backward", GatedNormDesc), ("kda_residual_norm_backward", ResidualNormDesc)):
         fn = getattr(lib, name + "_workspace_size")
         fn.argtypes = [ctypes.POINTER(desc), ctypes.POINTER(sz)]
         fn.restype = ctypes.c_int
@@ -278,7 +313,7 @@ def layer_workspace_size(name: str, desc) -> int:
 
 
 def layer_call(name: str, desc, *args) -> None:
-    """Call one of LAYER_CALLS with raw integer addresses; raises KdaError unless it returns KDA_OK."""
+    """Call one of LAYER_CALLS or BLOCK_CALLS with raw integer addresses; raises KdaError unless it returns KDA_OK."""
     st = getattr(_lib or load(), name)(desc, *args)
     if st != KDA_OK:
         raise KdaError(st, name)

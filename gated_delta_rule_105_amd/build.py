@@ -18,7 +18,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(HERE, "libkda.so")
 SOURCES = ["kda_api.cpp", "kda_prefill.hip", "kda_decode.hip", "kda_backward.hip",
-           "kda_layer_api.cpp", "kda_short_conv.hip", "kda_selective_scan.hip", "kda_qk_norm.hip"]
+           "kda_layer_api.cpp", "kda_short_conv.hip", "kda_selective_scan.hip", "kda_qk_norm.hip",
+           "kda_block_api.cpp", "kda_linear_attn.hip", "kda_block_norm.hip"]
 PEAKS_SOURCES = ["kda_peaks.hip"]
 PEAKS_LIBRARY = os.path.join(HERE, "libkda_peaks.so")
 ARCH = os.environ.get("KDA_OFFLOAD_ARCH", "gfx950")

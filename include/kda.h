@@ -420,7 +420,7 @@ int kda_decode_step_gated(int N, int H, int d_k, int d_v, kda_dtype_t dtype, kda
  *     order.
  */
 
-typedef enum { KDA_ACT_NONE = 0, KDA_ACT_SILU = 1 } kda_act_t;
+typedef enum { KDA_ACT_NONE = 0, KDA_ACT_SILU = 1, KDA_ACT_SIGMOID = 2 } kda_act_t;
 typedef enum { KDA_NORM_UNIT = 0, KDA_NORM_RMS = 1 } kda_norm_t;
 
 /* Shape of one short convolution. */
@@ -431,7 +431,7 @@ typedef struct {
   int width;        /* taps: 2, 3 or 4                                       */
   int n_seqs;       /* 0: B sequences of T tokens; > 0: packed sequences     */
   kda_dtype_t dtype;/* dtype of x, y, the states and their gradients         */
-  kda_act_t activation;
+  kda_act_t activation; /* none or SiLU                                      */
   int64_t ld_x;     /* distance between token rows of x, in elements (0: D)  */
 } kda_conv_desc_t;
 
@@ -599,6 +599,170 @@ int kda_qk_norm_backward(const kda_qk_norm_desc_t* d, const void* q, const void*
                          const float* k_weight, const int32_t* positions, const float* inv_freq, const void* dq_out,
                          const void* dk_out, void* dq, void* dk, float* dq_weight, float* dk_weight, void* workspace,
                          size_t workspace_bytes, void* stream);
+
+/* ---- linear attention with a decay for each head -------------------------
+ *
+ * The recurrence without the delta rule's erase step, as decayed linear
+ * attention and state space layers in their attention form have it.  The
+ * conventions of the operators above hold, with slices, alignment, packed
+ * batches and unchecked offsets as there.
+ */
+
+typedef enum {
+  KDA_DECAY_NONE = 0,  /* g NULL: nothing is forgotten                       */
+  KDA_DECAY_HEAD = 1,  /* g [H] fp32: one log decay for each head            */
+  KDA_DECAY_TOKEN = 2  /* g [B, T, H] dtype: one for each token and head     */
+} kda_decay_t;
+
+/* Shape of one linear attention. */
+typedef struct {
+  int B;            /* batch; must be 1 when n_seqs > 0                      */
+  int T;            /* tokens per batch row (packed total when n_seqs > 0)   */
+  int Hq;           /* heads of q and k                                      */
+  int H;            /* heads of v: a multiple of Hq; head h reads q's and k's head h / (H / Hq) */
+  int d_k, d_v;     /* channels of a head: 1 .. 128                          */
+  int n_seqs;       /* 0: B sequences of T tokens; > 0: packed sequences     */
+  kda_dtype_t dtype;/* dtype of q, k, v, g, o and their gradients            */
+  kda_decay_t decay;
+  float scale;      /* factor on o                                           */
+  int64_t ld_q, ld_k, ld_v, ld_g; /* distances between token rows, in elements (0: Hq d_k, Hq d_k, H d_v, H) */
+} kda_linear_desc_t;
+
+/*
+ * Per sequence and head, from S = h0 (or zeros):
+ *     a_t = exp(min(g_t, 0))
+ *     S_t = a_t S_{t-1} + k_t v_t^T          [d_k, d_v], fp32
+ *     o_t = scale S_t^T q_t
+ *   q, k    : [B, T, Hq, d_k] dtype, rows ld_q, ld_k apart
+ *   v       : [B, T, H, d_v] dtype, rows ld_v apart
+ *   g       : as the decay says; values above 0 count as 0, -infinity forgets
+ *             everything.  Rows ld_g apart (KDA_DECAY_TOKEN).
+ *   h0      : [S, H, d_k, d_v] fp32 or NULL (zero state); S = n_seqs or B
+ *   o       : [B, T, H, d_v] dtype, written
+ *   ht      : [S, H, d_k, d_v] fp32, written, or NULL
+ * Tokens go through in chunks of 64 (fp32: 32): the decay from one token of a
+ * chunk to another is one factor, which is 0 below 2^-126.
+ * A NaN or Inf reaches its own and later tokens of its sequence and head (an
+ * infinity as an infinity or a NaN), never an earlier token, another sequence
+ * or another head.
+ * Outputs must not overlap each other, the inputs or the workspace.  The
+ * workspace (kda_linear_attn_workspace_size; 0 bytes when the batch alone
+ * fills the device) holds the state of every range of tokens that the call
+ * scans side by side, at most about two for every compute unit and head.
+ */
+int kda_linear_attn_workspace_size(const kda_linear_desc_t* d, size_t* bytes);
+int kda_linear_attn_forward(const kda_linear_desc_t* d, const void* q, const void* k, const void* v, const void* g,
+                            const float* h0, const int32_t* cu_seqlens, void* o, float* ht, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/*
+ * One new token for each of d->B sequences (d->T must be 1, d->n_seqs 0), the
+ * state [B, H, d_k, d_v] updated in place; q, k [B, Hq, d_k], v, o [B, H, d_v],
+ * g [B, H] with KDA_DECAY_TOKEN.  o and state must not overlap each other or
+ * any input.
+ */
+int kda_linear_attn_step(const kda_linear_desc_t* d, const void* q, const void* k, const void* v, const void* g,
+                         float* state, void* o, void* stream);
+
+/*
+ * Gradients of <dout, o> + <dht, ht>.
+ *   dout    : [B, T, H, d_v] dtype;      dht: [S, H, d_k, d_v] fp32 or NULL (zero)
+ *   dq, dk  : [B, T, Hq, d_k] dtype, summed over the heads that share them
+ *   dv      : [B, T, H, d_v] dtype
+ *   dg      : [B, T, H] dtype or NULL (not written); 0 where g is above 0.
+ *             NULL unless the decay is KDA_DECAY_TOKEN (the others are constants)
+ *   dh0     : [S, H, d_k, d_v] fp32 or NULL (not written)
+ * A NaN or Inf reaches the gradients that the recurrence carries it to, and
+ * may reach all of its sequence's and head's dg.
+ * The workspace holds the states and their gradients between ranges of tokens
+ * as the forward call's, 8 bytes per token and head, and for shared queries
+ * and keys (H > Hq) their gradients by head in fp32, 8 d_k bytes per token and
+ * head.  Outputs must not overlap each other, the inputs or the workspace.
+ */
+int kda_linear_attn_backward_workspace_size(const kda_linear_desc_t* d, size_t* bytes);
+int kda_linear_attn_backward(const kda_linear_desc_t* d, const void* q, const void* k, const void* v, const void* g,
+                             const float* h0, const int32_t* cu_seqlens, const void* dout, const float* dht, void* dq,
+                             void* dk, void* dv, void* dg, float* dh0, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/* ---- the norms at a block's end -------------------------------------------
+ *
+ * What follows the recurrence in its layer (the norm of every head with the
+ * output gate), and what stands between that layer's output and the next
+ * block (the residual sum and the norm of it).  Slices and alignment as
+ * above.  KDA_ERR_UNSUPPORTED: norms over more than 8192 channels, more than
+ * 65536 heads, 2^31 rows (tokens times heads) or more.
+ */
+
+/* Shape of one gated norm. */
+typedef struct {
+  int n_tokens;     /* tokens of the whole batch                             */
+  int H;            /* heads                                                 */
+  int d;            /* channels per head: 1 .. 8192                          */
+  kda_dtype_t dtype;
+  kda_act_t activation; /* of the gate: KDA_ACT_SIGMOID or KDA_ACT_SILU      */
+  float eps;        /* >= 0, finite                                          */
+  int64_t ld_x, ld_gate; /* distances between token rows (0: H d)            */
+} kda_gated_norm_desc_t;
+
+/*
+ * For each head x of d channels with its gate z:
+ *     y = x (mean x^2 + eps)^-1/2 weight act(z)
+ *   x, gate : [n_tokens, H, d] dtype, token rows ld_* apart
+ *   weight  : [d] fp32 or NULL (ones)
+ *   y       : contiguous, written; must not overlap anything
+ */
+int kda_gated_norm_forward(const kda_gated_norm_desc_t* d, const void* x, const void* gate, const float* weight,
+                           void* y, void* stream);
+
+/*
+ * Gradients of <dy, y>: dy, dx, dgate [n_tokens, H, d] dtype, contiguous;
+ * dweight [d] fp32 or NULL (not written; given without the weight it is the
+ * gradient at a weight of ones).  The workspace holds partial sums of dweight.
+ */
+int kda_gated_norm_backward_workspace_size(const kda_gated_norm_desc_t* d, size_t* bytes);
+int kda_gated_norm_backward(const kda_gated_norm_desc_t* d, const void* x, const void* gate, const float* weight,
+                            const void* dy, void* dx, void* dgate, float* dweight, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* Shape of one residual norm. */
+typedef struct {
+  int n_tokens;     /* tokens of the whole batch                             */
+  int D;            /* channels: 1 .. 8192                                   */
+  kda_dtype_t dtype;
+  float scale;      /* on the block's output x                               */
+  float eps;        /* >= 0, finite                                          */
+  int64_t ld_x, ld_residual; /* distances between token rows (0: D)          */
+} kda_residual_norm_desc_t;
+
+/*
+ * For each token:
+ *     total = residual + scale channel_scale x
+ *     y     = total (mean total^2 + eps)^-1/2 weight
+ *   x, residual: [n_tokens, D] dtype, rows ld_* apart
+ *   weight, channel_scale: [D] fp32 or NULL (ones)
+ *   y, total: contiguous, written; must not overlap anything.  y is the norm
+ *             of the sum before it is rounded to total's dtype.
+ */
+int kda_residual_norm_forward(const kda_residual_norm_desc_t* d, const void* x, const void* residual,
+                              const float* weight, const float* channel_scale, void* y, void* total, void* stream);
+
+/*
+ * Gradients of <dy, y> + <dtotal, total>, from the total that the forward
+ * call left (its rows ld_residual apart):
+ *   dtotal  : [n_tokens, D] dtype, contiguous, or NULL (zero)
+ *   dresidual: [n_tokens, D] dtype, written
+ *   dx      : [n_tokens, D] dtype or NULL (not written: with a scale of 1 and
+ *             no channel_scale it is dresidual)
+ *   dweight, dchannel_scale: [D] fp32 or NULL (not written); the second needs
+ *             x, which is not read otherwise and may be NULL
+ * The workspace holds partial sums of the parameters' gradients.
+ */
+int kda_residual_norm_backward_workspace_size(const kda_residual_norm_desc_t* d, size_t* bytes);
+int kda_residual_norm_backward(const kda_residual_norm_desc_t* d, const void* x, const void* total, const float* weight,
+                               const float* channel_scale, const void* dy, const void* dtotal, void* dx,
+                               void* dresidual, float* dweight, float* dchannel_scale, void* workspace,
+                               size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }
