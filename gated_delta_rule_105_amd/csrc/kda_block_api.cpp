@@ -58,7 +58,10 @@ int check_linear(const kda_linear_desc_t* d, LinearSizes* s) {
   if (st != KDA_OK) return st;
   if (d->d_k > kda::kLinearMaxDim || d->d_v > kda::kLinearMaxDim) return KDA_ERR_UNSUPPORTED;
   if (n > (size_t)INT32_MAX - 4096) return KDA_ERR_UNSUPPORTED;  // the kernels count tokens in 32 bits, a chunk ahead
-  if (qk_row > (size_t)INT32_MAX || v_row > (size_t)INT32_MAX) return KDA_ERR_UNSUPPORTED;
+  // a chunk's rows are one buffer of less than 2^31 bytes: 64 of 2 or 32 of 4 bytes an element, outputs in fp32
+  const int64_t rows[] = {a.ld_q, a.ld_k, a.ld_v, a.ld_g, (int64_t)H * d->d_k, (int64_t)v_row};
+  for (int64_t ld : rows)
+    if (ld > (1 << 22)) return KDA_ERR_UNSUPPORTED;
   a.n_seqs = (int)s->t.seqs;
   a.T = d->T;
   a.tokens = (int64_t)n;
@@ -73,9 +76,9 @@ int check_linear(const kda_linear_desc_t* d, LinearSizes* s) {
 // False: a launch's grid would not fit.
 bool linear_plan(const kda_linear_desc_t* d, const LinearSizes& s, bool backward, kda::LinearPlan* p) {
   *p = kda::plan_linear(s.a.tokens, (int)s.t.seqs, d->T, d->n_seqs > 0, d->H, kda::device_compute_units(),
-                        s.state_floats, backward);
+                        kda::linear_record(d->d_k, d->d_v), backward);
   if (backward) kda::plan_linear_shared(p, s.a.tokens, d->H, d->Hq, d->d_k);
-  return kda::linear_fits(*p, s.a.tokens, d->H, s.state_floats, d->Hq, d->d_k);
+  return kda::linear_fits(*p, s.a.tokens, d->H, kda::linear_record(d->d_k, d->d_v), d->Hq, d->d_k);
 }
 
 // g and the offsets are there exactly where the descriptor says so

@@ -42,7 +42,12 @@ struct LinearPlan {
   size_t end_off, adj_off, sum_off, kind_off, dot_q_off, dot_k_off, slot_dot_off, seq_dot_off, dq_off, dk_off, ws_bytes;
 };
 
-inline LinearPlan plan_linear(int64_t tokens, int rows, int64_t T, bool packed, int H, int n_cu, size_t state_floats,
+// The kernels' tiles hold 64 or 128 channels of either kind; so do the states
+// in the workspace.
+constexpr int linear_pad(int d) { return d <= 64 ? 64 : 128; }
+constexpr size_t linear_record(int dk, int dv) { return (size_t)linear_pad(dk) * linear_pad(dv); }
+
+inline LinearPlan plan_linear(int64_t tokens, int rows, int64_t T, bool packed, int H, int n_cu, size_t record,
                               bool backward) {
   LinearPlan p{};
   const int64_t cus = n_cu > 0 ? n_cu : 256;
@@ -66,8 +71,8 @@ inline LinearPlan plan_linear(int64_t tokens, int rows, int64_t T, bool packed, 
     return at;
   };
   const size_t slots = p.carry ? (size_t)p.n_slots : 0, heads = (size_t)H;
-  p.end_off = take(slots * heads * state_floats * 4);
-  p.adj_off = backward ? take(slots * heads * state_floats * 4) : 0;
+  p.end_off = take(slots * heads * record * 4);
+  p.adj_off = backward ? take(slots * heads * record * 4) : 0;
   p.sum_off = take(slots * heads * 8);
   p.kind_off = take(slots * 4);
   if (backward) {
@@ -92,8 +97,8 @@ inline void plan_linear_shared(LinearPlan* p, int64_t tokens, int H, int Hq, int
 inline int64_t linear_groups(const LinearPlan& p, int H) { return p.n_slots * (int64_t)H; }
 // The launches' grids: sweeps of 256 threads a slot and head (three roles of
 // them backward), the chain's states, the shared heads' sums.
-inline bool linear_fits(const LinearPlan& p, int64_t tokens, int H, size_t state_floats, int Hq, int dk) {
-  return grid_fits(3 * linear_groups(p, H), 256) && grid_fits(H * (int64_t)ceil_div(state_floats, 256), 256) &&
+inline bool linear_fits(const LinearPlan& p, int64_t tokens, int H, size_t record, int Hq, int dk) {
+  return grid_fits(3 * linear_groups(p, H), 256) && grid_fits(H * (int64_t)record / 256, 256) &&
          grid_fits(ceil_div(tokens * Hq * dk, 256), 256);
 }
 

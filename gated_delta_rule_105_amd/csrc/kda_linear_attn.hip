@@ -26,6 +26,7 @@
 // of the sequence or slot.
 #include "kda_layer_device.h"
 #include "kda_linear.h"
+#include "kda_rows.h"
 
 namespace kda {
 namespace {
@@ -75,7 +76,8 @@ __device__ __forceinline__ f32x4 row_frag(const float* X, const Lane<float, W>& 
 // Operand whose k runs down column c0 + i, from row r0 (bf16: two transpose reads).
 template <int W>
 __device__ __forceinline__ bf16x8 col_frag(const bf16_t* X, const Lane<bf16_t, W>& l, int r0, int c0) {
-  const bf16_t* p = X + l.col + r0 * kLd<W> + c0;
+  typedef const __attribute__((address_space(3))) bf16_t lds_bf16;
+  lds_bf16* p = (lds_bf16*)X + l.col + (r0 * kLd<W> + c0);
   const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
   const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 16 * kLd<W>));
   return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -86,6 +88,16 @@ __device__ __forceinline__ f32x4 col_frag(const float* X, const Lane<float, W>& 
 #pragma unroll
   for (int e = 0; e < 4; ++e) x[e] = X[l.col + (r0 + e) * kLd<W> + c0];
   return x;
+}
+
+// Keeps the loads of x and y together, ahead of their first use.
+template <typename F>
+__device__ __forceinline__ void together(F (&x)[4], F (&y)[4]) {
+  asm volatile("" : "+v"(x[0]), "+v"(x[1]), "+v"(x[2]), "+v"(x[3]), "+v"(y[0]), "+v"(y[1]), "+v"(y[2]), "+v"(y[3]));
+}
+template <typename F>
+__device__ __forceinline__ void together(F (&x)[2], F (&y)[2]) {
+  asm volatile("" : "+v"(x[0]), "+v"(x[1]), "+v"(y[0]), "+v"(y[1]));
 }
 
 // ---- operands rounded from fp32 ---------------------------------------------------
@@ -140,69 +152,89 @@ struct View {
   int d;
 };
 
-// C tokens of W channels on the way from memory to LDS: 16 bytes a lane,
-// rows and channels that are not there read some that are, and become zeros
-// on the way to LDS.
+// Rows of one head as a buffer resource that ends with row n - 1: rows behind
+// read as zeros and are not written.  kNowhere is an offset past its end.
+// With n = 0 nothing is read: loads ahead need no branch (what is merged
+// behind one is waited for there).
+constexpr uint32_t kNowhere = 0x80000000u;
+template <typename T>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const View& x, int64_t tok, int n) {
+  return rsrc((const T*)x.p + tok * x.ld, n > 0 ? (uint32_t)(((n - 1) * (int)x.ld + x.d) * (int)sizeof(T)) : 0u);
+}
+
+// C tokens of W channels on the way from memory to LDS, 16 bytes a lane;
+// zeros for rows and channels that are not there.  A row's last vector, where
+// the row ends inside it, is read from further ahead and moved down.
 template <typename T, int W> struct Stage {
   static constexpr int VE = 16 / (int)sizeof(T), VPR = W / VE, RPP = kThreads / VPR, N = kTokens<T> / RPP;
-  typedef typename Pack<T, VE>::type vec;
-  vec v[N];
+  uint4 v[N];
   __device__ __forceinline__ void load(const View& x, int tok, int n) {
+    const int c = (int)(threadIdx.x % VPR) * VE, r = (int)(threadIdx.x / VPR), step = (int)x.ld * (int)sizeof(T);
+    const __amdgpu_buffer_rsrc_t rows = rows_of<T>(x, tok, n);
+    const int at = c + VE <= x.d ? c : x.d - VE;
+    const uint32_t off = c < x.d && x.d >= VE ? (uint32_t)(r * step + at * (int)sizeof(T)) : kNowhere;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      v[i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(rows, off, i * RPP * step, 0));
+  }
+  __device__ __forceinline__ void store(T* X, const View& x, int tok, int n) {
     const int c = (int)(threadIdx.x % VPR) * VE, r = (int)(threadIdx.x / VPR);
-    const T* p = (const T*)x.p;
-    if (x.d % VE == 0) {
-      p += c < x.d ? c : 0;
+    if (x.d % VE != 0 && x.d >= VE) {
+      const bool tail = c < x.d && c + VE > x.d;
+      const int bits = (VE - x.d % VE) * 8 * (int)sizeof(T);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const int row = r + i * RPP;
-        v[i] = *(const vec*)(p + (int64_t)(tok + (row < n ? row : n - 1)) * x.ld);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int row = r + i * RPP;
-        const T* at = p + (int64_t)(tok + (row < n ? row : n - 1)) * x.ld;
-#pragma unroll
-        for (int e = 0; e < VE; ++e) {
-          const T y = at[c + e < x.d ? c + e : 0];
-          v[i][e] = c + e < x.d ? y : (T)0;
-        }
+        const uint64_t lo = (uint64_t)v[i].y << 32 | v[i].x, hi = (uint64_t)v[i].w << 32 | v[i].z;
+        const uint64_t a = bits < 64 ? lo >> bits | hi << (64 - bits) : hi >> (bits - 64), b = bits < 64 ? hi >> bits : 0;
+        v[i] = tail ? make_uint4((uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b, (uint32_t)(b >> 32)) : v[i];
       }
     }
-  }
-  __device__ __forceinline__ void store(T* X, int d, int n) const {
-    const int c = (int)(threadIdx.x % VPR) * VE, r = (int)(threadIdx.x / VPR);
+    // RPP is a multiple of 8: the rows' swizzles differ in the upper bit at most
+    const int swizzle = (r >> 2) & 3, other = swizzle & 1 ? -4 : 4;
+    T* const row = X + r * kLd<W>;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int row = r + i * RPP, s = (row >> 2) & 3;
-      const bool there = c < d && row < n;
-      uint4 w = __builtin_bit_cast(uint4, v[i]);
-      w = there ? w : make_uint4(0, 0, 0, 0);
+      T* at = row + (((c >> 2) ^ swizzle ^ ((i * RPP >> 2) & 3)) << 2) + i * RPP * kLd<W>;
       if constexpr (sizeof(T) == 2) {
-        // two units, the swizzle's low bit swaps them
-        const bool swap = s & 1;
-        const uint4 y = swap ? make_uint4(w.z, w.w, w.x, w.y) : w;
-        *(uint4*)(X + row * kLd<W> + (((c >> 2) ^ (s & 2)) << 2)) = y;
+        *(uint2*)at = make_uint2(v[i].x, v[i].y);
+        *(uint2*)(at + other) = make_uint2(v[i].z, v[i].w);
       } else {
-        *(uint4*)(X + row * kLd<W> + (((c >> 2) ^ s) << 2)) = w;
+        *(uint4*)at = v[i];
       }
     }
+    // rows of fewer channels than a vector has, over the zeros that the same lane wrote
+    if (x.d < VE && c == 0)
+#pragma unroll 1
+      for (int k = r; k < n; k += RPP)
+#pragma unroll 1
+        for (int e = 0; e < x.d; ++e)
+          X[k * kLd<W> + (((e >> 2) ^ ((k >> 2) & 3)) << 2) + (e & 3)] = ((const T*)x.p)[(int64_t)(tok + k) * x.ld + e];
   }
-  // whether some row that is there holds an infinity or a NaN
-  __device__ __forceinline__ bool wild(int d, int n) const {
-    const int c = (int)(threadIdx.x % VPR) * VE, r = (int)(threadIdx.x / VPR);
-    bool found = false;
+  // Whether some row may hold an infinity or a NaN: the largest magnitude of
+  // all that was read, so that zeros for what is not there need no care.
+  __device__ __forceinline__ bool wild(const View& x) const {
+    if (x.d < VE) return true;
+    if constexpr (sizeof(T) == 2) {
+      typedef uint16_t pair __attribute__((ext_vector_type(2)));
+      pair most = {0, 0};
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      bool any = false;
+      for (int i = 0; i < N; ++i) {
+        const uint4 w = v[i];
 #pragma unroll
-      for (int e = 0; e < VE; ++e) {
-        if constexpr (sizeof(T) == 2) any |= (v[i][e] & 0x7f80) == 0x7f80;
-        else any |= (__float_as_uint(v[i][e]) & 0x7f800000u) == 0x7f800000u;
+        for (int e = 0; e < 4; ++e)
+          most = __builtin_elementwise_max(most, __builtin_bit_cast(pair, (&w.x)[e] & 0x7fff7fffu));
       }
-      found |= any && c < d && r + i * RPP < n;
+      return most[0] >= 0x7f80 || most[1] >= 0x7f80;
+    } else {
+      uint32_t most = 0;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const uint4 w = v[i];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) most = max(most, (&w.x)[e] & 0x7fffffffu);
+      }
+      return most >= 0x7f800000u;
     }
-    return found;
   }
 };
 
@@ -224,15 +256,70 @@ __device__ __forceinline__ f32x4 load4(const View& x, int64_t tok, int c) {
   }
   return (f32x4){v[0], v[1], v[2], v[3]};
 }
-template <typename T>
-__device__ __forceinline__ void store4(T* p, int c, int d, const f32x4& x) {
-  if (d % 4 == 0) {
-    const float v[4] = {x[0], x[1], x[2], x[3]};
-    if (c < d) store_vec<T, 4>(p + c, v);
+// Four channels of a lane's row of a resource: row i + r0 (r0 the same for the
+// wave), channels c + c1 (c1 a constant).  d is a multiple of 4 with QUADS.
+struct Lanes4 {
+  __amdgpu_buffer_rsrc_t rows;
+  int step, off, c, d;  // bytes between rows, the lane's offset, its first channel, channels
+  __device__ __forceinline__ Lanes4(__amdgpu_buffer_rsrc_t rows, int64_t ld, int esz, int d, int i, int c)
+      : rows(rows), step((int)ld * esz), off(i * step + c * esz), c(c), d(d) {}
+};
+template <typename T> struct Four {
+  typedef uint32_t words __attribute__((ext_vector_type(sizeof(T))));  // 4 elements
+  words w;
+  template <bool QUADS>
+  __device__ __forceinline__ void load(const Lanes4& l, int r0, int c1) {
+    constexpr int E = (int)sizeof(T);
+    const int row = r0 * l.step;
+    if constexpr (QUADS) {
+      const uint32_t off = l.c + c1 < l.d ? (uint32_t)(l.off + c1 * E) : kNowhere;
+      if constexpr (E == 2) w = __builtin_bit_cast(words, __builtin_amdgcn_raw_buffer_load_b64(l.rows, off, row, 0));
+      else w = __builtin_bit_cast(words, __builtin_amdgcn_raw_buffer_load_b128(l.rows, off, row, 0));
+    } else {
+      w = (words)0u;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (l.c + c1 + e < l.d) {
+          if constexpr (E == 2)
+            w[e / 2] |= ((uint32_t)__builtin_amdgcn_raw_buffer_load_b16(l.rows, l.off + (c1 + e) * E, row, 0) & 0xffffu)
+                        << e % 2 * 16;
+          else w[e] = __builtin_amdgcn_raw_buffer_load_b32(l.rows, l.off + (c1 + e) * E, row, 0);
+        }
+    }
+  }
+  __device__ __forceinline__ void load(const Lanes4& l, int r0, int c1) {
+    if (l.d % 4 == 0) load<true>(l, r0, c1);
+    else load<false>(l, r0, c1);
+  }
+  __device__ __forceinline__ f32x4 get() const {
+    if constexpr (sizeof(T) == 2)
+      return (f32x4){__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xffff0000u), __uint_as_float(w[1] << 16),
+                     __uint_as_float(w[1] & 0xffff0000u)};
+    else return __builtin_bit_cast(f32x4, w);
+  }
+};
+template <typename T, bool QUADS>
+__device__ __forceinline__ void store4(const Lanes4& l, int r0, int c1, const f32x4& x) {
+  constexpr int E = (int)sizeof(T);
+  const int row = r0 * l.step;
+  if constexpr (QUADS) {
+    const uint32_t off = l.c + c1 < l.d ? (uint32_t)(l.off + c1 * E) : kNowhere;
+    if constexpr (E == 2) {
+      typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+      const bf16x2 a = f32x2_to_bf16x2(x[0], x[1]), b = f32x2_to_bf16x2(x[2], x[3]);
+      __builtin_amdgcn_raw_buffer_store_b64((u32x2){__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b)},
+                                            l.rows, off, row, 0);
+    } else {
+      typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), l.rows, off, row, 0);
+    }
   } else {
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (c + e < d) p[c + e] = Elem<T>::from_f32(x[e]);
+      if (l.c + c1 + e < l.d) {
+        if constexpr (E == 2) __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16(x[e]), l.rows, l.off + (c1 + e) * E, row, 0);
+        else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x[e]), l.rows, l.off + (c1 + e) * E, row, 0);
+      }
   }
 }
 
@@ -266,18 +353,30 @@ __device__ __forceinline__ double log2_decay(float g) {
   return (double)g * 1.4426950408889634;
 }
 
-template <typename T>
-__device__ __forceinline__ float raw_decay(const LinearArgs& a, int h, int tok, int n, int lane) {
-  if (a.g) return Elem<T>::to_f32(((const T*)a.g)[(int64_t)(tok + (lane < n ? lane : n - 1)) * a.ld_g + h]);
-  return a.decay ? a.decay[h] : 0.f;
-}
+// A chunk's log decays, a lane each, on their way from memory.
+template <typename T> struct LogDecays {
+  View g;       // by token (none: an empty range)
+  float fixed;  // by head
+  float raw;
+  __device__ __forceinline__ LogDecays(const LinearArgs& a, int h)
+      : g{(const T*)a.g + h, a.g ? a.ld_g : 0, a.g ? 1 : 0}, fixed(a.decay ? a.decay[h] : 0.f), raw(0.f) {}
+  __device__ __forceinline__ void load(int tok, int n, int lane) {
+    const __amdgpu_buffer_rsrc_t rows = rows_of<T>(g, tok, n);
+    const int off = lane * (int)g.ld * (int)sizeof(T);
+    if constexpr (sizeof(T) == 2) raw = __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b16(rows, off, 0, 0));
+    else raw = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rows, off, 0, 0));
+  }
+  __device__ __forceinline__ float get() const {
+    const float x = sizeof(T) == 2 ? __uint_as_float(__float_as_uint(raw) << 16) : raw;
+    return g.d ? x : fixed;
+  }
+};
 
 // Decays of a chunk's tokens in LDS.
 template <typename T> struct Decays {
   double sum[kTokens<T>];               // running sums
   float row[kTokens<T>], col[kTokens<T>];  // factors of the state's part of an output, and of a token's part in the state
   float whole;
-  int wild;
   __device__ __forceinline__ void fill(float g, int n, bool back, float row_scale, float col_scale, int lane) {
     const double s = wave_sums(lane < n ? log2_decay(g) : 0.0);
     const uint64_t w = __builtin_bit_cast(uint64_t, s);
@@ -296,10 +395,15 @@ template <typename T> struct Decays {
 
 // ---- states in registers ----------------------------------------------------------
 // State tiles: rows the channels that a product sums over (16 m + 4 g + r in
-// lane 16 g + i), columns a wave's own (c0 + 16 nt + i).  In memory states are
-// [d_k][d_v]; TR: rows are d_v.
-template <int M, int NT>
+// lane 16 g + i), columns a wave's own (16 (NT wave + t) + i).  Records in the
+// workspace hold whole tiles, padding included, in the order of the lanes:
+// tile (row tile, column tile) is 256 floats, a lane's four side by side.  A
+// role whose state is the transposed one (TR) reads them across.  The
+// caller's states are [d_k][d_v] and go through LDS, a column tile of every
+// wave at a time.
+template <int DK, int NT>
 struct State {
+  static constexpr int M = DK / 16, DV = 64 * NT;
   f32x4 s[M][NT];
   __device__ __forceinline__ void zero() {
 #pragma unroll
@@ -307,59 +411,124 @@ struct State {
 #pragma unroll
       for (int t = 0; t < NT; ++t) s[m][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
   }
-  // element (row, col), f(pointer offset, its four values)
-  template <bool TR>
-  __device__ __forceinline__ void load(const float* p, int rows, int cols, int c0, int lane) {
-    if (!p) return zero();
-    const int g = lane >> 4, i = lane & 15;
+  // f(tile's four values, record's four values)
+  template <bool TR, typename F>
+  __device__ __forceinline__ void with_record(const float* p, int lane, int wave, F&& f) const {
+    const __amdgpu_buffer_rsrc_t rec = rsrc(p, DK * DV * 4);
+    const int g = lane >> 4, i = lane & 15, off = 4 * (TR ? 64 * (i >> 2) + 16 * g + (i & 3) : 4 * lane);
 #pragma unroll
     for (int m = 0; m < M; ++m)
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const int col = c0 + 16 * t + i;
+        const int n = wave * NT + t;
+        f32x4 x;
+        if (TR) {
+          // row tile n, column tile m of a record of DV rows and DK columns
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row = 16 * m + 4 * g + r;
-          const bool there = row < rows && col < cols;
-          const float x = p[there ? TR ? col * rows + row : row * cols + col : 0];
-          s[m][t][r] = there ? x : 0.f;
+          for (int r = 0; r < 4; ++r)
+            x[r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rec, off + 16 * r, (n * M + m) * 1024, 0));
+        } else {
+          x = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rec, off, (m * (DV / 16) + n) * 1024, 0));
         }
+        f(m, t, x);
       }
   }
   template <bool TR>
-  __device__ __forceinline__ void store(float* p, int rows, int cols, int c0, int lane) const {
-    const int g = lane >> 4, i = lane & 15;
+  __device__ __forceinline__ void load(const float* p, int lane, int wave) {
+    with_record<TR>(p, lane, wave, [&](int m, int t, const f32x4& x) { s[m][t] = x; });
+  }
+  __device__ __forceinline__ void store(float* p, int lane, int wave) const {
 #pragma unroll
     for (int m = 0; m < M; ++m)
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const int col = c0 + 16 * t + i;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row = 16 * m + 4 * g + r;
-          if (row < rows && col < cols) p[TR ? col * rows + row : row * cols + col] = s[m][t][r];
-        }
-      }
+      for (int t = 0; t < NT; ++t) *(f32x4*)(p + (m * (DV / 16) + wave * NT + t) * 256 + 4 * lane) = s[m][t];
   }
-  // this lane's part of the inner product with a state in memory
-  template <bool TR>
-  __device__ __forceinline__ float dot(const float* p, int rows, int cols, int c0, int lane) const {
-    const int g = lane >> 4, i = lane & 15;
+  __device__ __forceinline__ float dot(const float* p, int lane, int wave) const {
     float sum = 0.f;
+    with_record<false>(p, lane, wave, [&](int m, int t, const f32x4& x) {
 #pragma unroll
-    for (int m = 0; m < M; ++m)
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const int col = c0 + 16 * t + i;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row = 16 * m + 4 * g + r;
-          const bool there = row < rows && col < cols;
-          const float x = p[there ? TR ? col * rows + row : row * cols + col : 0];
-          sum += there ? s[m][t][r] * x : 0.f;
-        }
-      }
+      for (int r = 0; r < 4; ++r) sum += s[m][t][r] * x[r];
+    });
     return sum;
+  }
+
+  // a caller's state, rows by cols of it (TR: held cols by rows)
+  static constexpr int kLds = DK * 64 * 4;  // bytes
+  static constexpr int kEach = DK * 64 / kThreads;
+  // this thread's number, formed anew at every use: what follows from it is not kept in registers across the chunks
+  __device__ __forceinline__ static int thread() {
+    int x = (int)threadIdx.x;
+    asm volatile("" : "+v"(x));
+    return x;
+  }
+  // element j of a thread in column tile t of every wave: its place in memory (kNowhere: not there) and in LDS
+  template <bool TR>
+  __device__ __forceinline__ static void place(int thread, int j, int t, int rows, int cols, uint32_t* off, int* at) {
+    const int x = thread + j * kThreads, c = TR ? x / DK : x % 64, row = TR ? x % DK : x / 64;
+    const int col = 16 * (NT * (c / 16) + t) + c % 16;
+    *off = row < rows && col < cols ? (uint32_t)((TR ? col * rows + row : row * cols + col) * 4) : kNowhere;
+    *at = ((c / 16 * M + row / 16) * 64 + row % 16 / 4 * 16 + c % 16) * 4 + row % 4;
+  }
+  template <bool TR, typename F>
+  __device__ __forceinline__ void with_caller(const float* p, int rows, int cols, float* lds, int lane, int wave,
+                                              F&& f) const {
+    const __amdgpu_buffer_rsrc_t mem = rsrc(p, (uint32_t)(rows * cols * 4));
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int x = thread();
+      lds_barrier();
+#pragma unroll 1
+      for (int j0 = 0; j0 < kEach; j0 += 16) {
+        float y[16];
+        int at[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          uint32_t off;
+          place<TR>(x, j0 + j, t, rows, cols, &off, &at[j]);
+          y[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(mem, off, 0, 0));
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) lds[at[j]] = y[j];
+      }
+      lds_barrier();
+#pragma unroll
+      for (int m = 0; m < M; ++m) f(m, t, *(const f32x4*)(lds + ((wave * M + m) * 64 + lane) * 4));
+    }
+    lds_barrier();
+  }
+  template <bool TR>
+  __device__ __forceinline__ void load_caller(const float* p, int rows, int cols, float* lds, int lane, int wave) {
+    if (!p) return zero();
+    with_caller<TR>(p, rows, cols, lds, lane, wave, [&](int m, int t, const f32x4& x) { s[m][t] = x; });
+  }
+  template <bool TR>
+  __device__ __forceinline__ float dot_caller(const float* p, int rows, int cols, float* lds, int lane, int wave) const {
+    float sum = 0.f;
+    with_caller<TR>(p, rows, cols, lds, lane, wave, [&](int m, int t, const f32x4& x) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) sum += s[m][t][r] * x[r];
+    });
+    return sum;
+  }
+  template <bool TR>
+  __device__ __forceinline__ void store_caller(float* p, int rows, int cols, float* lds, int lane, int wave) const {
+    const __amdgpu_buffer_rsrc_t mem = rsrc(p, (uint32_t)(rows * cols * 4));
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int x = thread();
+      lds_barrier();
+#pragma unroll
+      for (int m = 0; m < M; ++m) *(f32x4*)(lds + ((wave * M + m) * 64 + lane) * 4) = s[m][t];
+      lds_barrier();
+#pragma unroll 16
+      for (int j = 0; j < kEach; ++j) {
+        uint32_t off;
+        int at;
+        place<TR>(x, j, t, rows, cols, &off, &at);
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(lds[at]), mem, off, 0, 0);
+      }
+    }
+    lds_barrier();
   }
 };
 
@@ -368,12 +537,17 @@ struct State {
 // scaled and cut to pieces; K's are read from LDS as they are.
 template <typename T, int DK, int NT, int PIECES>
 __device__ __forceinline__ void step_state(const T* K, const Lane<T, DK>& lk, const typename Frag<T>::type (&vf)[2][NT],
-                                           const Decays<T>& d, int lane, State<DK / 16, NT>& st) {
+                                           const Decays<T>& d, int lane, State<DK, NT>& st) {
   constexpr int KB = Elem<T>::KB;
   const int g = lane >> 4;
-  typename Frag<T>::type f[2][NT][PIECES];
+  const float whole = d.whole;
+#pragma unroll
+  for (int m = 0; m < DK / 16; ++m)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) st.s[m][t] *= whole;
 #pragma unroll
   for (int kb = 0; kb < 2; ++kb) {
+    typename Frag<T>::type f[NT][PIECES];
     f32x4 by[kAccs<T>];
 #pragma unroll
     for (int h = 0; h < kAccs<T>; ++h) by[h] = *(const f32x4*)(d.col + KB * kb + 16 * h + 4 * g);
@@ -383,21 +557,20 @@ __device__ __forceinline__ void step_state(const T* K, const Lane<T, DK>& lk, co
       widen(vf[kb][t], x);
 #pragma unroll
       for (int h = 0; h < kAccs<T>; ++h) x[h] *= by[h];
-      Pieces<T>::template cut<PIECES>(x, f[kb][t]);
+      Pieces<T>::template cut<PIECES>(x, f[t]);
     }
-  }
-  const float whole = d.whole;
+    // four row tiles at a time: a product's result is not wanted by the next
 #pragma unroll
-  for (int m = 0; m < DK / 16; ++m) {
+    for (int m = 0; m < DK / 16; m += 4) {
+      typename Frag<T>::type kf[4];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) st.s[m][t] *= whole;
+      for (int i = 0; i < 4; ++i) kf[i] = col_frag<DK>(K, lk, KB * kb, 16 * (m + i));
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-      const auto kf = col_frag<DK>(K, lk, KB * kb, 16 * m);
+      for (int p = PIECES - 1; p >= 0; --p)
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int p = PIECES - 1; p >= 0; --p) st.s[m][t] = mma(kf, f[kb][t][p], st.s[m][t]);
+          for (int t = 0; t < NT; ++t) st.s[m + i][t] = mma(kf[i], f[t][p], st.s[m + i][t]);
     }
   }
 }
@@ -428,10 +601,11 @@ struct Slot {
 // What a slot hands on: forward the state at its end, of the sequence that
 // goes on past it, from zero where that sequence entered; backward
 // (blockIdx.y = 1) the gradient of the state at its start, of the sequence
-// that entered.  rows of K, columns of V: k and v, backward q and dout.
+// that entered.  Rows and columns: k and v.  In the backward pass (TR) the
+// transposed states are wanted: v and k, and for the gradients dout and q.
 template <typename T, int DK, int NT, bool BACK>
 __device__ __forceinline__ void states_range(const LinearArgs& a, const View& k, const View& v, int h, int t0, int end,
-                                             char* smem, State<DK / 16, NT>& st, double* total) {
+                                             char* smem, State<DK, NT>& st, double* total) {
   constexpr int C = kTokens<T>, DV = 64 * NT;
   T* K = (T*)smem;
   T* V = (T*)(smem + kTileBytes<T, DK>);
@@ -442,21 +616,21 @@ __device__ __forceinline__ void states_range(const LinearArgs& a, const View& k,
   const int chunks = (end - t0 + C - 1) / C;
   Stage<T, DK> sk;
   Stage<T, DV> sv;
-  float g = 0.f;
+  LogDecays<T> g(a, h);
   auto load = [&](int i) {
-    const int t = t0 + (BACK ? chunks - 1 - i : i) * C, n = end - t < C ? end - t : C;
-    sk.load(k, t, n);
-    sv.load(v, t, n);
-    g = raw_decay<T>(a, h, t, n, lane);
+    const int t = t0 + (BACK ? chunks - 1 - i : i) * C, left = end - t < C ? end - t : C, n = i < chunks ? left : 0;
+    sk.load(k, n ? t : t0, n);
+    sv.load(v, n ? t : t0, n);
+    g.load(n ? t : t0, n, lane);
   };
   load(0);
   for (int i = 0; i < chunks; ++i) {
     const int t = t0 + (BACK ? chunks - 1 - i : i) * C, n = end - t < C ? end - t : C;
-    sk.store(K, k.d, n);
-    sv.store(V, v.d, n);
-    if (wave == 0) d->fill(g, n, BACK, 1.f, BACK ? a.scale : 1.f, lane);
+    sk.store(K, k, t, n);
+    sv.store(V, v, t, n);
+    if (wave == 0) d->fill(g.get(), n, BACK, 1.f, BACK ? a.scale : 1.f, lane);
     lds_barrier();
-    if (i + 1 < chunks) load(i + 1);
+    load(i + 1);
     if (total) *total += d->sum[C - 1];
     typename Frag<T>::type vf[2][NT];
     own_columns<T, DV, NT>(V, lv, c0, vf);
@@ -466,9 +640,12 @@ __device__ __forceinline__ void states_range(const LinearArgs& a, const View& k,
 }
 
 template <typename T, int DK, int NT>
-constexpr int kStatesLds = kTileBytes<T, DK> + kTileBytes<T, 64 * NT> + (int)sizeof(Decays<T>);
-
+constexpr int kStatesTiles = kTileBytes<T, DK> + kTileBytes<T, 64 * NT> + (int)sizeof(Decays<T>);
+// callers' states go through the same memory
 template <typename T, int DK, int NT>
+constexpr int kStatesLds = kStatesTiles<T, DK, NT> > State<DK, NT>::kLds ? kStatesTiles<T, DK, NT> : State<DK, NT>::kLds;
+
+template <typename T, int DK, int NT, bool TR>
 __global__ void __launch_bounds__(kThreads, 2)
 linear_states(const LinearArgs a, const T* __restrict__ dout, const float* __restrict__ dht, float* __restrict__ ends,
               float* __restrict__ adj, double* __restrict__ sums, int* __restrict__ kinds) {
@@ -476,13 +653,13 @@ linear_states(const LinearArgs a, const T* __restrict__ dout, const float* __res
   const int h = (int)(blockIdx.x % (unsigned)a.H), hq = h / (a.H / a.Hq);
   const Slot w(a, (int)(blockIdx.x / (unsigned)a.H));
   const Seqs seqs{a.cu, a.n_seqs, a.T, a.tokens};
-  const int lane = threadIdx.x & 63, c0 = uniform(threadIdx.x >> 6) * 16 * NT;
-  const int64_t floats = (int64_t)a.dk * a.dv, at = ((int64_t)w.slot * a.H + h) * floats;
-  State<DK / 16, NT> st;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int64_t floats = (int64_t)a.dk * a.dv, at = ((int64_t)w.slot * a.H + h) * DK * 64 * NT;
+  State<DK, NT> st;
   const int first = uniform(seqs.from(w.lo)), before = first > 0 ? uniform((int)seqs.end(first - 1)) : w.lo;
   const bool entered = before > w.lo;
   double total = 0.0;
-  if (blockIdx.y == 0) {
+  if (!TR || blockIdx.y == 0) {
     const int n = uniform(seqs.from(w.hi)) - 1;  // the last sequence that starts in the slot or before
     const bool on = !w.last && n >= 0 && uniform((int)seqs.end(n)) > w.hi;
     const int start = on ? uniform((int)seqs.start(n)) : 0;
@@ -490,19 +667,20 @@ linear_states(const LinearArgs a, const T* __restrict__ dout, const float* __res
     if (h == 0 && threadIdx.x == 0)
       kinds[w.slot] = (!on ? kNothing : own ? kStarted : kPassed) | (entered ? kEntered : 0);
     if (!on) return;
-    st.template load<false>(own && a.h0 ? a.h0 + ((int64_t)n * a.H + h) * floats : nullptr, a.dk, a.dv, c0, lane);
+    st.template load_caller<TR>(own && a.h0 ? a.h0 + ((int64_t)n * a.H + h) * floats : nullptr, TR ? a.dv : a.dk,
+                                TR ? a.dk : a.dv, (float*)smem, lane, wave);
     const View k{(const T*)a.k + hq * a.dk, a.ld_k, a.dk}, v{(const T*)a.v + h * a.dv, a.ld_v, a.dv};
-    states_range<T, DK, NT, false>(a, k, v, h, own ? start : w.lo, w.hi, smem, st, &total);
-    st.template store<false>(ends + at, a.dk, a.dv, c0, lane);
+    states_range<T, DK, NT, false>(a, TR ? v : k, TR ? k : v, h, own ? start : w.lo, w.hi, smem, st, &total);
+    st.store(ends + at, lane, wave);
     if (!own && threadIdx.x == 0) sums[(int64_t)w.slot * a.H + h] = total;
-  } else {
+  } else if constexpr (TR) {
     if (!entered) return;
     const bool ends_here = before <= w.hi;
-    st.template load<false>(ends_here && dht ? dht + ((int64_t)(first - 1) * a.H + h) * floats : nullptr, a.dk, a.dv, c0,
-                            lane);
+    st.template load_caller<TR>(ends_here && dht ? dht + ((int64_t)(first - 1) * a.H + h) * floats : nullptr, a.dv, a.dk,
+                                (float*)smem, lane, wave);
     const View q{(const T*)a.q + hq * a.dk, a.ld_q, a.dk}, d{dout + h * a.dv, (int64_t)a.H * a.dv, a.dv};
-    states_range<T, DK, NT, true>(a, q, d, h, w.lo, ends_here ? before : w.hi, smem, st, nullptr);
-    st.template store<false>(adj + at, a.dk, a.dv, c0, lane);
+    states_range<T, DK, NT, true>(a, d, q, h, w.lo, ends_here ? before : w.hi, smem, st, nullptr);
+    st.store(adj + at, lane, wave);
   }
 }
 
@@ -515,10 +693,9 @@ linear_chain(int H, int64_t floats, int n_slots, float* __restrict__ ends, float
              const double* __restrict__ sums, const int* __restrict__ kinds) {
   constexpr int BATCH = 8;
   const bool back = blockIdx.y != 0;
-  const int64_t per = (floats + 255) / 256;
+  const int64_t per = floats / 256;
   const int h = (int)(blockIdx.x / per);
-  int64_t el = (blockIdx.x % per) * 256 + threadIdx.x;
-  if (el >= floats) return;
+  const int64_t el = (blockIdx.x % per) * 256 + threadIdx.x;
   float* __restrict__ v = (back ? adj : ends) + h * floats + el;
   const int64_t step = (int64_t)H * floats;
   float s = 0.f;
@@ -561,7 +738,8 @@ template <typename T, int DK, int NT>
 struct SweepLds {
   T q[kTokens<T> * kLd<DK>], k[kTokens<T> * kLd<DK>], v[kTokens<T> * kLd<64 * NT>];
   T p[Pieces<T>::OUT][kTokens<T> * kLd<kTokens<T>>];
-  Decays<T> d;
+  Decays<T> d[2];  // of this chunk and the next
+  int wild;
   float dot[kWaves][kTokens<T>];
   float sums[10][2][16];  // row and column sums of M's tiles
 };
@@ -575,9 +753,10 @@ __device__ __forceinline__ void tile_of(int t, int* a, int* b) {
 // Tokens [t0, end) of one sequence; the state before them (BACK: the gradient
 // of the state after them) in, that after (before) them out.
 template <typename T, int DK, int NT, Role R>
-__device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w, int h, int t0, int end, bool keep,
-                                            SweepLds<T, DK, NT>& m, State<DK / 16, NT>& st) {
-  constexpr bool BACK = R == kDk || R == kDv, M_SUMS = R == kDq;
+__device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w, int h, int t0, int end,
+                                            SweepLds<T, DK, NT>& m, State<DK, NT>& st) {
+  // the state of these two roles is handed out at a sequence's end
+  constexpr bool BACK = R == kDk || R == kDv, M_SUMS = R == kDq, KEPT = R == kForward || R == kDv;
   constexpr int C = kTokens<T>, DV = 64 * NT, KB = Elem<T>::KB, RT = C / 16, TILES = RT * (RT + 1) / 2;
   constexpr int OUT = Pieces<T>::OUT;
   typedef typename Frag<T>::type frag;
@@ -589,42 +768,48 @@ __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w,
   const int chunks = (end - t0 + C - 1) / C;
   Stage<T, DK> sq, sk;
   Stage<T, DV> sv;
-  float gd = 0.f;
+  LogDecays<T> gd(a, h);
   auto load = [&](int t, int n) {
     sq.load(w.q, t, n);
     sk.load(w.k, t, n);
     sv.load(w.v, t, n);
-    gd = raw_decay<T>(a, h, t, n, lane);
   };
   // chunk i is [t, t + n); one that holds an infinity or a NaN among V is
   // walked token by token (one < n), so that a weight of zero never meets it
   int i = 0, one = 0;
   auto start_of = [&](int c) { return t0 + (BACK ? chunks - 1 - c : c) * C; };
   auto size_of = [&](int t) { return end - t < C ? end - t : C; };
-  int t = start_of(0), n = size_of(t), whole_n = n;
+  int t = start_of(0), n = size_of(t), whole_n = n, buf = 0;
   bool single = false;
+  // one wave does the decays of a chunk, ahead of it
+  auto decays = [&](int b, int n) {
+    if (wave == kWaves - 1) m.d[b].fill(gd.get(), n, BACK, w.row_scale, w.col_scale, lane);
+  };
+  gd.load(t, n, lane);
   load(t, n);
+  decays(0, n);
   while (true) {
-    sq.store(m.q, w.q.d, n);
-    sk.store(m.k, w.k.d, n);
-    sv.store(m.v, w.v.d, n);
-    if (wave == 0) m.d.fill(gd, n, BACK, w.row_scale, w.col_scale, lane);
-    if (!single && n > 1 && __ballot(sv.wild(w.v.d, n)) != 0 && lane == 0) m.d.wild = 1;
+    if (!single && n > 1 && __ballot(sv.wild(w.v)) != 0 && lane == 0) m.wild = 1;
+    sq.store(m.q, w.q, t, n);
+    sk.store(m.k, w.k, t, n);
+    sv.store(m.v, w.v, t, n);
     lds_barrier();
-    if (!single && uniform(m.d.wild)) {
+    if (!single && uniform(m.wild)) {
       lds_barrier();  // all have read it
-      if (threadIdx.x == 0) m.d.wild = 0;
+      if (threadIdx.x == 0) m.wild = 0;
       single = true;
       one = 0;
       whole_n = n;
       n = 1;
       t = start_of(i) + (BACK ? whole_n - 1 : 0);
+      gd.load(t, n, lane);
       load(t, n);
+      decays(buf, n);
       lds_barrier();
       continue;
     }
     // what comes next
-    int t_next = -1, n_next = 0;
+    int t_next = t, n_next = 0;
     if (single && one + 1 < whole_n) {
       t_next = BACK ? t - 1 : t + 1;
       n_next = 1;
@@ -632,48 +817,63 @@ __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w,
       t_next = start_of(i + 1);
       n_next = size_of(t_next);
     }
-    if (t_next >= 0) load(t_next, n_next);
+    gd.load(t_next, n_next, lane);
+    const Decays<T>& d = m.d[buf];
 
     // P, shared out by tiles
-#pragma unroll
-    for (int u = 0; u < (TILES + kWaves - 1) / kWaves; ++u) {
-      const int tile = wave + u * kWaves;
-      if (tile >= TILES) break;
+    auto p_tile = [&](int tile) {
       int ra, rb;
       tile_of(tile, &ra, &rb);
       const int rt = BACK ? rb : ra, ct = BACK ? ra : rb;
       f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+      // four steps' operands at a time, so that one wait serves them
 #pragma unroll
-      for (int kb = 0; kb < DK / KB; ++kb)
-        acc = mma(row_frag<DK>(m.k, lk, 16 * ct, KB * kb), row_frag<DK>(m.q, lk, 16 * rt, KB * kb), acc);
-      const double gi = m.d.sum[16 * rt + i16];
+      for (int kb = 0; kb < DK / KB; kb += 4) {
+        constexpr int U = DK / KB < 4 ? DK / KB : 4;
+        frag x[U], y[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          x[u] = row_frag<DK>(m.k, lk, 16 * ct, KB * (kb + u));
+          y[u] = row_frag<DK>(m.q, lk, 16 * rt, KB * (kb + u));
+        }
+        together(x, y);
+#pragma unroll
+        for (int u = 0; u < U; ++u) acc = mma(x[u], y[u], acc);
+      }
+      const double gi = d.sum[16 * rt + i16];
+      int at = i16 - 4 * g + 16 * (rt - ct);  // row minus column, of r = 0
+      asm volatile("" : "+v"(at));            // masks are compared here, not kept in registers across the loop
       f32x4 p;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const double gj = m.d.sum[16 * ct + 4 * g + r];
-        const int di = 16 * (rt - ct) + i16 - 4 * g - r;  // row minus column
-        const bool on = BACK ? di <= 0 : di >= 0;
-        p[r] = on ? acc[r] * decay_of(BACK ? gj - gi : gi - gj) * w.p_scale : 0.f;
+        const double gj = d.sum[16 * ct + 4 * g + r];
+        float x = acc[r] * (decay_of(BACK ? gj - gi : gi - gj) * w.p_scale);
+        asm volatile("" : "+v"(x));  // a select, not a branch around the factor
+        p[r] = (BACK ? at <= r : at >= r) ? x : 0.f;
       }
       if (M_SUMS && w.dots) {
         // M = (Q K^T) o P, this role's V being the keys
+        const Lanes4 other(rows_of<T>(w.other, t, n), w.other.ld, sizeof(T), w.other.d, i16, 4 * g);
         f32x4 s = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int kb = 0; kb < DV / KB; ++kb) {
-          const int row = 16 * rt + i16;
-          const int64_t tok = t + (row < n ? row : n - 1);
           frag qf;
-          if constexpr (sizeof(T) == 2)
-            qf = round8(load4<T>(w.other, tok, KB * kb + 4 * g), load4<T>(w.other, tok, KB * kb + 16 + 4 * g));
-          else
-            qf = load4<T>(w.other, tok, KB * kb + 4 * g);
+          Four<T> x, y;
+          x.load(other, 16 * rt, KB * kb);
+          if constexpr (sizeof(T) == 2) {
+            y.load(other, 16 * rt, KB * kb + 16);
+            qf = __builtin_bit_cast(frag, make_uint4(x.w[0], x.w[1], y.w[0], y.w[1]));
+          } else {
+            qf = x.get();
+          }
           s = mma(row_frag<DV>(m.v, lv, 16 * ct, KB * kb), qf, s);
         }
         float across = 0.f;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int di = 16 * (rt - ct) + i16 - 4 * g - r;
-          s[r] = di > 0 ? s[r] * p[r] : 0.f;
+          float x = s[r] * p[r];
+          asm volatile("" : "+v"(x));
+          s[r] = at > r ? x : 0.f;
           across += s[r];
           s[r] = row_sum(s[r]);
         }
@@ -696,8 +896,14 @@ __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w,
           *(f32x4*)at = x;
         }
       }
+    };
+    if constexpr (TILES >= 2 * kWaves) {
+      p_tile(wave);
+      p_tile(wave + kWaves);
+      if (wave + 2 * kWaves < TILES) p_tile(wave + 2 * kWaves);
+    } else {
+      if (wave < TILES) p_tile(wave);
     }
-    lds_barrier();
 
     // the state's part of the outputs, transposed: rows are channels of V, columns tokens
     f32x4 acc[RT][NT];
@@ -715,66 +921,75 @@ __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w,
         for (int e = 0; e < kAccs<T>; ++e) s[e] = st.s[kAccs<T> * kb + e][x];
         Pieces<T>::template cut<OUT>(s, sf[x]);
       }
+      frag qf[RT];
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        const frag qf = row_frag<DK>(m.q, lk, 16 * rt, KB * kb);
+      for (int rt = 0; rt < RT; ++rt) qf[rt] = row_frag<DK>(m.q, lk, 16 * rt, KB * kb);
 #pragma unroll
-        for (int x = 0; x < NT; ++x)
+      for (int c = OUT - 1; c >= 0; --c)
 #pragma unroll
-          for (int c = OUT - 1; c >= 0; --c) acc[rt][x] = mma(sf[x][c], qf, acc[rt][x]);
-      }
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+          for (int x = 0; x < NT; ++x) acc[rt][x] = mma(sf[x][c], qf[rt], acc[rt][x]);
     }
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      const float by = m.d.row[16 * rt + i16];
+      const float by = d.row[16 * rt + i16];
 #pragma unroll
       for (int x = 0; x < NT; ++x) acc[rt][x] *= by;
     }
     if ((R == kDq || R == kDk) && w.dots) {
+      const Lanes4 other(rows_of<T>(w.other, t, n), w.other.ld, sizeof(T), w.other.d, i16, c0 + 4 * g);
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
         const int row = 16 * rt + i16;
         float s = 0.f;
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
-          const f32x4 y = load4<T>(w.other, t + (row < n ? row : n - 1), c0 + 16 * x + 4 * g);
+          Four<T> y;
+          y.load(other, 16 * rt, 16 * x);
+          const f32x4 z = y.get();
 #pragma unroll
-          for (int r = 0; r < 4; ++r) s += acc[rt][x][r] * y[r];
+          for (int r = 0; r < 4; ++r) s += acc[rt][x][r] * z[r];
         }
         s += __shfl_xor(s, 16, 64);
         s += __shfl_xor(s, 32, 64);
         if (g == 0) m.dot[wave][row] = s;
       }
     }
+    // the next chunk's loads have the products below to arrive in (ahead of those above they would cost registers)
+    load(t_next, n_next);
+    decays(buf ^ 1, n_next);
+    lds_barrier();
     // the chunk's own part
     frag vf[2][NT];
     own_columns<T, DV, NT>(m.v, lv, c0, vf);
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
+    for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        if (BACK ? KB * (kb + 1) <= 16 * rt : KB * kb > 16 * rt) continue;
+      for (int c = OUT - 1; c >= 0; --c)
 #pragma unroll
-        for (int c = OUT - 1; c >= 0; --c) {
+        for (int rt = 0; rt < RT; ++rt) {
+          if (BACK ? KB * (kb + 1) <= 16 * rt : KB * kb > 16 * rt) continue;  // zeros of P
           const frag pf = row_frag<C>(m.p[c], lp, 16 * rt, KB * kb);
 #pragma unroll
           for (int x = 0; x < NT; ++x) acc[rt][x] = mma(vf[kb][x], pf, acc[rt][x]);
         }
-      }
+    auto out = [&](auto type, auto quads) {
+      typedef decltype(type) E;
+      const View y{w.out, (int64_t)a.H * w.v.d, w.v.d};
+      const Lanes4 to(rows_of<E>(y, t, n), y.ld, sizeof(E), y.d, i16, c0 + 4 * g);
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      const int row = 16 * rt + i16;
-      if (row < n) {
-        const int64_t at = (int64_t)(t + row) * a.H * w.v.d;
+      for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-        for (int x = 0; x < NT; ++x) {
-          if (w.wide) store4<float>((float*)w.out + at, c0 + 16 * x + 4 * g, w.v.d, acc[rt][x]);
-          else store4<T>((T*)w.out + at, c0 + 16 * x + 4 * g, w.v.d, acc[rt][x]);
-        }
-      }
-    }
-    if (keep) step_state<T, DK, NT, Pieces<T>::STATE>(m.k, lk, vf, m.d, lane, st);
-    else step_state<T, DK, NT, OUT>(m.k, lk, vf, m.d, lane, st);
+        for (int x = 0; x < NT; ++x) store4<E, quads.value>(to, 16 * rt, 16 * x, acc[rt][x]);
+    };
+    auto out_as = [&](auto type) {
+      if (w.v.d % 4 == 0) out(type, std::true_type{});
+      else out(type, std::false_type{});
+    };
+    if ((R == kDq || R == kDk) && w.wide) out_as(float{});
+    else out_as(T{});
+    step_state<T, DK, NT, KEPT ? Pieces<T>::STATE : OUT>(m.k, lk, vf, d, lane, st);
     lds_barrier();
     if ((R == kDq || R == kDk) && w.dots && (int)threadIdx.x < n) {
       const int row = threadIdx.x;
@@ -786,7 +1001,7 @@ __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w,
       }
       w.dots[t + row] = s;
     }
-    if (t_next < 0) break;
+    if (n_next == 0) break;
     if (single && one + 1 < whole_n) {
       ++one;
     } else {
@@ -795,6 +1010,7 @@ __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w,
     }
     t = t_next;
     n = n_next;
+    buf ^= 1;
   }
   if (w.dots) lds_barrier();  // dot and sums are read
 }
@@ -806,19 +1022,21 @@ __device__ __forceinline__ void sweep_slot(const LinearArgs& a, const Sweep& w, 
                                            float* seq_dot, float* slot_dot, SweepLds<T, DK, NT>& m) {
   constexpr bool BACK = R == kDk || R == kDv, TR = R == kDq || R == kDk;
   const Seqs seqs{a.cu, a.n_seqs, a.T, a.tokens};
-  const int lane = threadIdx.x & 63, c0 = uniform(threadIdx.x >> 6) * 16 * NT;
-  const int64_t floats = (int64_t)a.dk * a.dv;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int64_t floats = (int64_t)a.dk * a.dv, record = DK * 64 * NT;
   const int rows = w.q.d, cols = w.v.d;
-  State<DK / 16, NT> st;
+  // callers' states go through the inputs' LDS, in front of P
+  static_assert(State<DK, NT>::kLds <= sizeof(m.q) + sizeof(m.k) + sizeof(m.v), "");
+  float* lds = (float*)&m;
+  State<DK, NT> st;
   // all of P beside the tiles that are written stays zero
   for (int x = threadIdx.x; x < (int)(sizeof(m.p) / 16); x += kThreads) ((uint4*)m.p)[x] = make_uint4(0, 0, 0, 0);
-  if (threadIdx.x == 0) m.d.wild = 0;
+  if (threadIdx.x == 0) m.wild = 0;
   lds_barrier();
-  auto of_slot = [&](int i) { return enter + ((int64_t)i * a.H + h) * floats; };
+  auto of_slot = [&](int i) { return enter + ((int64_t)i * a.H + h) * record; };
   auto of_seq = [&](const float* p, int n) { return p ? p + ((int64_t)n * a.H + h) * floats : nullptr; };
   // <S, dS> at the end of a range
-  auto inner = [&](const float* p, float* out) {
-    float x = p ? st.template dot<TR>(p, rows, cols, c0, lane) : 0.f;
+  auto inner = [&](float x, float* out) {
     x = row_sum(x);
     x += __shfl_xor(x, 16, 64);
     x += __shfl_xor(x, 32, 64);
@@ -830,30 +1048,29 @@ __device__ __forceinline__ void sweep_slot(const LinearArgs& a, const Sweep& w, 
   auto piece = [&](int n, int start, int end, bool entered) {
     const bool done = end <= s.hi;
     const int stop = done ? end : s.hi;
-    if (BACK) st.template load<TR>(done ? of_seq(seq_state, n) : of_slot(s.slot + 1), rows, cols, c0, lane);
-    else st.template load<TR>(entered ? of_slot(s.slot - 1) : of_seq(seq_state, n), rows, cols, c0, lane);
+    // records: the state's own orientation forward, the transposed one backward
+    if (BACK ? !done : entered) st.template load<R == kDv>(of_slot(BACK ? s.slot + 1 : s.slot - 1), lane, wave);
+    else st.template load_caller<TR>(of_seq(seq_state, n), rows, cols, lds, lane, wave);
     const bool out = leave && (BACK ? !entered : done);
-    if (start < stop) sweep_range<T, DK, NT, R>(a, w, h, start, stop, out, m, st);
+    if (start < stop) sweep_range<T, DK, NT, R>(a, w, h, start, stop, m, st);
     if (R == kDq && w.dots) {
-      if (done) inner(of_seq(dht, n), seq_dot + (int64_t)n * a.H + h);
-      else inner(adj + ((int64_t)(s.slot + 1) * a.H + h) * floats, slot_dot + (int64_t)s.slot * a.H + h);
+      float x = 0.f;
+      if (!done) x = st.dot(adj + ((int64_t)(s.slot + 1) * a.H + h) * record, lane, wave);
+      else if (dht) x = st.template dot_caller<TR>(of_seq(dht, n), rows, cols, lds, lane, wave);
+      inner(x, (done ? seq_dot + (int64_t)n * a.H : slot_dot + (int64_t)s.slot * a.H) + h);
     }
-    if (out) st.template store<TR>(leave + ((int64_t)n * a.H + h) * floats, rows, cols, c0, lane);
+    if (out) st.template store_caller<TR>(leave + ((int64_t)n * a.H + h) * floats, rows, cols, lds, lane, wave);
   };
+  // the sequence that entered, then those that start here; the last slot also has the empty ones behind the last token
   int n = uniform(seqs.from(s.lo)), at = s.lo;
-  if (n > 0) {
-    const int end = uniform((int)seqs.end(n - 1));
-    if (end > s.lo) {
-      at = end;
-      piece(n - 1, s.lo, end, true);
-    }
-  }
-  // those that start here; the last slot also has the empty ones behind the last token
+  bool entered = n > 0 && uniform((int)seqs.end(n - 1)) > s.lo;
+  if (entered) --n;
   for (; n < a.n_seqs; ++n) {
     const Span range = seqs.next(n, &at);
     const int start = uniform(range.start), end = uniform(range.end);
     if (!s.last && start >= s.hi) break;
-    piece(n, start, end, false);
+    piece(n, start, end, entered);
+    entered = false;
   }
 }
 
@@ -1055,7 +1272,10 @@ linear_step(const LinearArgs a, float* __restrict__ state, T* __restrict__ o) {
   y = part[0][tid];
 #pragma unroll
   for (int w = 1; w < NW; ++w) y += part[w][tid];
-  store4<T>(o + nh * a.dv, c, a.dv, y);
+  const View out{o + h * a.dv, (int64_t)a.H * a.dv, a.dv};
+  const Lanes4 to(rows_of<T>(out, seq, 1), 0, sizeof(T), a.dv, 0, c);
+  if (quads) store4<T, true>(to, 0, 0, y);
+  else store4<T, false>(to, 0, 0, y);
 }
 
 // ---- launches ---------------------------------------------------------------------------------
@@ -1071,20 +1291,20 @@ int dispatch(int is_bf16, const LinearArgs& a, F&& f) {
   return is_bf16 ? dims(bf16_t{}) : dims(float{});
 }
 
-// the states that the slots hand on, and (backward) the gradients
-template <typename T, int DK, int DV>
-int states(const LinearArgs& a, const LinearPlan& p, const void* dout, const float* dht, char* ws, bool back,
-           hipStream_t st) {
+// the states that the slots hand on, and (BACK) the gradients
+template <typename T, int DK, int DV, bool BACK>
+int states(const LinearArgs& a, const LinearPlan& p, const void* dout, const float* dht, char* ws, hipStream_t st) {
   float *ends = (float*)(ws + p.end_off), *adj = (float*)(ws + p.adj_off);
   double* sums = (double*)(ws + p.sum_off);
   int* kinds = (int*)(ws + p.kind_off);
-  const unsigned sides = back ? 2 : 1;
-  hipError_t e = launch_kernel(linear_states<T, DK, DV / 64>, dim3((unsigned)linear_groups(p, a.H), sides),
-                               dim3(kThreads), st, a, (const T*)dout, dht, ends, adj, sums, kinds);
+  const unsigned sides = BACK ? 2 : 1;
+  const hipError_t e = launch_kernel(linear_states<T, BACK ? DV : DK, (BACK ? DK : DV) / 64, BACK>,
+                                     dim3((unsigned)linear_groups(p, a.H), sides), dim3(kThreads), st, a,
+                                     (const T*)dout, dht, ends, adj, sums, kinds);
   if (e != hipSuccess) return (int)e;
-  const int64_t floats = (int64_t)a.dk * a.dv;
-  return (int)launch_kernel(linear_chain, dim3((unsigned)(a.H * ceil_div(floats, 256)), sides), dim3(256), st, a.H,
-                            floats, (int)p.n_slots, ends, adj, sums, kinds);
+  const int64_t floats = DK * DV;
+  return (int)launch_kernel(linear_chain, dim3((unsigned)(a.H * floats / 256), sides), dim3(256), st, a.H, floats,
+                            (int)p.n_slots, ends, adj, sums, kinds);
 }
 
 }  // namespace
@@ -1095,7 +1315,7 @@ int launch_linear_forward(int is_bf16, const LinearArgs& a, const LinearPlan& p,
   return dispatch(is_bf16, a, [&](auto t, auto dims) {
     typedef decltype(t) T;
     if (p.carry) {
-      const int e = states<T, dims.DK, dims.DV>(a, p, nullptr, nullptr, (char*)ws, false, st);
+      const int e = states<T, dims.DK, dims.DV, false>(a, p, nullptr, nullptr, (char*)ws, st);
       if (e != 0) return e;
     }
     return (int)launch_kernel(linear_forward<T, dims.DK, dims.DV / 64>, dim3((unsigned)linear_groups(p, a.H)),
@@ -1118,7 +1338,7 @@ int launch_linear_backward(int is_bf16, const LinearArgs& a, const LinearPlan& p
     typedef decltype(t) T;
     char* w = (char*)ws;
     if (p.carry) {
-      const int e = states<T, dims.DK, dims.DV>(a, p, g.dout, g.dht, w, true, st);
+      const int e = states<T, dims.DK, dims.DV, true>(a, p, g.dout, g.dht, w, st);
       if (e != 0) return e;
     }
     const LinearWork x{(float*)(w + p.end_off),    (float*)(w + p.adj_off),     (float*)(w + p.dot_q_off),
