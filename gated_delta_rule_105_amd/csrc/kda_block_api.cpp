@@ -76,7 +76,7 @@ int check_linear(const kda_linear_desc_t* d, LinearSizes* s) {
 // False: a launch's grid would not fit.
 bool linear_plan(const kda_linear_desc_t* d, const LinearSizes& s, bool backward, kda::LinearPlan* p) {
   *p = kda::plan_linear(s.a.tokens, (int)s.t.seqs, d->T, d->n_seqs > 0, d->H, kda::device_compute_units(),
-                        kda::linear_record(d->d_k, d->d_v), backward);
+                        d->d_k, d->d_v, backward);
   if (backward) kda::plan_linear_shared(p, s.a.tokens, d->H, d->Hq, d->d_k);
   return kda::linear_fits(*p, s.a.tokens, d->H, kda::linear_record(d->d_k, d->d_v), d->Hq, d->d_k);
 }

@@ -47,10 +47,13 @@ struct LinearPlan {
 constexpr int linear_pad(int d) { return d <= 64 ? 64 : 128; }
 constexpr size_t linear_record(int dk, int dv) { return (size_t)linear_pad(dk) * linear_pad(dv); }
 
-inline LinearPlan plan_linear(int64_t tokens, int rows, int64_t T, bool packed, int H, int n_cu, size_t record,
+inline LinearPlan plan_linear(int64_t tokens, int rows, int64_t T, bool packed, int H, int n_cu, int dk, int dv,
                               bool backward) {
   LinearPlan p{};
   const int64_t cus = n_cu > 0 ? n_cu : 256;
+  dk = linear_pad(dk);
+  dv = linear_pad(dv);
+  const size_t record = (size_t)dk * dv;
   if (tokens == 0) {
     p.slot = 1;
     p.n_slots = 1;
@@ -58,9 +61,17 @@ inline LinearPlan plan_linear(int64_t tokens, int rows, int64_t T, bool packed, 
     p.slot = T;
     p.n_slots = rows;
   } else {
-    int64_t n = 2 * cus / H;
-    if (n < 1) n = 1;
-    p.slot = ceil_div(ceil_div(tokens, n), kLinearChunk) * kLinearChunk;
+    // Two workgroups for every compute unit, unless their states, one for every
+    // slot and head, then cost more than the second workgroup hides: at least
+    // the tokens whose keys and values are half a state (256 with 128 channels
+    // of both).  Shorter slots only where not even one each would be left.
+    auto slots_of = [&](int64_t groups) {
+      const int64_t n = groups / H < 1 ? 1 : groups / H;
+      return ceil_div(ceil_div(tokens, n), kLinearChunk) * kLinearChunk;
+    };
+    const int64_t two = slots_of(2 * cus), one = slots_of(cus);
+    const int64_t least = ceil_div(4 * dk * dv / (dk + dv), kLinearChunk) * kLinearChunk;
+    p.slot = two >= least ? two : one < least ? one : least;
     p.n_slots = ceil_div(tokens, p.slot);
   }
   p.carry = p.n_slots > 1 && (packed || p.slot % T != 0);
@@ -95,10 +106,10 @@ inline void plan_linear_shared(LinearPlan* p, int64_t tokens, int H, int Hq, int
 }
 
 inline int64_t linear_groups(const LinearPlan& p, int H) { return p.n_slots * (int64_t)H; }
-// The launches' grids: sweeps of 256 threads a slot and head (three roles of
-// them backward), the chain's states, the shared heads' sums.
+// The launches' grids: sweeps of 512 threads at most a slot and head (three
+// roles of them backward), the chain's states, the shared heads' sums.
 inline bool linear_fits(const LinearPlan& p, int64_t tokens, int H, size_t record, int Hq, int dk) {
-  return grid_fits(3 * linear_groups(p, H), 256) && grid_fits(H * (int64_t)record / 256, 256) &&
+  return grid_fits(3 * linear_groups(p, H), 512) && grid_fits(H * (int64_t)record / 256, 256) &&
          grid_fits(ceil_div(tokens * Hq * dk, 256), 256);
 }
 

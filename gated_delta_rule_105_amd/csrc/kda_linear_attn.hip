@@ -34,7 +34,9 @@ namespace {
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
-constexpr int kThreads = 256, kWaves = 4;
+// A workgroup has a wave for every 16 columns of the state (channels of V).
+template <int DV> constexpr int kWaves = DV / 16;
+template <int DV> constexpr int kThreads = 64 * kWaves<DV>;
 
 // Tokens of a chunk: both types then fill LDS alike.
 template <typename T> constexpr int kTokens = sizeof(T) == 2 ? 64 : 32;
@@ -90,15 +92,15 @@ __device__ __forceinline__ f32x4 col_frag(const float* X, const Lane<float, W>& 
   return x;
 }
 
-// Keeps the loads of x and y together, ahead of their first use.
-template <typename F>
-__device__ __forceinline__ void together(F (&x)[4], F (&y)[4]) {
-  asm volatile("" : "+v"(x[0]), "+v"(x[1]), "+v"(x[2]), "+v"(x[3]), "+v"(y[0]), "+v"(y[1]), "+v"(y[2]), "+v"(y[3]));
-}
-template <typename F>
-__device__ __forceinline__ void together(F (&x)[2], F (&y)[2]) {
-  asm volatile("" : "+v"(x[0]), "+v"(x[1]), "+v"(y[0]), "+v"(y[1]));
-}
+// x, formed anew (a move that the compiler takes for an exchange between
+// lanes): what follows from it, addresses and masks, is computed where it is
+// used and not kept in registers across the chunks.  Inline assembly would do
+// the same, but the wait states behind matrix instructions are counted by
+// what the compiler knows of the instructions between.
+__device__ __forceinline__ int here(int x) { return __builtin_amdgcn_update_dpp(x, x, 0xe4, 0xf, 0xf, false); }
+
+// Nothing is moved across: operands' loads stay together ahead of their first use.
+__device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
 
 // ---- operands rounded from fp32 ---------------------------------------------------
 // bf16 operands that are not inputs are sums of pieces of 8 bits each: two
@@ -165,11 +167,11 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const View& x, int64_t
 // C tokens of W channels on the way from memory to LDS, 16 bytes a lane;
 // zeros for rows and channels that are not there.  A row's last vector, where
 // the row ends inside it, is read from further ahead and moved down.
-template <typename T, int W> struct Stage {
-  static constexpr int VE = 16 / (int)sizeof(T), VPR = W / VE, RPP = kThreads / VPR, N = kTokens<T> / RPP;
+template <typename T, int W, int THREADS> struct Stage {
+  static constexpr int VE = 16 / (int)sizeof(T), VPR = W / VE, RPP = THREADS / VPR, N = kTokens<T> / RPP;
   uint4 v[N];
   __device__ __forceinline__ void load(const View& x, int tok, int n) {
-    const int c = (int)(threadIdx.x % VPR) * VE, r = (int)(threadIdx.x / VPR), step = (int)x.ld * (int)sizeof(T);
+    const int thread = here((int)threadIdx.x), c = thread % VPR * VE, r = thread / VPR, step = (int)x.ld * (int)sizeof(T);
     const __amdgpu_buffer_rsrc_t rows = rows_of<T>(x, tok, n);
     const int at = c + VE <= x.d ? c : x.d - VE;
     const uint32_t off = c < x.d && x.d >= VE ? (uint32_t)(r * step + at * (int)sizeof(T)) : kNowhere;
@@ -178,7 +180,7 @@ template <typename T, int W> struct Stage {
       v[i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(rows, off, i * RPP * step, 0));
   }
   __device__ __forceinline__ void store(T* X, const View& x, int tok, int n) {
-    const int c = (int)(threadIdx.x % VPR) * VE, r = (int)(threadIdx.x / VPR);
+    const int thread = here((int)threadIdx.x), c = thread % VPR * VE, r = thread / VPR;
     if (x.d % VE != 0 && x.d >= VE) {
       const bool tail = c < x.d && c + VE > x.d;
       const int bits = (VE - x.d % VE) * 8 * (int)sizeof(T);
@@ -311,7 +313,9 @@ __device__ __forceinline__ void store4(const Lanes4& l, int r0, int c1, const f3
                                             l.rows, off, row, 0);
     } else {
       typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), l.rows, off, row, 0);
+      // the row in the lanes' offset: a store of 16 bytes with a scalar one read registers that the next instruction had
+      // written already (the compiler leaves a wait state only without it)
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), l.rows, off + (uint32_t)row, 0, 0);
     }
   } else {
 #pragma unroll
@@ -395,21 +399,18 @@ template <typename T> struct Decays {
 
 // ---- states in registers ----------------------------------------------------------
 // State tiles: rows the channels that a product sums over (16 m + 4 g + r in
-// lane 16 g + i), columns a wave's own (16 (NT wave + t) + i).  Records in the
+// lane 16 g + i), columns a wave's own (16 wave + i).  Records in the
 // workspace hold whole tiles, padding included, in the order of the lanes:
 // tile (row tile, column tile) is 256 floats, a lane's four side by side.  A
 // role whose state is the transposed one (TR) reads them across.  The
-// caller's states are [d_k][d_v] and go through LDS, a column tile of every
-// wave at a time.
-template <int DK, int NT>
+// caller's states are [d_k][d_v] and go through LDS, 64 columns at a time.
+template <int DK, int DV>
 struct State {
-  static constexpr int M = DK / 16, DV = 64 * NT;
-  f32x4 s[M][NT];
+  static constexpr int M = DK / 16, THREADS = kThreads<DV>;
+  f32x4 s[M];
   __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int m = 0; m < M; ++m)
-#pragma unroll
-      for (int t = 0; t < NT; ++t) s[m][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    for (int m = 0; m < M; ++m) s[m] = (f32x4){0.f, 0.f, 0.f, 0.f};
   }
   // f(tile's four values, record's four values)
   template <bool TR, typename F>
@@ -417,55 +418,43 @@ struct State {
     const __amdgpu_buffer_rsrc_t rec = rsrc(p, DK * DV * 4);
     const int g = lane >> 4, i = lane & 15, off = 4 * (TR ? 64 * (i >> 2) + 16 * g + (i & 3) : 4 * lane);
 #pragma unroll
-    for (int m = 0; m < M; ++m)
+    for (int m = 0; m < M; ++m) {
+      f32x4 x;
+      if (TR) {
+        // row tile `wave`, column tile m of a record of DV rows and DK columns
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const int n = wave * NT + t;
-        f32x4 x;
-        if (TR) {
-          // row tile n, column tile m of a record of DV rows and DK columns
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            x[r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rec, off + 16 * r, (n * M + m) * 1024, 0));
-        } else {
-          x = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rec, off, (m * (DV / 16) + n) * 1024, 0));
-        }
-        f(m, t, x);
+        for (int r = 0; r < 4; ++r)
+          x[r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rec, off + 16 * r, (wave * M + m) * 1024, 0));
+      } else {
+        x = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rec, off, (m * (DV / 16) + wave) * 1024, 0));
       }
+      f(m, x);
+    }
   }
   template <bool TR>
   __device__ __forceinline__ void load(const float* p, int lane, int wave) {
-    with_record<TR>(p, lane, wave, [&](int m, int t, const f32x4& x) { s[m][t] = x; });
+    with_record<TR>(p, lane, wave, [&](int m, const f32x4& x) { s[m] = x; });
   }
   __device__ __forceinline__ void store(float* p, int lane, int wave) const {
 #pragma unroll
-    for (int m = 0; m < M; ++m)
-#pragma unroll
-      for (int t = 0; t < NT; ++t) *(f32x4*)(p + (m * (DV / 16) + wave * NT + t) * 256 + 4 * lane) = s[m][t];
+    for (int m = 0; m < M; ++m) *(f32x4*)(p + (m * (DV / 16) + wave) * 256 + 4 * lane) = s[m];
   }
   __device__ __forceinline__ float dot(const float* p, int lane, int wave) const {
     float sum = 0.f;
-    with_record<false>(p, lane, wave, [&](int m, int t, const f32x4& x) {
+    with_record<false>(p, lane, wave, [&](int m, const f32x4& x) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) sum += s[m][t][r] * x[r];
+      for (int r = 0; r < 4; ++r) sum += s[m][r] * x[r];
     });
     return sum;
   }
 
   // a caller's state, rows by cols of it (TR: held cols by rows)
   static constexpr int kLds = DK * 64 * 4;  // bytes
-  static constexpr int kEach = DK * 64 / kThreads;
-  // this thread's number, formed anew at every use: what follows from it is not kept in registers across the chunks
-  __device__ __forceinline__ static int thread() {
-    int x = (int)threadIdx.x;
-    asm volatile("" : "+v"(x));
-    return x;
-  }
-  // element j of a thread in column tile t of every wave: its place in memory (kNowhere: not there) and in LDS
+  static constexpr int kEach = DK * 64 / THREADS, kAhead = kEach < 16 ? kEach : 16;
+  // element j of a thread among columns 64 t .. 64 t + 63: its place in memory (kNowhere: not there) and in LDS
   template <bool TR>
   __device__ __forceinline__ static void place(int thread, int j, int t, int rows, int cols, uint32_t* off, int* at) {
-    const int x = thread + j * kThreads, c = TR ? x / DK : x % 64, row = TR ? x % DK : x / 64;
-    const int col = 16 * (NT * (c / 16) + t) + c % 16;
+    const int x = thread + j * THREADS, c = TR ? x / DK : x % 64, row = TR ? x % DK : x / 64, col = 64 * t + c;
     *off = row < rows && col < cols ? (uint32_t)((TR ? col * rows + row : row * cols + col) * 4) : kNowhere;
     *at = ((c / 16 * M + row / 16) * 64 + row % 16 / 4 * 16 + c % 16) * 4 + row % 4;
   }
@@ -474,39 +463,44 @@ struct State {
                                               F&& f) const {
     const __amdgpu_buffer_rsrc_t mem = rsrc(p, (uint32_t)(rows * cols * 4));
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int x = thread();
+    for (int t = 0; t < DV / 64; ++t) {
+      const int x = here((int)threadIdx.x);
       lds_barrier();
 #pragma unroll 1
-      for (int j0 = 0; j0 < kEach; j0 += 16) {
-        float y[16];
-        int at[16];
+      for (int j0 = 0; j0 < kEach; j0 += kAhead) {
+        float y[kAhead];
+        uint32_t off;
+        int at;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          uint32_t off;
-          place<TR>(x, j0 + j, t, rows, cols, &off, &at[j]);
+        for (int j = 0; j < kAhead; ++j) {
+          place<TR>(x, j0 + j, t, rows, cols, &off, &at);
           y[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(mem, off, 0, 0));
         }
+        const int again = here(x);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) lds[at[j]] = y[j];
+        for (int j = 0; j < kAhead; ++j) {
+          place<TR>(again, j0 + j, t, rows, cols, &off, &at);
+          lds[at] = y[j];
+        }
       }
       lds_barrier();
+      if (wave / 4 == t)
 #pragma unroll
-      for (int m = 0; m < M; ++m) f(m, t, *(const f32x4*)(lds + ((wave * M + m) * 64 + lane) * 4));
+        for (int m = 0; m < M; ++m) f(m, *(const f32x4*)(lds + ((wave % 4 * M + m) * 64 + lane) * 4));
     }
     lds_barrier();
   }
   template <bool TR>
   __device__ __forceinline__ void load_caller(const float* p, int rows, int cols, float* lds, int lane, int wave) {
     if (!p) return zero();
-    with_caller<TR>(p, rows, cols, lds, lane, wave, [&](int m, int t, const f32x4& x) { s[m][t] = x; });
+    with_caller<TR>(p, rows, cols, lds, lane, wave, [&](int m, const f32x4& x) { s[m] = x; });
   }
   template <bool TR>
   __device__ __forceinline__ float dot_caller(const float* p, int rows, int cols, float* lds, int lane, int wave) const {
     float sum = 0.f;
-    with_caller<TR>(p, rows, cols, lds, lane, wave, [&](int m, int t, const f32x4& x) {
+    with_caller<TR>(p, rows, cols, lds, lane, wave, [&](int m, const f32x4& x) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) sum += s[m][t][r] * x[r];
+      for (int r = 0; r < 4; ++r) sum += s[m][r] * x[r];
     });
     return sum;
   }
@@ -514,13 +508,14 @@ struct State {
   __device__ __forceinline__ void store_caller(float* p, int rows, int cols, float* lds, int lane, int wave) const {
     const __amdgpu_buffer_rsrc_t mem = rsrc(p, (uint32_t)(rows * cols * 4));
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int x = thread();
+    for (int t = 0; t < DV / 64; ++t) {
+      const int x = here((int)threadIdx.x);
       lds_barrier();
+      if (wave / 4 == t)
 #pragma unroll
-      for (int m = 0; m < M; ++m) *(f32x4*)(lds + ((wave * M + m) * 64 + lane) * 4) = s[m][t];
+        for (int m = 0; m < M; ++m) *(f32x4*)(lds + ((wave % 4 * M + m) * 64 + lane) * 4) = s[m];
       lds_barrier();
-#pragma unroll 16
+#pragma unroll 8
       for (int j = 0; j < kEach; ++j) {
         uint32_t off;
         int at;
@@ -535,30 +530,22 @@ struct State {
 // ---- a chunk's step of the state ------------------------------------------------------
 // S <- whole S + K^T (col V): V's fragments are this wave's own columns,
 // scaled and cut to pieces; K's are read from LDS as they are.
-template <typename T, int DK, int NT, int PIECES>
-__device__ __forceinline__ void step_state(const T* K, const Lane<T, DK>& lk, const typename Frag<T>::type (&vf)[2][NT],
-                                           const Decays<T>& d, int lane, State<DK, NT>& st) {
+template <typename T, int DK, int DV, int PIECES>
+__device__ __forceinline__ void step_state(const T* K, const Lane<T, DK>& lk, const typename Frag<T>::type (&vf)[2],
+                                           const Decays<T>& d, int lane, State<DK, DV>& st) {
   constexpr int KB = Elem<T>::KB;
   const int g = lane >> 4;
   const float whole = d.whole;
 #pragma unroll
-  for (int m = 0; m < DK / 16; ++m)
-#pragma unroll
-    for (int t = 0; t < NT; ++t) st.s[m][t] *= whole;
+  for (int m = 0; m < DK / 16; ++m) st.s[m] *= whole;
 #pragma unroll
   for (int kb = 0; kb < 2; ++kb) {
-    typename Frag<T>::type f[NT][PIECES];
-    f32x4 by[kAccs<T>];
+    typename Frag<T>::type f[PIECES];
+    f32x4 x[kAccs<T>];
+    widen(vf[kb], x);
 #pragma unroll
-    for (int h = 0; h < kAccs<T>; ++h) by[h] = *(const f32x4*)(d.col + KB * kb + 16 * h + 4 * g);
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      f32x4 x[kAccs<T>];
-      widen(vf[kb][t], x);
-#pragma unroll
-      for (int h = 0; h < kAccs<T>; ++h) x[h] *= by[h];
-      Pieces<T>::template cut<PIECES>(x, f[t]);
-    }
+    for (int h = 0; h < kAccs<T>; ++h) x[h] *= *(const f32x4*)(d.col + KB * kb + 16 * h + 4 * g);
+    Pieces<T>::template cut<PIECES>(x, f);
     // four row tiles at a time: a product's result is not wanted by the next
 #pragma unroll
     for (int m = 0; m < DK / 16; m += 4) {
@@ -568,20 +555,15 @@ __device__ __forceinline__ void step_state(const T* K, const Lane<T, DK>& lk, co
 #pragma unroll
       for (int p = PIECES - 1; p >= 0; --p)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int t = 0; t < NT; ++t) st.s[m + i][t] = mma(kf[i], f[t][p], st.s[m + i][t]);
+        for (int i = 0; i < 4; ++i) st.s[m + i] = mma(kf[i], f[p], st.s[m + i]);
     }
   }
 }
 
-template <typename T, int DV, int NT>
-__device__ __forceinline__ void own_columns(const T* V, const Lane<T, DV>& lv, int c0,
-                                            typename Frag<T>::type (&vf)[2][NT]) {
+template <typename T, int DV>
+__device__ __forceinline__ void own_columns(const T* V, const Lane<T, DV>& lv, int c0, typename Frag<T>::type (&vf)[2]) {
 #pragma unroll
-  for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-    for (int t = 0; t < NT; ++t) vf[kb][t] = col_frag<DV>(V, lv, Elem<T>::KB * kb, c0 + 16 * t);
+  for (int kb = 0; kb < 2; ++kb) vf[kb] = col_frag<DV>(V, lv, Elem<T>::KB * kb, c0);
 }
 
 // Slots, and what of a sequence passes through one.
@@ -603,19 +585,19 @@ struct Slot {
 // (blockIdx.y = 1) the gradient of the state at its start, of the sequence
 // that entered.  Rows and columns: k and v.  In the backward pass (TR) the
 // transposed states are wanted: v and k, and for the gradients dout and q.
-template <typename T, int DK, int NT, bool BACK>
+template <typename T, int DK, int DV, bool BACK>
 __device__ __forceinline__ void states_range(const LinearArgs& a, const View& k, const View& v, int h, int t0, int end,
-                                             char* smem, State<DK, NT>& st, double* total) {
-  constexpr int C = kTokens<T>, DV = 64 * NT;
+                                             char* smem, State<DK, DV>& st, double* total) {
+  constexpr int C = kTokens<T>, THREADS = kThreads<DV>;
   T* K = (T*)smem;
   T* V = (T*)(smem + kTileBytes<T, DK>);
   Decays<T>* d = (Decays<T>*)(smem + kTileBytes<T, DK> + kTileBytes<T, DV>);
-  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), c0 = wave * 16 * NT;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), c0 = wave * 16;
   const Lane<T, DK> lk(lane);
   const Lane<T, DV> lv(lane);
   const int chunks = (end - t0 + C - 1) / C;
-  Stage<T, DK> sk;
-  Stage<T, DV> sv;
+  Stage<T, DK, THREADS> sk;
+  Stage<T, DV, THREADS> sv;
   LogDecays<T> g(a, h);
   auto load = [&](int i) {
     const int t = t0 + (BACK ? chunks - 1 - i : i) * C, left = end - t < C ? end - t : C, n = i < chunks ? left : 0;
@@ -632,30 +614,30 @@ __device__ __forceinline__ void states_range(const LinearArgs& a, const View& k,
     lds_barrier();
     load(i + 1);
     if (total) *total += d->sum[C - 1];
-    typename Frag<T>::type vf[2][NT];
-    own_columns<T, DV, NT>(V, lv, c0, vf);
-    step_state<T, DK, NT, Pieces<T>::STATE>(K, lk, vf, *d, lane, st);
+    typename Frag<T>::type vf[2];
+    own_columns<T, DV>(V, lv, c0, vf);
+    step_state<T, DK, DV, Pieces<T>::STATE>(K, lk, vf, *d, lane, st);
     lds_barrier();
   }
 }
 
-template <typename T, int DK, int NT>
-constexpr int kStatesTiles = kTileBytes<T, DK> + kTileBytes<T, 64 * NT> + (int)sizeof(Decays<T>);
+template <typename T, int DK, int DV>
+constexpr int kStatesTiles = kTileBytes<T, DK> + kTileBytes<T, DV> + (int)sizeof(Decays<T>);
 // callers' states go through the same memory
-template <typename T, int DK, int NT>
-constexpr int kStatesLds = kStatesTiles<T, DK, NT> > State<DK, NT>::kLds ? kStatesTiles<T, DK, NT> : State<DK, NT>::kLds;
+template <typename T, int DK, int DV>
+constexpr int kStatesLds = kStatesTiles<T, DK, DV> > State<DK, DV>::kLds ? kStatesTiles<T, DK, DV> : State<DK, DV>::kLds;
 
-template <typename T, int DK, int NT, bool TR>
-__global__ void __launch_bounds__(kThreads, 2)
+template <typename T, int DK, int DV, bool TR>
+__global__ void __launch_bounds__(kThreads<DV>, 2 * kThreads<DV> / 256)
 linear_states(const LinearArgs a, const T* __restrict__ dout, const float* __restrict__ dht, float* __restrict__ ends,
               float* __restrict__ adj, double* __restrict__ sums, int* __restrict__ kinds) {
-  __shared__ __align__(16) char smem[kStatesLds<T, DK, NT>];
+  __shared__ __align__(16) char smem[kStatesLds<T, DK, DV>];
   const int h = (int)(blockIdx.x % (unsigned)a.H), hq = h / (a.H / a.Hq);
   const Slot w(a, (int)(blockIdx.x / (unsigned)a.H));
   const Seqs seqs{a.cu, a.n_seqs, a.T, a.tokens};
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const int64_t floats = (int64_t)a.dk * a.dv, at = ((int64_t)w.slot * a.H + h) * DK * 64 * NT;
-  State<DK, NT> st;
+  const int64_t floats = (int64_t)a.dk * a.dv, at = ((int64_t)w.slot * a.H + h) * DK * DV;
+  State<DK, DV> st;
   const int first = uniform(seqs.from(w.lo)), before = first > 0 ? uniform((int)seqs.end(first - 1)) : w.lo;
   const bool entered = before > w.lo;
   double total = 0.0;
@@ -670,7 +652,7 @@ linear_states(const LinearArgs a, const T* __restrict__ dout, const float* __res
     st.template load_caller<TR>(own && a.h0 ? a.h0 + ((int64_t)n * a.H + h) * floats : nullptr, TR ? a.dv : a.dk,
                                 TR ? a.dk : a.dv, (float*)smem, lane, wave);
     const View k{(const T*)a.k + hq * a.dk, a.ld_k, a.dk}, v{(const T*)a.v + h * a.dv, a.ld_v, a.dv};
-    states_range<T, DK, NT, false>(a, TR ? v : k, TR ? k : v, h, own ? start : w.lo, w.hi, smem, st, &total);
+    states_range<T, DK, DV, false>(a, TR ? v : k, TR ? k : v, h, own ? start : w.lo, w.hi, smem, st, &total);
     st.store(ends + at, lane, wave);
     if (!own && threadIdx.x == 0) sums[(int64_t)w.slot * a.H + h] = total;
   } else if constexpr (TR) {
@@ -679,7 +661,7 @@ linear_states(const LinearArgs a, const T* __restrict__ dout, const float* __res
     st.template load_caller<TR>(ends_here && dht ? dht + ((int64_t)(first - 1) * a.H + h) * floats : nullptr, a.dv, a.dk,
                                 (float*)smem, lane, wave);
     const View q{(const T*)a.q + hq * a.dk, a.ld_q, a.dk}, d{dout + h * a.dv, (int64_t)a.H * a.dv, a.dv};
-    states_range<T, DK, NT, true>(a, d, q, h, w.lo, ends_here ? before : w.hi, smem, st, nullptr);
+    states_range<T, DK, DV, true>(a, d, q, h, w.lo, ends_here ? before : w.hi, smem, st, nullptr);
     st.store(adj + at, lane, wave);
   }
 }
@@ -734,13 +716,13 @@ struct Sweep {
   float* dots;      // [H, tokens], this head's row (null: none)
 };
 
-template <typename T, int DK, int NT>
+template <typename T, int DK, int DV>
 struct SweepLds {
-  T q[kTokens<T> * kLd<DK>], k[kTokens<T> * kLd<DK>], v[kTokens<T> * kLd<64 * NT>];
+  T q[kTokens<T> * kLd<DK>], k[kTokens<T> * kLd<DK>], v[kTokens<T> * kLd<DV>];
   T p[Pieces<T>::OUT][kTokens<T> * kLd<kTokens<T>>];
   Decays<T> d[2];  // of this chunk and the next
   int wild;
-  float dot[kWaves][kTokens<T>];
+  float dot[kWaves<DV>][kTokens<T>];
   float sums[10][2][16];  // row and column sums of M's tiles
 };
 
@@ -751,23 +733,20 @@ __device__ __forceinline__ void tile_of(int t, int* a, int* b) {
 }
 
 // Tokens [t0, end) of one sequence; the state before them (BACK: the gradient
-// of the state after them) in, that after (before) them out.
-template <typename T, int DK, int NT, Role R>
+// of the state after them) comes from `enter`, called when the first loads are
+// under way, and that after (before) them is left in st.
+template <typename T, int DK, int DV, Role R, typename F>
 __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w, int h, int t0, int end,
-                                            SweepLds<T, DK, NT>& m, State<DK, NT>& st) {
+                                            SweepLds<T, DK, DV>& m, State<DK, DV>& st, F&& enter) {
   // the state of these two roles is handed out at a sequence's end
   constexpr bool BACK = R == kDk || R == kDv, M_SUMS = R == kDq, KEPT = R == kForward || R == kDv;
-  constexpr int C = kTokens<T>, DV = 64 * NT, KB = Elem<T>::KB, RT = C / 16, TILES = RT * (RT + 1) / 2;
-  constexpr int OUT = Pieces<T>::OUT;
+  constexpr int C = kTokens<T>, KB = Elem<T>::KB, RT = C / 16, TILES = RT * (RT + 1) / 2;
+  constexpr int OUT = Pieces<T>::OUT, WAVES = kWaves<DV>, THREADS = kThreads<DV>;
   typedef typename Frag<T>::type frag;
-  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), c0 = wave * 16 * NT;
-  const int g = lane >> 4, i16 = lane & 15;
-  const Lane<T, DK> lk(lane);
-  const Lane<T, DV> lv(lane);
-  const Lane<T, C> lp(lane);
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), c0 = wave * 16;
   const int chunks = (end - t0 + C - 1) / C;
-  Stage<T, DK> sq, sk;
-  Stage<T, DV> sv;
+  Stage<T, DK, THREADS> sq, sk;
+  Stage<T, DV, THREADS> sv;
   LogDecays<T> gd(a, h);
   auto load = [&](int t, int n) {
     sq.load(w.q, t, n);
@@ -783,10 +762,11 @@ __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w,
   bool single = false;
   // one wave does the decays of a chunk, ahead of it
   auto decays = [&](int b, int n) {
-    if (wave == kWaves - 1) m.d[b].fill(gd.get(), n, BACK, w.row_scale, w.col_scale, lane);
+    if (wave == WAVES - 1) m.d[b].fill(gd.get(), n, BACK, w.row_scale, w.col_scale, lane);
   };
   gd.load(t, n, lane);
   load(t, n);
+  enter();
   decays(0, n);
   while (true) {
     if (!single && n > 1 && __ballot(sv.wild(w.v)) != 0 && lane == 0) m.wild = 1;
@@ -822,6 +802,9 @@ __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w,
 
     // P, shared out by tiles
     auto p_tile = [&](int tile) {
+      const int ln = here(lane), g = ln >> 4, i16 = ln & 15;
+      const Lane<T, DK> lk(ln);
+      const Lane<T, C> lp(ln);
       int ra, rb;
       tile_of(tile, &ra, &rb);
       const int rt = BACK ? rb : ra, ct = BACK ? ra : rb;
@@ -836,19 +819,17 @@ __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w,
           x[u] = row_frag<DK>(m.k, lk, 16 * ct, KB * (kb + u));
           y[u] = row_frag<DK>(m.q, lk, 16 * rt, KB * (kb + u));
         }
-        together(x, y);
+        fence();
 #pragma unroll
         for (int u = 0; u < U; ++u) acc = mma(x[u], y[u], acc);
       }
       const double gi = d.sum[16 * rt + i16];
-      int at = i16 - 4 * g + 16 * (rt - ct);  // row minus column, of r = 0
-      asm volatile("" : "+v"(at));            // masks are compared here, not kept in registers across the loop
+      const int at = i16 - 4 * g + 16 * (rt - ct);  // row minus column, of r = 0
       f32x4 p;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const double gj = d.sum[16 * ct + 4 * g + r];
-        float x = acc[r] * (decay_of(BACK ? gj - gi : gi - gj) * w.p_scale);
-        asm volatile("" : "+v"(x));  // a select, not a branch around the factor
+        const float x = acc[r] * (decay_of(BACK ? gj - gi : gi - gj) * w.p_scale);
         p[r] = (BACK ? at <= r : at >= r) ? x : 0.f;
       }
       if (M_SUMS && w.dots) {
@@ -866,13 +847,12 @@ __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w,
           } else {
             qf = x.get();
           }
-          s = mma(row_frag<DV>(m.v, lv, 16 * ct, KB * kb), qf, s);
+          s = mma(row_frag<DV>(m.v, Lane<T, DV>(ln), 16 * ct, KB * kb), qf, s);
         }
         float across = 0.f;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          float x = s[r] * p[r];
-          asm volatile("" : "+v"(x));
+          const float x = s[r] * p[r];
           s[r] = at > r ? x : 0.f;
           across += s[r];
           s[r] = row_sum(s[r]);
@@ -897,60 +877,43 @@ __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w,
         }
       }
     };
-    if constexpr (TILES >= 2 * kWaves) {
-      p_tile(wave);
-      p_tile(wave + kWaves);
-      if (wave + 2 * kWaves < TILES) p_tile(wave + 2 * kWaves);
-    } else {
-      if (wave < TILES) p_tile(wave);
-    }
+#pragma unroll 1
+    for (int tile = wave; tile < TILES; tile += WAVES) p_tile(tile);
 
     // the state's part of the outputs, transposed: rows are channels of V, columns tokens
-    f32x4 acc[RT][NT];
+    const int ln = here(lane), g = ln >> 4, i16 = ln & 15;
+    const Lane<T, DK> lk(ln);
+    f32x4 acc[RT];
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-      for (int x = 0; x < NT; ++x) acc[rt][x] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    for (int rt = 0; rt < RT; ++rt) acc[rt] = (f32x4){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int kb = 0; kb < DK / KB; ++kb) {
-      frag sf[NT][OUT];
+      frag sf[OUT];
+      f32x4 s[kAccs<T>];
 #pragma unroll
-      for (int x = 0; x < NT; ++x) {
-        f32x4 s[kAccs<T>];
-#pragma unroll
-        for (int e = 0; e < kAccs<T>; ++e) s[e] = st.s[kAccs<T> * kb + e][x];
-        Pieces<T>::template cut<OUT>(s, sf[x]);
-      }
+      for (int e = 0; e < kAccs<T>; ++e) s[e] = st.s[kAccs<T> * kb + e];
+      Pieces<T>::template cut<OUT>(s, sf);
       frag qf[RT];
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) qf[rt] = row_frag<DK>(m.q, lk, 16 * rt, KB * kb);
 #pragma unroll
       for (int c = OUT - 1; c >= 0; --c)
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-          for (int x = 0; x < NT; ++x) acc[rt][x] = mma(sf[x][c], qf[rt], acc[rt][x]);
+        for (int rt = 0; rt < RT; ++rt) acc[rt] = mma(sf[c], qf[rt], acc[rt]);
     }
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      const float by = d.row[16 * rt + i16];
-#pragma unroll
-      for (int x = 0; x < NT; ++x) acc[rt][x] *= by;
-    }
+    for (int rt = 0; rt < RT; ++rt) acc[rt] *= d.row[16 * rt + i16];
     if ((R == kDq || R == kDk) && w.dots) {
       const Lanes4 other(rows_of<T>(w.other, t, n), w.other.ld, sizeof(T), w.other.d, i16, c0 + 4 * g);
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
         const int row = 16 * rt + i16;
         float s = 0.f;
+        Four<T> y;
+        y.load(other, 16 * rt, 0);
+        const f32x4 z = y.get();
 #pragma unroll
-        for (int x = 0; x < NT; ++x) {
-          Four<T> y;
-          y.load(other, 16 * rt, 16 * x);
-          const f32x4 z = y.get();
-#pragma unroll
-          for (int r = 0; r < 4; ++r) s += acc[rt][x][r] * z[r];
-        }
+        for (int r = 0; r < 4; ++r) s += acc[rt][r] * z[r];
         s += __shfl_xor(s, 16, 64);
         s += __shfl_xor(s, 32, 64);
         if (g == 0) m.dot[wave][row] = s;
@@ -961,8 +924,9 @@ __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w,
     decays(buf ^ 1, n_next);
     lds_barrier();
     // the chunk's own part
-    frag vf[2][NT];
-    own_columns<T, DV, NT>(m.v, lv, c0, vf);
+    const Lane<T, C> lp(ln);
+    frag vf[2];
+    own_columns<T, DV>(m.v, Lane<T, DV>(ln), c0, vf);
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
@@ -970,18 +934,14 @@ __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w,
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
           if (BACK ? KB * (kb + 1) <= 16 * rt : KB * kb > 16 * rt) continue;  // zeros of P
-          const frag pf = row_frag<C>(m.p[c], lp, 16 * rt, KB * kb);
-#pragma unroll
-          for (int x = 0; x < NT; ++x) acc[rt][x] = mma(vf[kb][x], pf, acc[rt][x]);
+          acc[rt] = mma(vf[kb], row_frag<C>(m.p[c], lp, 16 * rt, KB * kb), acc[rt]);
         }
     auto out = [&](auto type, auto quads) {
       typedef decltype(type) E;
       const View y{w.out, (int64_t)a.H * w.v.d, w.v.d};
       const Lanes4 to(rows_of<E>(y, t, n), y.ld, sizeof(E), y.d, i16, c0 + 4 * g);
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int x = 0; x < NT; ++x) store4<E, quads.value>(to, 16 * rt, 16 * x, acc[rt][x]);
+      for (int rt = 0; rt < RT; ++rt) store4<E, quads.value>(to, 16 * rt, 0, acc[rt]);
     };
     auto out_as = [&](auto type) {
       if (w.v.d % 4 == 0) out(type, std::true_type{});
@@ -989,11 +949,13 @@ __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w,
     };
     if ((R == kDq || R == kDk) && w.wide) out_as(float{});
     else out_as(T{});
-    step_state<T, DK, NT, KEPT ? Pieces<T>::STATE : OUT>(m.k, lk, vf, d, lane, st);
+    step_state<T, DK, DV, KEPT ? Pieces<T>::STATE : OUT>(m.k, Lane<T, DK>(here(lane)), vf, d, lane, st);
     lds_barrier();
     if ((R == kDq || R == kDk) && w.dots && (int)threadIdx.x < n) {
       const int row = threadIdx.x;
-      float s = m.dot[0][row] + m.dot[1][row] + m.dot[2][row] + m.dot[3][row];
+      float s = 0.f;
+#pragma unroll
+      for (int x = 0; x < WAVES; ++x) s += m.dot[x][row];
       if (M_SUMS) {
         const int mt = row / 16;
         for (int b = 0; b <= mt; ++b) s += m.sums[mt * (mt + 1) / 2 + b][0][row % 16];
@@ -1016,21 +978,21 @@ __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w,
 }
 
 // One slot of one head.  dS: what a sequence's last state's inner product with its gradient is wanted of.
-template <typename T, int DK, int NT, Role R>
+template <typename T, int DK, int DV, Role R>
 __device__ __forceinline__ void sweep_slot(const LinearArgs& a, const Sweep& w, int h, const Slot& s, const float* enter,
                                            const float* seq_state, float* leave, const float* dht, const float* adj,
-                                           float* seq_dot, float* slot_dot, SweepLds<T, DK, NT>& m) {
+                                           float* seq_dot, float* slot_dot, SweepLds<T, DK, DV>& m) {
   constexpr bool BACK = R == kDk || R == kDv, TR = R == kDq || R == kDk;
   const Seqs seqs{a.cu, a.n_seqs, a.T, a.tokens};
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const int64_t floats = (int64_t)a.dk * a.dv, record = DK * 64 * NT;
+  const int64_t floats = (int64_t)a.dk * a.dv, record = DK * DV;
   const int rows = w.q.d, cols = w.v.d;
   // callers' states go through the inputs' LDS, in front of P
-  static_assert(State<DK, NT>::kLds <= sizeof(m.q) + sizeof(m.k) + sizeof(m.v), "");
+  static_assert(State<DK, DV>::kLds <= sizeof(m.q) + sizeof(m.k) + sizeof(m.v), "");
   float* lds = (float*)&m;
-  State<DK, NT> st;
+  State<DK, DV> st;
   // all of P beside the tiles that are written stays zero
-  for (int x = threadIdx.x; x < (int)(sizeof(m.p) / 16); x += kThreads) ((uint4*)m.p)[x] = make_uint4(0, 0, 0, 0);
+  for (int x = threadIdx.x; x < (int)(sizeof(m.p) / 16); x += kThreads<DV>) ((uint4*)m.p)[x] = make_uint4(0, 0, 0, 0);
   if (threadIdx.x == 0) m.wild = 0;
   lds_barrier();
   auto of_slot = [&](int i) { return enter + ((int64_t)i * a.H + h) * record; };
@@ -1042,17 +1004,25 @@ __device__ __forceinline__ void sweep_slot(const LinearArgs& a, const Sweep& w, 
     x += __shfl_xor(x, 32, 64);
     if (lane == 0) m.dot[threadIdx.x >> 6][0] = x;
     lds_barrier();
-    if (threadIdx.x == 0) *out = m.dot[0][0] + m.dot[1][0] + m.dot[2][0] + m.dot[3][0];
+    if (threadIdx.x == 0) {
+      float sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWaves<DV>; ++w) sum += m.dot[w][0];
+      *out = sum;
+    }
     lds_barrier();
   };
   auto piece = [&](int n, int start, int end, bool entered) {
     const bool done = end <= s.hi;
     const int stop = done ? end : s.hi;
-    // records: the state's own orientation forward, the transposed one backward
-    if (BACK ? !done : entered) st.template load<R == kDv>(of_slot(BACK ? s.slot + 1 : s.slot - 1), lane, wave);
-    else st.template load_caller<TR>(of_seq(seq_state, n), rows, cols, lds, lane, wave);
+    auto enter_state = [&] {
+      // records: the state's own orientation forward, the transposed one backward
+      if (BACK ? !done : entered) st.template load<R == kDv>(of_slot(BACK ? s.slot + 1 : s.slot - 1), lane, wave);
+      else st.template load_caller<TR>(of_seq(seq_state, n), rows, cols, lds, lane, wave);
+    };
     const bool out = leave && (BACK ? !entered : done);
-    if (start < stop) sweep_range<T, DK, NT, R>(a, w, h, start, stop, m, st);
+    if (start < stop) sweep_range<T, DK, DV, R>(a, w, h, start, stop, m, st, enter_state);
+    else enter_state();
     if (R == kDq && w.dots) {
       float x = 0.f;
       if (!done) x = st.dot(adj + ((int64_t)(s.slot + 1) * a.H + h) * record, lane, wave);
@@ -1074,10 +1044,10 @@ __device__ __forceinline__ void sweep_slot(const LinearArgs& a, const Sweep& w, 
   }
 }
 
-template <typename T, int DK, int NT>
-__global__ void __launch_bounds__(kThreads, 2)
+template <typename T, int DK, int DV>
+__global__ void __launch_bounds__(kThreads<DV>, 2 * kThreads<DV> / 256)
 linear_forward(const LinearArgs a, const float* __restrict__ ends, T* __restrict__ o, float* __restrict__ ht) {
-  __shared__ __align__(16) SweepLds<T, DK, NT> m;
+  __shared__ __align__(16) SweepLds<T, DK, DV> m;
   const int h = (int)(blockIdx.x % (unsigned)a.H), hq = h / (a.H / a.Hq);
   const Slot s(a, (int)(blockIdx.x / (unsigned)a.H));
   Sweep w{};
@@ -1087,7 +1057,7 @@ linear_forward(const LinearArgs a, const float* __restrict__ ends, T* __restrict
   w.out = o + h * a.dv;
   w.p_scale = w.row_scale = a.scale;
   w.col_scale = 1.f;
-  sweep_slot<T, DK, NT, kForward>(a, w, h, s, ends, a.h0, ht, nullptr, nullptr, nullptr, nullptr, m);
+  sweep_slot<T, DK, DV, kForward>(a, w, h, s, ends, a.h0, ht, nullptr, nullptr, nullptr, nullptr, m);
 }
 
 // Where the backward pass's launches leave what others read.
@@ -1125,26 +1095,30 @@ __device__ __forceinline__ void gradient(const LinearArgs& a, const LinearGrads&
     if (shared) w.out = (R == kDq ? x.dq : x.dk) + h * a.dk;
     else w.out = (T*)(R == kDq ? g.dq : g.dk) + h * a.dk;
   }
-  sweep_slot<T, R == kDv ? DK : DV, (R == kDv ? DV : DK) / 64, R>(
+  sweep_slot<T, R == kDv ? DK : DV, R == kDv ? DV : DK, R>(
       a, w, h, s, enter, R == kDq ? a.h0 : g.dht, R == kDv ? g.dh0 : nullptr, g.dht, x.adj, x.seq_dot, x.slot_dot,
-      *(SweepLds<T, R == kDv ? DK : DV, (R == kDv ? DV : DK) / 64>*)smem);
+      *(SweepLds<T, R == kDv ? DK : DV, R == kDv ? DV : DK>*)smem);
 }
 
-template <typename T, int DK, int DV>
-constexpr int kBackwardLds = sizeof(SweepLds<T, DK, DV / 64>) > sizeof(SweepLds<T, DV, DK / 64>)
-                                 ? sizeof(SweepLds<T, DK, DV / 64>)
-                                 : sizeof(SweepLds<T, DV, DK / 64>);
-
-template <typename T, int DK, int DV>
-__global__ void __launch_bounds__(kThreads, 2)
+// The workgroups of a launch take its roles in turn: all three where their
+// workgroups are of one size, else those with columns of d_k, and dv alone.
+template <typename T, int DK, int DV, Role FIRST, int COUNT>
+__global__ void __launch_bounds__(kThreads<FIRST == kDv ? DV : DK>, 2 * kThreads<FIRST == kDv ? DV : DK> / 256)
 linear_backward(const LinearArgs a, const LinearGrads g, const LinearWork x) {
-  __shared__ __align__(16) char smem[kBackwardLds<T, DK, DV>];
-  const unsigned role = blockIdx.x % 3, id = blockIdx.x / 3;
+  typedef SweepLds<T, DV, DK> OfKeys;
+  typedef SweepLds<T, DK, DV> OfValues;
+  constexpr size_t keys = FIRST == kDv ? 0 : sizeof(OfKeys), values = FIRST == kDv || COUNT == 3 ? sizeof(OfValues) : 0;
+  __shared__ __align__(16) char smem[keys > values ? keys : values];
+  const unsigned role = blockIdx.x % COUNT, id = blockIdx.x / COUNT;
   const int h = (int)(id % (unsigned)a.H);
   const Slot s(a, (int)(id / (unsigned)a.H));
-  if (role == 0) gradient<T, DK, DV, kDq>(a, g, x, h, s, smem);
-  else if (role == 1) gradient<T, DK, DV, kDk>(a, g, x, h, s, smem);
-  else gradient<T, DK, DV, kDv>(a, g, x, h, s, smem);
+  if constexpr (FIRST == kDv) {
+    gradient<T, DK, DV, kDv>(a, g, x, h, s, smem);
+  } else {
+    if (role == 0) gradient<T, DK, DV, kDq>(a, g, x, h, s, smem);
+    else if (role == 1) gradient<T, DK, DV, kDk>(a, g, x, h, s, smem);
+    else if constexpr (COUNT == 3) gradient<T, DK, DV, kDv>(a, g, x, h, s, smem);
+  }
 }
 
 // The decays' gradients: a wave takes one slot of one head, 64 tokens at a
@@ -1298,9 +1272,9 @@ int states(const LinearArgs& a, const LinearPlan& p, const void* dout, const flo
   double* sums = (double*)(ws + p.sum_off);
   int* kinds = (int*)(ws + p.kind_off);
   const unsigned sides = BACK ? 2 : 1;
-  const hipError_t e = launch_kernel(linear_states<T, BACK ? DV : DK, (BACK ? DK : DV) / 64, BACK>,
-                                     dim3((unsigned)linear_groups(p, a.H), sides), dim3(kThreads), st, a,
-                                     (const T*)dout, dht, ends, adj, sums, kinds);
+  constexpr int ROWS = BACK ? DV : DK, COLS = BACK ? DK : DV;
+  const hipError_t e = launch_kernel(linear_states<T, ROWS, COLS, BACK>, dim3((unsigned)linear_groups(p, a.H), sides),
+                                     dim3(kThreads<COLS>), st, a, (const T*)dout, dht, ends, adj, sums, kinds);
   if (e != hipSuccess) return (int)e;
   const int64_t floats = DK * DV;
   return (int)launch_kernel(linear_chain, dim3((unsigned)(a.H * floats / 256), sides), dim3(256), st, a.H, floats,
@@ -1318,8 +1292,8 @@ int launch_linear_forward(int is_bf16, const LinearArgs& a, const LinearPlan& p,
       const int e = states<T, dims.DK, dims.DV, false>(a, p, nullptr, nullptr, (char*)ws, st);
       if (e != 0) return e;
     }
-    return (int)launch_kernel(linear_forward<T, dims.DK, dims.DV / 64>, dim3((unsigned)linear_groups(p, a.H)),
-                              dim3(kThreads), st, a, (const float*)((char*)ws + p.end_off), (T*)o, ht);
+    return (int)launch_kernel(linear_forward<T, dims.DK, dims.DV>, dim3((unsigned)linear_groups(p, a.H)),
+                              dim3(kThreads<dims.DV>), st, a, (const float*)((char*)ws + p.end_off), (T*)o, ht);
   });
 }
 
@@ -1345,7 +1319,17 @@ int launch_linear_backward(int is_bf16, const LinearArgs& a, const LinearPlan& p
                        (float*)(w + p.dot_k_off),  (float*)(w + p.slot_dot_off), (float*)(w + p.seq_dot_off),
                        (float*)(w + p.dq_off),     (float*)(w + p.dk_off)};
     const unsigned groups = (unsigned)linear_groups(p, a.H);
-    hipError_t e = launch_kernel(linear_backward<T, dims.DK, dims.DV>, dim3(3 * groups), dim3(kThreads), st, a, g, x);
+    hipError_t e;
+    if constexpr (dims.DK == dims.DV) {
+      e = launch_kernel(linear_backward<T, dims.DK, dims.DV, kDq, 3>, dim3(3 * groups), dim3(kThreads<dims.DK>), st, a, g,
+                        x);
+    } else {
+      e = launch_kernel(linear_backward<T, dims.DK, dims.DV, kDq, 2>, dim3(2 * groups), dim3(kThreads<dims.DK>), st, a, g,
+                        x);
+      if (e == hipSuccess)
+        e = launch_kernel(linear_backward<T, dims.DK, dims.DV, kDv, 1>, dim3(groups), dim3(kThreads<dims.DV>), st, a, g,
+                          x);
+    }
     if (e != hipSuccess) return (int)e;
     if (a.H != a.Hq && a.tokens > 0) {
       const int64_t n = a.tokens * a.Hq * a.dk;
