@@ -109,7 +109,7 @@ inline int64_t linear_groups(const LinearPlan& p, int H) { return p.n_slots * (i
 // The launches' grids: sweeps of 512 threads at most a slot and head (three
 // roles of them backward), the chain's states, the shared heads' sums.
 inline bool linear_fits(const LinearPlan& p, int64_t tokens, int H, size_t record, int Hq, int dk) {
-  return grid_fits(3 * linear_groups(p, H), 512) && grid_fits(H * (int64_t)record / 256, 256) &&
+  return grid_fits(3 * linear_groups(p, H), 512) && grid_fits(H * (int64_t)record / 1024, 256) &&
          grid_fits(ceil_div(tokens * Hq * dk, 256), 256);
 }
 

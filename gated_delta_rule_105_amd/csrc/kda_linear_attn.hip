@@ -585,44 +585,63 @@ struct Slot {
 // (blockIdx.y = 1) the gradient of the state at its start, of the sequence
 // that entered.  Rows and columns: k and v.  In the backward pass (TR) the
 // transposed states are wanted: v and k, and for the gradients dout and q.
-template <typename T, int DK, int DV, bool BACK>
+template <typename T, int DK, int DV, bool BACK, typename F>
 __device__ __forceinline__ void states_range(const LinearArgs& a, const View& k, const View& v, int h, int t0, int end,
-                                             char* smem, State<DK, DV>& st, double* total) {
+                                             char* smem, State<DK, DV>& st, double* total, F&& enter) {
   constexpr int C = kTokens<T>, THREADS = kThreads<DV>;
   T* K = (T*)smem;
   T* V = (T*)(smem + kTileBytes<T, DK>);
-  Decays<T>* d = (Decays<T>*)(smem + kTileBytes<T, DK> + kTileBytes<T, DV>);
+  Decays<T>* const both = (Decays<T>*)(smem + kTileBytes<T, DK> + kTileBytes<T, DV>);  // of this chunk and the next
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), c0 = wave * 16;
   const Lane<T, DK> lk(lane);
   const Lane<T, DV> lv(lane);
   const int chunks = (end - t0 + C - 1) / C;
-  Stage<T, DK, THREADS> sk;
-  Stage<T, DV, THREADS> sv;
+  // Chunks are loaded two ahead: one chunk's products are shorter than memory
+  // takes with a workgroup or two on a compute unit.
+  Stage<T, DK, THREADS> sk[2];
+  Stage<T, DV, THREADS> sv[2];
   LogDecays<T> g(a, h);
-  auto load = [&](int i) {
-    const int t = t0 + (BACK ? chunks - 1 - i : i) * C, left = end - t < C ? end - t : C, n = i < chunks ? left : 0;
-    sk.load(k, n ? t : t0, n);
-    sv.load(v, n ? t : t0, n);
-    g.load(n ? t : t0, n, lane);
+  auto start_of = [&](int i) { return i < chunks ? t0 + (BACK ? chunks - 1 - i : i) * C : t0; };
+  auto size_of = [&](int i) {
+    const int left = end - start_of(i), n = left < C ? left : C;
+    return i < chunks ? n : 0;
   };
-  load(0);
-  for (int i = 0; i < chunks; ++i) {
-    const int t = t0 + (BACK ? chunks - 1 - i : i) * C, n = end - t < C ? end - t : C;
-    sk.store(K, k, t, n);
-    sv.store(V, v, t, n);
-    if (wave == 0) d->fill(g.get(), n, BACK, 1.f, BACK ? a.scale : 1.f, lane);
+  auto load = [&](auto set, int i) {
+    sk[set.value].load(k, start_of(i), size_of(i));
+    sv[set.value].load(v, start_of(i), size_of(i));
+  };
+  auto decays = [&](int i) {
+    if (wave == 0) both[i & 1].fill(g.get(), size_of(i), BACK, 1.f, BACK ? a.scale : 1.f, lane);
+  };
+  auto chunk = [&](auto set, int i) {
+    sk[set.value].store(K, k, start_of(i), size_of(i));
+    sv[set.value].store(V, v, start_of(i), size_of(i));
     lds_barrier();
-    load(i + 1);
+    const Decays<T>* d = both + (i & 1);
+    load(set, i + 2);
+    g.load(start_of(i + 1), size_of(i + 1), lane);
     if (total) *total += d->sum[C - 1];
     typename Frag<T>::type vf[2];
     own_columns<T, DV>(V, lv, c0, vf);
     step_state<T, DK, DV, Pieces<T>::STATE>(K, lk, vf, *d, lane, st);
+    decays(i + 1);
     lds_barrier();
+  };
+  constexpr std::integral_constant<int, 0> even;
+  constexpr std::integral_constant<int, 1> odd;
+  g.load(start_of(0), size_of(0), lane);
+  load(even, 0);
+  load(odd, 1);
+  enter();
+  decays(0);
+  for (int i = 0; i < chunks; i += 2) {
+    chunk(even, i);
+    if (i + 1 < chunks) chunk(odd, i + 1);
   }
 }
 
 template <typename T, int DK, int DV>
-constexpr int kStatesTiles = kTileBytes<T, DK> + kTileBytes<T, DV> + (int)sizeof(Decays<T>);
+constexpr int kStatesTiles = kTileBytes<T, DK> + kTileBytes<T, DV> + 2 * (int)sizeof(Decays<T>);
 // callers' states go through the same memory
 template <typename T, int DK, int DV>
 constexpr int kStatesLds = kStatesTiles<T, DK, DV> > State<DK, DV>::kLds ? kStatesTiles<T, DK, DV> : State<DK, DV>::kLds;
@@ -649,19 +668,23 @@ linear_states(const LinearArgs a, const T* __restrict__ dout, const float* __res
     if (h == 0 && threadIdx.x == 0)
       kinds[w.slot] = (!on ? kNothing : own ? kStarted : kPassed) | (entered ? kEntered : 0);
     if (!on) return;
-    st.template load_caller<TR>(own && a.h0 ? a.h0 + ((int64_t)n * a.H + h) * floats : nullptr, TR ? a.dv : a.dk,
-                                TR ? a.dk : a.dv, (float*)smem, lane, wave);
+    auto enter = [&] {
+      st.template load_caller<TR>(own && a.h0 ? a.h0 + ((int64_t)n * a.H + h) * floats : nullptr, TR ? a.dv : a.dk,
+                                  TR ? a.dk : a.dv, (float*)smem, lane, wave);
+    };
     const View k{(const T*)a.k + hq * a.dk, a.ld_k, a.dk}, v{(const T*)a.v + h * a.dv, a.ld_v, a.dv};
-    states_range<T, DK, DV, false>(a, TR ? v : k, TR ? k : v, h, own ? start : w.lo, w.hi, smem, st, &total);
+    states_range<T, DK, DV, false>(a, TR ? v : k, TR ? k : v, h, own ? start : w.lo, w.hi, smem, st, &total, enter);
     st.store(ends + at, lane, wave);
     if (!own && threadIdx.x == 0) sums[(int64_t)w.slot * a.H + h] = total;
   } else if constexpr (TR) {
     if (!entered) return;
     const bool ends_here = before <= w.hi;
-    st.template load_caller<TR>(ends_here && dht ? dht + ((int64_t)(first - 1) * a.H + h) * floats : nullptr, a.dv, a.dk,
-                                (float*)smem, lane, wave);
+    auto enter = [&] {
+      st.template load_caller<TR>(ends_here && dht ? dht + ((int64_t)(first - 1) * a.H + h) * floats : nullptr, a.dv,
+                                  a.dk, (float*)smem, lane, wave);
+    };
     const View q{(const T*)a.q + hq * a.dk, a.ld_q, a.dk}, d{dout + h * a.dv, (int64_t)a.H * a.dv, a.dv};
-    states_range<T, DK, DV, true>(a, d, q, h, w.lo, ends_here ? before : w.hi, smem, st, nullptr);
+    states_range<T, DK, DV, true>(a, d, q, h, w.lo, ends_here ? before : w.hi, smem, st, nullptr, enter);
     st.store(adj + at, lane, wave);
   }
 }
@@ -669,20 +692,21 @@ linear_states(const LinearArgs a, const T* __restrict__ dout, const float* __res
 // True states at the slots' ends out of what each slot made of a zero state,
 // in place: S_i <- S_i + decay_i S_{i-1} where a sequence passes through slot
 // i; likewise (blockIdx.y = 1) the gradients from the last slot to the first.
-// A lane takes one element; loads go ahead of the chain in batches.
+// A lane takes four elements; loads go ahead of the chain in batches.
 __global__ void __launch_bounds__(256)
-linear_chain(int H, int64_t floats, int n_slots, float* __restrict__ ends, float* __restrict__ adj,
+linear_chain(int H, int64_t quads, int n_slots, float* __restrict__ ends, float* __restrict__ adj,
              const double* __restrict__ sums, const int* __restrict__ kinds) {
   constexpr int BATCH = 8;
   const bool back = blockIdx.y != 0;
-  const int64_t per = floats / 256;
+  const int64_t per = quads / 256;
   const int h = (int)(blockIdx.x / per);
   const int64_t el = (blockIdx.x % per) * 256 + threadIdx.x;
-  float* __restrict__ v = (back ? adj : ends) + h * floats + el;
-  const int64_t step = (int64_t)H * floats;
-  float s = 0.f;
+  f32x4* __restrict__ v = (f32x4*)(back ? adj : ends) + h * quads + el;
+  const int64_t step = (int64_t)H * quads;
+  f32x4 s = {0.f, 0.f, 0.f, 0.f};
   for (int i0 = 0; i0 < n_slots; i0 += BATCH) {
-    float made[BATCH], by[BATCH];
+    f32x4 made[BATCH];
+    float by[BATCH];
     int kd[BATCH];
 #pragma unroll
     for (int j = 0; j < BATCH; ++j) {
@@ -695,9 +719,10 @@ linear_chain(int H, int64_t floats, int n_slots, float* __restrict__ ends, float
     for (int j = 0; j < BATCH; ++j) {
       if (i0 + j >= n_slots) break;
       const int slot = back ? n_slots - 1 - i0 - j : i0 + j;
-      const bool holds = back ? kd[j] & kEntered : kd[j] & (kStarted | kPassed);
-      s = (kd[j] & kPassed ? by[j] * s : 0.f) + (holds ? made[j] : 0.f);
-      if (kd[j] & kPassed) v[slot * step] = s;
+      const bool holds = back ? kd[j] & kEntered : kd[j] & (kStarted | kPassed), passed = kd[j] & kPassed;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[e] = (passed ? by[j] * s[e] : 0.f) + (holds ? made[j][e] : 0.f);
+      if (passed) v[slot * step] = s;
     }
   }
 }
@@ -1276,8 +1301,8 @@ int states(const LinearArgs& a, const LinearPlan& p, const void* dout, const flo
   const hipError_t e = launch_kernel(linear_states<T, ROWS, COLS, BACK>, dim3((unsigned)linear_groups(p, a.H), sides),
                                      dim3(kThreads<COLS>), st, a, (const T*)dout, dht, ends, adj, sums, kinds);
   if (e != hipSuccess) return (int)e;
-  const int64_t floats = DK * DV;
-  return (int)launch_kernel(linear_chain, dim3((unsigned)(a.H * floats / 256), sides), dim3(256), st, a.H, floats,
+  const int64_t quads = DK * DV / 4;
+  return (int)launch_kernel(linear_chain, dim3((unsigned)(a.H * quads / 256), sides), dim3(256), st, a.H, quads,
                             (int)p.n_slots, ends, adj, sums, kinds);
 }
 
