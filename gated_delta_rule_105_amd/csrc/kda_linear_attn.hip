@@ -403,10 +403,10 @@ template <typename T> struct Decays {
 // workspace hold whole tiles, padding included, in the order of the lanes:
 // tile (row tile, column tile) is 256 floats, a lane's four side by side.  A
 // role whose state is the transposed one (TR) reads them across.  The
-// caller's states are [d_k][d_v] and go through LDS, 64 columns at a time.
+// caller's states are [d_k][d_v].
 template <int DK, int DV>
 struct State {
-  static constexpr int M = DK / 16, THREADS = kThreads<DV>;
+  static constexpr int M = DK / 16;
   f32x4 s[M];
   __device__ __forceinline__ void zero() {
 #pragma unroll
@@ -448,82 +448,47 @@ struct State {
     return sum;
   }
 
-  // a caller's state, rows by cols of it (TR: held cols by rows)
-  static constexpr int kLds = DK * 64 * 4;  // bytes
-  static constexpr int kEach = DK * 64 / THREADS, kAhead = kEach < 16 ? kEach : 16;
-  // element j of a thread among columns 64 t .. 64 t + 63: its place in memory (kNowhere: not there) and in LDS
-  template <bool TR>
-  __device__ __forceinline__ static void place(int thread, int j, int t, int rows, int cols, uint32_t* off, int* at) {
-    const int x = thread + j * THREADS, c = TR ? x / DK : x % 64, row = TR ? x % DK : x / 64, col = 64 * t + c;
-    *off = row < rows && col < cols ? (uint32_t)((TR ? col * rows + row : row * cols + col) * 4) : kNowhere;
-    *at = ((c / 16 * M + row / 16) * 64 + row % 16 / 4 * 16 + c % 16) * 4 + row % 4;
+  // A caller's state, rows by cols of it (TR: held cols by rows).  Straight to
+  // the lanes: through LDS, where every load and store would be of whole
+  // lines, a workgroup with a state to read started 5 us later.
+  // f(tile, its place r: offset of the lane, offset of the wave)
+  template <bool TR, typename F>
+  __device__ __forceinline__ static void places(int rows, int cols, int lane, int wave, F&& f) {
+    const int g = lane >> 4, col = 16 * wave + (lane & 15);
+    const uint32_t off = col < cols ? (uint32_t)(TR ? col * rows + 4 * g : 4 * g * cols + col) * 4 : kNowhere;
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        // not transposed, rows past the last are past the end
+        if (TR) f(m, r, (16 * m + 4 * g + r < rows ? off : kNowhere) + (16 * m + r) * 4, 0);
+        else f(m, r, off, (16 * m + r) * cols * 4);
+      }
   }
   template <bool TR, typename F>
-  __device__ __forceinline__ void with_caller(const float* p, int rows, int cols, float* lds, int lane, int wave,
-                                              F&& f) const {
+  __device__ __forceinline__ static void with_caller(const float* p, int rows, int cols, int lane, int wave, F&& f) {
     const __amdgpu_buffer_rsrc_t mem = rsrc(p, (uint32_t)(rows * cols * 4));
-#pragma unroll
-    for (int t = 0; t < DV / 64; ++t) {
-      const int x = here((int)threadIdx.x);
-      lds_barrier();
-#pragma unroll 1
-      for (int j0 = 0; j0 < kEach; j0 += kAhead) {
-        float y[kAhead];
-        uint32_t off;
-        int at;
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-          place<TR>(x, j0 + j, t, rows, cols, &off, &at);
-          y[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(mem, off, 0, 0));
-        }
-        const int again = here(x);
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-          place<TR>(again, j0 + j, t, rows, cols, &off, &at);
-          lds[at] = y[j];
-        }
-      }
-      lds_barrier();
-      if (wave / 4 == t)
-#pragma unroll
-        for (int m = 0; m < M; ++m) f(m, *(const f32x4*)(lds + ((wave % 4 * M + m) * 64 + lane) * 4));
-    }
-    lds_barrier();
-  }
-  template <bool TR>
-  __device__ __forceinline__ void load_caller(const float* p, int rows, int cols, float* lds, int lane, int wave) {
-    if (!p) return zero();
-    with_caller<TR>(p, rows, cols, lds, lane, wave, [&](int m, const f32x4& x) { s[m] = x; });
-  }
-  template <bool TR>
-  __device__ __forceinline__ float dot_caller(const float* p, int rows, int cols, float* lds, int lane, int wave) const {
-    float sum = 0.f;
-    with_caller<TR>(p, rows, cols, lds, lane, wave, [&](int m, const f32x4& x) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r) sum += s[m][r] * x[r];
+    places<TR>(rows, cols, here(lane), wave, [&](int m, int r, uint32_t off, int at) {
+      f(m, r, __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(mem, off, at, 0)));
     });
+  }
+  template <bool TR>
+  __device__ __forceinline__ void load_caller(const float* p, int rows, int cols, int lane, int wave) {
+    if (!p) return zero();
+    with_caller<TR>(p, rows, cols, lane, wave, [&](int m, int r, float x) { s[m][r] = x; });
+  }
+  template <bool TR>
+  __device__ __forceinline__ float dot_caller(const float* p, int rows, int cols, int lane, int wave) const {
+    float sum = 0.f;
+    with_caller<TR>(p, rows, cols, lane, wave, [&](int m, int r, float x) { sum += s[m][r] * x; });
     return sum;
   }
   template <bool TR>
-  __device__ __forceinline__ void store_caller(float* p, int rows, int cols, float* lds, int lane, int wave) const {
+  __device__ __forceinline__ void store_caller(float* p, int rows, int cols, int lane, int wave) const {
     const __amdgpu_buffer_rsrc_t mem = rsrc(p, (uint32_t)(rows * cols * 4));
-#pragma unroll
-    for (int t = 0; t < DV / 64; ++t) {
-      const int x = here((int)threadIdx.x);
-      lds_barrier();
-      if (wave / 4 == t)
-#pragma unroll
-        for (int m = 0; m < M; ++m) *(f32x4*)(lds + ((wave % 4 * M + m) * 64 + lane) * 4) = s[m];
-      lds_barrier();
-#pragma unroll 8
-      for (int j = 0; j < kEach; ++j) {
-        uint32_t off;
-        int at;
-        place<TR>(x, j, t, rows, cols, &off, &at);
-        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(lds[at]), mem, off, 0, 0);
-      }
-    }
-    lds_barrier();
+    places<TR>(rows, cols, here(lane), wave, [&](int m, int r, uint32_t off, int at) {
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(s[m][r]), mem, off, at, 0);
+    });
   }
 };
 
@@ -641,11 +606,7 @@ __device__ __forceinline__ void states_range(const LinearArgs& a, const View& k,
 }
 
 template <typename T, int DK, int DV>
-constexpr int kStatesTiles = kTileBytes<T, DK> + kTileBytes<T, DV> + 2 * (int)sizeof(Decays<T>);
-// callers' states go through the same memory
-template <typename T, int DK, int DV>
-constexpr int kStatesLds = kStatesTiles<T, DK, DV> > State<DK, DV>::kLds ? kStatesTiles<T, DK, DV> : State<DK, DV>::kLds;
-
+constexpr int kStatesLds = kTileBytes<T, DK> + kTileBytes<T, DV> + 2 * (int)sizeof(Decays<T>);
 template <typename T, int DK, int DV, bool TR>
 __global__ void __launch_bounds__(kThreads<DV>, 2 * kThreads<DV> / 256)
 linear_states(const LinearArgs a, const T* __restrict__ dout, const float* __restrict__ dht, float* __restrict__ ends,
@@ -670,7 +631,7 @@ linear_states(const LinearArgs a, const T* __restrict__ dout, const float* __res
     if (!on) return;
     auto enter = [&] {
       st.template load_caller<TR>(own && a.h0 ? a.h0 + ((int64_t)n * a.H + h) * floats : nullptr, TR ? a.dv : a.dk,
-                                  TR ? a.dk : a.dv, (float*)smem, lane, wave);
+                                  TR ? a.dk : a.dv, lane, wave);
     };
     const View k{(const T*)a.k + hq * a.dk, a.ld_k, a.dk}, v{(const T*)a.v + h * a.dv, a.ld_v, a.dv};
     states_range<T, DK, DV, false>(a, TR ? v : k, TR ? k : v, h, own ? start : w.lo, w.hi, smem, st, &total, enter);
@@ -681,7 +642,7 @@ linear_states(const LinearArgs a, const T* __restrict__ dout, const float* __res
     const bool ends_here = before <= w.hi;
     auto enter = [&] {
       st.template load_caller<TR>(ends_here && dht ? dht + ((int64_t)(first - 1) * a.H + h) * floats : nullptr, a.dv,
-                                  a.dk, (float*)smem, lane, wave);
+                                  a.dk, lane, wave);
     };
     const View q{(const T*)a.q + hq * a.dk, a.ld_q, a.dk}, d{dout + h * a.dv, (int64_t)a.H * a.dv, a.dv};
     states_range<T, DK, DV, true>(a, d, q, h, w.lo, ends_here ? before : w.hi, smem, st, nullptr, enter);
@@ -1012,9 +973,6 @@ __device__ __forceinline__ void sweep_slot(const LinearArgs& a, const Sweep& w, 
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int64_t floats = (int64_t)a.dk * a.dv, record = DK * DV;
   const int rows = w.q.d, cols = w.v.d;
-  // callers' states go through the inputs' LDS, in front of P
-  static_assert(State<DK, DV>::kLds <= sizeof(m.q) + sizeof(m.k) + sizeof(m.v), "");
-  float* lds = (float*)&m;
   State<DK, DV> st;
   // all of P beside the tiles that are written stays zero
   for (int x = threadIdx.x; x < (int)(sizeof(m.p) / 16); x += kThreads<DV>) ((uint4*)m.p)[x] = make_uint4(0, 0, 0, 0);
@@ -1043,7 +1001,7 @@ __device__ __forceinline__ void sweep_slot(const LinearArgs& a, const Sweep& w, 
     auto enter_state = [&] {
       // records: the state's own orientation forward, the transposed one backward
       if (BACK ? !done : entered) st.template load<R == kDv>(of_slot(BACK ? s.slot + 1 : s.slot - 1), lane, wave);
-      else st.template load_caller<TR>(of_seq(seq_state, n), rows, cols, lds, lane, wave);
+      else st.template load_caller<TR>(of_seq(seq_state, n), rows, cols, lane, wave);
     };
     const bool out = leave && (BACK ? !entered : done);
     if (start < stop) sweep_range<T, DK, DV, R>(a, w, h, start, stop, m, st, enter_state);
@@ -1051,10 +1009,10 @@ __device__ __forceinline__ void sweep_slot(const LinearArgs& a, const Sweep& w, 
     if (R == kDq && w.dots) {
       float x = 0.f;
       if (!done) x = st.dot(adj + ((int64_t)(s.slot + 1) * a.H + h) * record, lane, wave);
-      else if (dht) x = st.template dot_caller<TR>(of_seq(dht, n), rows, cols, lds, lane, wave);
+      else if (dht) x = st.template dot_caller<TR>(of_seq(dht, n), rows, cols, lane, wave);
       inner(x, (done ? seq_dot + (int64_t)n * a.H : slot_dot + (int64_t)s.slot * a.H) + h);
     }
-    if (out) st.template store_caller<TR>(leave + ((int64_t)n * a.H + h) * floats, rows, cols, lds, lane, wave);
+    if (out) st.template store_caller<TR>(leave + ((int64_t)n * a.H + h) * floats, rows, cols, lane, wave);
   };
   // the sequence that entered, then those that start here; the last slot also has the empty ones behind the last token
   int n = uniform(seqs.from(s.lo)), at = s.lo;
