@@ -665,26 +665,38 @@ linear_chain(int H, int64_t quads, int n_slots, float* __restrict__ ends, float*
   f32x4* __restrict__ v = (f32x4*)(back ? adj : ends) + h * quads + el;
   const int64_t step = (int64_t)H * quads;
   f32x4 s = {0.f, 0.f, 0.f, 0.f};
-  for (int i0 = 0; i0 < n_slots; i0 += BATCH) {
+  struct Batch {
     f32x4 made[BATCH];
-    float by[BATCH];
+    double by[BATCH];
     int kd[BATCH];
+  } x, y;
+  auto load = [&](Batch& b, int i0) {
 #pragma unroll
     for (int j = 0; j < BATCH; ++j) {
       const int i = i0 + j < n_slots ? i0 + j : n_slots - 1, slot = back ? n_slots - 1 - i : i;
-      kd[j] = kinds[slot];
-      made[j] = v[slot * step];
-      by[j] = decay_of(sums[(int64_t)slot * H + h]);
+      b.kd[j] = kinds[slot];
+      b.made[j] = v[slot * step];
+      b.by[j] = sums[(int64_t)slot * H + h];
     }
+  };
+  auto pass = [&](const Batch& b, int i0) {
 #pragma unroll
     for (int j = 0; j < BATCH; ++j) {
       if (i0 + j >= n_slots) break;
       const int slot = back ? n_slots - 1 - i0 - j : i0 + j;
-      const bool holds = back ? kd[j] & kEntered : kd[j] & (kStarted | kPassed), passed = kd[j] & kPassed;
+      const bool holds = back ? b.kd[j] & kEntered : b.kd[j] & (kStarted | kPassed), passed = b.kd[j] & kPassed;
+      const float by = decay_of(b.by[j]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[e] = (passed ? by[j] * s[e] : 0.f) + (holds ? made[j][e] : 0.f);
+      for (int e = 0; e < 4; ++e) s[e] = (passed ? by * s[e] : 0.f) + (holds ? b.made[j][e] : 0.f);
       if (passed) v[slot * step] = s;
     }
+  };
+  load(x, 0);
+  for (int i0 = 0; i0 < n_slots; i0 += 2 * BATCH) {
+    load(y, i0 + BATCH);
+    pass(x, i0);
+    load(x, i0 + 2 * BATCH);
+    pass(y, i0 + BATCH);
   }
 }
 
