@@ -212,6 +212,29 @@ template <typename T, int W, int THREADS> struct Stage {
         for (int e = 0; e < x.d; ++e)
           X[k * kLd<W> + (((e >> 2) ^ ((k >> 2) & 3)) << 2) + (e & 3)] = ((const T*)x.p)[(int64_t)(tok + k) * x.ld + e];
   }
+  // Back to memory, from the places that store() gives a lane, so that it may
+  // write them anew without a barrier.  Whole vectors only.
+  __device__ __forceinline__ static void write(const T* X, const View& y, int tok, int n) {
+    const int thread = here((int)threadIdx.x), c = thread % VPR * VE, r = thread / VPR, step = (int)y.ld * (int)sizeof(T);
+    const __amdgpu_buffer_rsrc_t rows = rows_of<T>(y, tok, n);
+    const uint32_t off = c < y.d ? (uint32_t)(r * step + c * (int)sizeof(T)) : kNowhere;
+    const int swizzle = (r >> 2) & 3, other = swizzle & 1 ? -4 : 4;
+    const T* const row = X + r * kLd<W>;
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    u32x4 x[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const T* at = row + (((c >> 2) ^ swizzle ^ ((i * RPP >> 2) & 3)) << 2) + i * RPP * kLd<W>;
+      if constexpr (sizeof(T) == 2) {
+        const uint2 a = *(const uint2*)at, b = *(const uint2*)(at + other);
+        x[i] = (u32x4){a.x, a.y, b.x, b.y};
+      } else {
+        x[i] = *(const u32x4*)at;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) __builtin_amdgcn_raw_buffer_store_b128(x[i], rows, off + (uint32_t)(i * RPP * step), 0, 0);
+  }
   // Whether some row may hold an infinity or a NaN: the largest magnitude of
   // all that was read, so that zeros for what is not there need no care.
   __device__ __forceinline__ bool wild(const View& x) const {
@@ -325,6 +348,13 @@ __device__ __forceinline__ void store4(const Lanes4& l, int r0, int c1, const f3
         else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x[e]), l.rows, l.off + (c1 + e) * E, row, 0);
       }
   }
+}
+
+// four elements in LDS
+__device__ __forceinline__ void put4(float* at, const f32x4& x) { *(f32x4*)at = x; }
+__device__ __forceinline__ void put4(bf16_t* at, const f32x4& x) {
+  *(uint2*)at = make_uint2(__builtin_bit_cast(uint32_t, f32x2_to_bf16x2(x[0], x[1])),
+                           __builtin_bit_cast(uint32_t, f32x2_to_bf16x2(x[2], x[3])));
 }
 
 // ---- decays ------------------------------------------------------------------------
@@ -934,21 +964,32 @@ __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w,
           if (BACK ? KB * (kb + 1) <= 16 * rt : KB * kb > 16 * rt) continue;  // zeros of P
           acc[rt] = mma(vf[kb], row_frag<C>(m.p[c], lp, 16 * rt, KB * kb), acc[rt]);
         }
+    // The outputs go to memory in whole vectors, by way of this wave's own
+    // columns of V, which nothing else reads any more; or as they are.
+    const View y{w.out, (int64_t)a.H * w.v.d, w.v.d};
+    const bool by_rows = !((R == kDq || R == kDk) && w.wide) && y.d % (16 / (int)sizeof(T)) == 0;
     auto out = [&](auto type, auto quads) {
       typedef decltype(type) E;
-      const View y{w.out, (int64_t)a.H * w.v.d, w.v.d};
       const Lanes4 to(rows_of<E>(y, t, n), y.ld, sizeof(E), y.d, i16, c0 + 4 * g);
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) store4<E, quads.value>(to, 16 * rt, 0, acc[rt]);
     };
     auto out_as = [&](auto type) {
-      if (w.v.d % 4 == 0) out(type, std::true_type{});
+      if (y.d % 4 == 0) out(type, std::true_type{});
       else out(type, std::false_type{});
     };
-    if ((R == kDq || R == kDk) && w.wide) out_as(float{});
-    else out_as(T{});
+    if (by_rows) {
+      const Lane<T, DV> lv(ln);
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) put4(m.v + lv.row + 16 * rt * kLd<DV> + c0, acc[rt]);
+    } else if ((R == kDq || R == kDk) && w.wide) {
+      out_as(float{});
+    } else {
+      out_as(T{});
+    }
     step_state<T, DK, DV, KEPT ? Pieces<T>::STATE : OUT>(m.k, Lane<T, DK>(here(lane)), vf, d, lane, st);
     lds_barrier();
+    if (by_rows) Stage<T, DV, THREADS>::write(m.v, y, t, n);
     if ((R == kDq || R == kDk) && w.dots && (int)threadIdx.x < n) {
       const int row = threadIdx.x;
       float s = 0.f;
