@@ -17,13 +17,13 @@
 // the form going back in time with (k, q, dout) and (v, dout, q):
 //   dV = P^T dO + e^{G_C - G} K dS,   dS <- e^{G_C} dS + scale (e^G Q)^T dO,
 // dS the gradient of the state after the chunk.  A decay stands in every
-// product of a query at its token or later with a key before it, so with M =
-// (Q K^T) o D o scale (dO V^T) below the diagonal
-//   dg_t = sum_{i >= t > j} M_ij + sum_{s >= t} x_s + sum_{s < t} y_s + e^{G_C} <S, dS>,
-// x_s = q_s . (the state's part of dq_s), y_s = k_s . (dS's part of dk_s),
-// and because <S_end, dS> = e^{G_C} <S, dS> + sum y, all of it is the suffix
-// sum of (row sum of M - column sum of M + x - y) plus <S_end, dS> of the end
-// of the sequence or slot.
+// product of a query at its token or later with a key before it.  With P below
+// the diagonal only, x_s = q_s . (dq_s without its own token's key) and y_s =
+// k_s . (dk_s without its own token's query), the products between tokens
+// before t or tokens from t on stand in both, and
+//   dg_t = sum_{s >= t} (x_s - y_s) + <S_end, dS>
+// of the end of the sequence or slot.  A token's product with itself, which
+// has no decay, would be the largest of either sum and is left out of both.
 #include "kda_layer_device.h"
 #include "kda_linear.h"
 #include "kda_rows.h"
@@ -98,6 +98,19 @@ __device__ __forceinline__ f32x4 col_frag(const float* X, const Lane<float, W>& 
 // the same, but the wait states behind matrix instructions are counted by
 // what the compiler knows of the instructions between.
 __device__ __forceinline__ int here(int x) { return __builtin_amdgcn_update_dpp(x, x, 0xe4, 0xf, 0xf, false); }
+
+// The sum of neighbouring groups of N lanes: of x in the even ones, of y in the odd ones.
+template <int N>
+__device__ __forceinline__ float swap_sum(float x, float y) {
+  const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
+  if constexpr (N == 16) {
+    const auto p = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    return __uint_as_float(p[0]) + __uint_as_float(p[1]);
+  } else {
+    const auto p = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    return __uint_as_float(p[0]) + __uint_as_float(p[1]);
+  }
+}
 
 // Nothing is moved across: operands' loads stay together ahead of their first use.
 __device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
@@ -355,6 +368,13 @@ __device__ __forceinline__ void put4(float* at, const f32x4& x) { *(f32x4*)at = 
 __device__ __forceinline__ void put4(bf16_t* at, const f32x4& x) {
   *(uint2*)at = make_uint2(__builtin_bit_cast(uint32_t, f32x2_to_bf16x2(x[0], x[1])),
                            __builtin_bit_cast(uint32_t, f32x2_to_bf16x2(x[2], x[3])));
+}
+
+__device__ __forceinline__ f32x4 get4(const float* at) { return *(const f32x4*)at; }
+__device__ __forceinline__ f32x4 get4(const bf16_t* at) {
+  const uint2 w = *(const uint2*)at;
+  return (f32x4){__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                 __uint_as_float(w.y & 0xffff0000u)};
 }
 
 // ---- decays ------------------------------------------------------------------------
@@ -751,7 +771,7 @@ struct SweepLds {
   Decays<T> d[2];  // of this chunk and the next
   int wild;
   float dot[kWaves<DV>][kTokens<T>];
-  float sums[10][2][16];  // row and column sums of M's tiles
+  float diagonal[kTokens<T>];  // of P, where it is kept apart
 };
 
 // the tiles on and beside the diagonal, in the order that waves take them
@@ -767,12 +787,15 @@ template <typename T, int DK, int DV, Role R, typename F>
 __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w, int h, int t0, int end,
                                             SweepLds<T, DK, DV>& m, State<DK, DV>& st, F&& enter) {
   // the state of these two roles is handed out at a sequence's end
-  constexpr bool BACK = R == kDk || R == kDv, M_SUMS = R == kDq, KEPT = R == kForward || R == kDv;
+  constexpr bool BACK = R == kDk || R == kDv, KEPT = R == kForward || R == kDv;
   constexpr int C = kTokens<T>, KB = Elem<T>::KB, RT = C / 16, TILES = RT * (RT + 1) / 2;
   constexpr int OUT = Pieces<T>::OUT, WAVES = kWaves<DV>, THREADS = kThreads<DV>;
   typedef typename Frag<T>::type frag;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), c0 = wave * 16;
   const int chunks = (end - t0 + C - 1) / C;
+  // For the decays' gradients a token's own product is added to the output
+  // behind the inner product that they take, which is to hold other tokens' only.
+  const bool strict = (R == kDq || R == kDk) && w.dots;
   Stage<T, DK, THREADS> sq, sk;
   Stage<T, DV, THREADS> sv;
   LogDecays<T> gd(a, h);
@@ -860,35 +883,12 @@ __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w,
         const float x = acc[r] * (decay_of(BACK ? gj - gi : gi - gj) * w.p_scale);
         p[r] = (BACK ? at <= r : at >= r) ? x : 0.f;
       }
-      if (M_SUMS && w.dots) {
-        // M = (Q K^T) o P, this role's V being the keys
-        const Lanes4 other(rows_of<T>(w.other, t, n), w.other.ld, sizeof(T), w.other.d, i16, 4 * g);
-        f32x4 s = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int kb = 0; kb < DV / KB; ++kb) {
-          frag qf;
-          Four<T> x, y;
-          x.load(other, 16 * rt, KB * kb);
-          if constexpr (sizeof(T) == 2) {
-            y.load(other, 16 * rt, KB * kb + 16);
-            qf = __builtin_bit_cast(frag, make_uint4(x.w[0], x.w[1], y.w[0], y.w[1]));
-          } else {
-            qf = x.get();
-          }
-          s = mma(row_frag<DV>(m.v, Lane<T, DV>(ln), 16 * ct, KB * kb), qf, s);
-        }
-        float across = 0.f;
+      if (strict && rt == ct) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float x = s[r] * p[r];
-          s[r] = at > r ? x : 0.f;
-          across += s[r];
-          s[r] = row_sum(s[r]);
+          if (at == r) m.diagonal[16 * rt + i16] = p[r];
+          p[r] = at == r ? 0.f : p[r];
         }
-        across += __shfl_xor(across, 16, 64);
-        across += __shfl_xor(across, 32, 64);
-        if (g == 0) m.sums[tile][0][i16] = across;
-        if (i16 == 0) *(f32x4*)&m.sums[tile][1][4 * g] = s;
       }
       f32x4 x = p;
 #pragma unroll
@@ -911,6 +911,13 @@ __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w,
     // the state's part of the outputs, transposed: rows are channels of V, columns tokens
     const int ln = here(lane), g = ln >> 4, i16 = ln & 15;
     const Lane<T, DK> lk(ln);
+    // the rows that outputs are multiplied with arrive under the products
+    Four<T> other[RT];
+    if (strict) {
+      const Lanes4 rows(rows_of<T>(w.other, t, n), w.other.ld, sizeof(T), w.other.d, i16, c0 + 4 * g);
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) other[rt].load(rows, 16 * rt, 0);
+    }
     f32x4 acc[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) acc[rt] = (f32x4){0.f, 0.f, 0.f, 0.f};
@@ -931,22 +938,6 @@ __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w,
     }
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) acc[rt] *= d.row[16 * rt + i16];
-    if ((R == kDq || R == kDk) && w.dots) {
-      const Lanes4 other(rows_of<T>(w.other, t, n), w.other.ld, sizeof(T), w.other.d, i16, c0 + 4 * g);
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        const int row = 16 * rt + i16;
-        float s = 0.f;
-        Four<T> y;
-        y.load(other, 16 * rt, 0);
-        const f32x4 z = y.get();
-#pragma unroll
-        for (int r = 0; r < 4; ++r) s += acc[rt][r] * z[r];
-        s += __shfl_xor(s, 16, 64);
-        s += __shfl_xor(s, 32, 64);
-        if (g == 0) m.dot[wave][row] = s;
-      }
-    }
     // the next chunk's loads have the products below to arrive in (ahead of those above they would cost registers)
     load(t_next, n_next);
     decays(buf ^ 1, n_next);
@@ -955,15 +946,35 @@ __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w,
     const Lane<T, C> lp(ln);
     frag vf[2];
     own_columns<T, DV>(m.v, Lane<T, DV>(ln), c0, vf);
+    if (!strict || n > 1)  // the one token may hold an infinity, which a zero is not multiplied with
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
+      for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-      for (int c = OUT - 1; c >= 0; --c)
+        for (int c = OUT - 1; c >= 0; --c)
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          if (BACK ? KB * (kb + 1) <= 16 * rt : KB * kb > 16 * rt) continue;  // zeros of P
-          acc[rt] = mma(vf[kb], row_frag<C>(m.p[c], lp, 16 * rt, KB * kb), acc[rt]);
+          for (int rt = 0; rt < RT; ++rt) {
+            if (BACK ? KB * (kb + 1) <= 16 * rt : KB * kb > 16 * rt) continue;  // zeros of P
+            acc[rt] = mma(vf[kb], row_frag<C>(m.p[c], lp, 16 * rt, KB * kb), acc[rt]);
+          }
+    if (strict) {
+      float s[RT];
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        const f32x4 z = other[rt].get(), v = get4(m.v + Lane<T, DV>(ln).row + 16 * rt * kLd<DV> + c0);
+        const float own = m.diagonal[16 * rt + i16];
+        s[rt] = 0.f;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          s[rt] += acc[rt][r] * z[r];
+          acc[rt][r] += own * v[r];
         }
+      }
+      // over the four rows of lanes; row g is left with the sum of tokens 16 g + i
+      float all = swap_sum<16>(s[0], s[1]);
+      if constexpr (RT == 4) all = swap_sum<32>(all, swap_sum<16>(s[2], s[3]));
+      else all = swap_sum<32>(all, all);
+      if (lane < C) m.dot[wave][lane] = all;
+    }
     // The outputs go to memory in whole vectors, by way of this wave's own
     // columns of V, which nothing else reads any more; or as they are.
     const View y{w.out, (int64_t)a.H * w.v.d, w.v.d};
@@ -990,16 +1001,11 @@ __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w,
     step_state<T, DK, DV, KEPT ? Pieces<T>::STATE : OUT>(m.k, Lane<T, DK>(here(lane)), vf, d, lane, st);
     lds_barrier();
     if (by_rows) Stage<T, DV, THREADS>::write(m.v, y, t, n);
-    if ((R == kDq || R == kDk) && w.dots && (int)threadIdx.x < n) {
+    if (strict && (int)threadIdx.x < n) {
       const int row = threadIdx.x;
       float s = 0.f;
 #pragma unroll
       for (int x = 0; x < WAVES; ++x) s += m.dot[x][row];
-      if (M_SUMS) {
-        const int mt = row / 16;
-        for (int b = 0; b <= mt; ++b) s += m.sums[mt * (mt + 1) / 2 + b][0][row % 16];
-        for (int b = mt; b < RT; ++b) s -= m.sums[b * (b + 1) / 2 + mt][1][row % 16];
-      }
       w.dots[t + row] = s;
     }
     if (n_next == 0) break;
@@ -1013,7 +1019,7 @@ __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w,
     n = n_next;
     buf ^= 1;
   }
-  if (w.dots) lds_barrier();  // dot and sums are read
+  if (strict) lds_barrier();  // the dots are read
 }
 
 // One slot of one head.  dS: what a sequence's last state's inner product with its gradient is wanted of.
