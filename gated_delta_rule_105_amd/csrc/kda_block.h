@@ -51,19 +51,8 @@ constexpr int kBlockNormThreads = 256;
 // for every parameter.
 constexpr int kBlockNormParts = 512;
 
-// Forward: rows a lane takes one after the other, with their loads issued
-// together: four of one load each where 2048 workgroups are left, which fill
-// the device (10.9 against 11.2 us for 65536 heads of 128 channels, gated);
-// one of more (two of two loads took 22.7 us, one 21.7, for 4096 rows of 4096
-// channels).
-inline int block_norm_rows(int64_t rows, const RowShape& s) {
-  const int most = s.loads == 1 ? 4 : 1;
-  return most > 1 && ceil_div(rows, (int64_t)(kBlockNormThreads / s.lanes) * most) >= 2048 ? most : 1;
-}
 inline bool block_norm_fits(int64_t rows, int D, int elem) {
-  const RowShape s = block_norm_shape(D, elem);
-  const int64_t each = (int64_t)(kBlockNormThreads / s.lanes) * block_norm_rows(rows, s);
-  return rows <= INT32_MAX && grid_fits(ceil_div(rows, each), kBlockNormThreads);
+  return rows <= INT32_MAX && grid_fits(ceil_div(rows, kBlockNormThreads / block_norm_shape(D, elem).lanes), kBlockNormThreads);
 }
 inline int64_t block_norm_parts(int64_t rows, int D, int elem) {
   const int64_t n = ceil_div(rows, kBlockNormThreads / block_norm_shape(D, elem).lanes);

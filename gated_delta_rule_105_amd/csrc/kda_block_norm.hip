@@ -118,51 +118,44 @@ __device__ __forceinline__ int64_t row_at(int row, int H, int D, int64_t ld) {
   return tok * ld + (int64_t)(row - tok * H) * D;
 }
 
-// Forward.  A group of LANES lanes takes U rows.
-template <typename T, int V, int LANES, int N, int U, bool GATED>
+// Forward.  A group of LANES lanes takes a row (four, with their loads
+// together, took 82 us against 71 for 524288 heads of 128 channels in bf16).
+template <typename T, int V, int LANES, int N, bool GATED>
 __global__ void __launch_bounds__(kThreads)
 block_forward(const BlockNormArgs a, T* __restrict__ y, T* __restrict__ total) {
   constexpr int G = kThreads / LANES;
   __shared__ float lds[1][kWaves];
-  const int sub = threadIdx.x % LANES, group = threadIdx.x / LANES, last = (int)a.rows - 1;
-  int64_t first = (int64_t)blockIdx.x * G * U + group;
-  RawRow<T, V, N> rx[U], rz[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t at = first + u * G;
-    const int row = at < last ? (int)at : last;
-    rx[u].template load<LANES>((const T*)a.x + row_at(row, a.H, a.D, a.ld_x), sub, a.D);
-    rz[u].template load<LANES>((const T*)a.z + row_at(row, a.H, a.D, a.ld_z), sub, a.D);
-  }
+  const int sub = threadIdx.x % LANES, last = (int)a.rows - 1;
+  const int64_t at = (int64_t)blockIdx.x * G + threadIdx.x / LANES, flat = at * a.D;
+  const int row = at < last ? (int)at : last;
+  RawRow<T, V, N> rx, rz;
+  rx.template load<LANES>((const T*)a.x + row_at(row, a.H, a.D, a.ld_x), sub, a.D);
+  rz.template load<LANES>((const T*)a.z + row_at(row, a.H, a.D, a.ld_z), sub, a.D);
   const Row<V, N> w = param_row<LANES, V, N>(a.w, sub, a.D);
   const Row<V, N> c = param_row<LANES, V, N>(GATED ? nullptr : a.channels, sub, a.D);
+  Row<V, N> x = rx.template get<LANES>(sub, a.D);
+  const Row<V, N> z = rz.template get<LANES>(sub, a.D);
+  float ss[1] = {0.f};
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t row = first + u * G;
-    Row<V, N> x = rx[u].template get<LANES>(sub, a.D);
-    const Row<V, N> z = rz[u].template get<LANES>(sub, a.D);
-    float ss[1] = {0.f};
+  for (int i = 0; i < N; ++i)
 #pragma unroll
-    for (int i = 0; i < N; ++i)
+    for (int e = 0; e < V; ++e) {
+      if (!GATED) x.v[i][e] = z.v[i][e] + a.scale * c.v[i][e] * x.v[i][e];
+      ss[0] += x.v[i][e] * x.v[i][e];
+    }
+  row_sums<LANES>(ss, lds);
+  const float r = inv_norm(ss[0], a.D, a.eps);
+  Row<V, N> o;
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        if (!GATED) x.v[i][e] = z.v[i][e] + a.scale * c.v[i][e] * x.v[i][e];
-        ss[0] += x.v[i][e] * x.v[i][e];
-      }
-    row_sums<LANES>(ss, lds);
-    const float r = inv_norm(ss[0], a.D, a.eps);
-    Row<V, N> o;
+  for (int i = 0; i < N; ++i)
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float n = x.v[i][e] * r * w.v[i][e];
-        o.v[i][e] = GATED ? n * Gate(z.v[i][e], a.act).a : n;
-      }
-    if (row > last) continue;
-    store_row<T, LANES>(y + row * a.D, sub, a.D, o);
-    if (!GATED) store_row<T, LANES>(total + row * a.D, sub, a.D, x);
-  }
+    for (int e = 0; e < V; ++e) {
+      const float n = x.v[i][e] * r * w.v[i][e];
+      o.v[i][e] = GATED ? n * Gate(z.v[i][e], a.act).a : n;
+    }
+  if (at > last) return;
+  store_row<T, LANES>(y + flat, sub, a.D, o);
+  if (!GATED) store_row<T, LANES>(total + flat, sub, a.D, x);
 }
 
 // Backward.  Each group of lanes takes every (gridDim.x G)-th row and keeps
@@ -332,14 +325,9 @@ template <bool GATED>
 int forward(int is_bf16, const BlockNormArgs& a, void* y, void* total, hipStream_t st) {
   return dispatch(is_bf16, a.D, [&](auto t, auto s) {
     typedef decltype(t) T;
-    constexpr int MOST = s.N == 1 ? 4 : 1;
-    auto go = [&](auto u) {
-      const int64_t each = (int64_t)(kThreads / s.LANES) * u.value;
-      return (int)launch_kernel(block_forward<T, s.V, s.LANES, s.N, u.value, GATED>,
-                                dim3((unsigned)ceil_div(a.rows, each)), dim3(kThreads), st, a, (T*)y, (T*)total);
-    };
-    if (block_norm_rows(a.rows, RowShape{s.V, s.LANES, s.N}) == MOST) return go(std::integral_constant<int, MOST>{});
-    return go(std::integral_constant<int, 1>{});
+    return (int)launch_kernel(block_forward<T, s.V, s.LANES, s.N, GATED>,
+                              dim3((unsigned)ceil_div(a.rows, kThreads / s.LANES)), dim3(kThreads), st, a, (T*)y,
+                              (T*)total);
   });
 }
 
