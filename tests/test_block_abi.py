@@ -141,7 +141,9 @@ BAD_LINEAR = [(dict(B=0), INV), (dict(T=-1), INV), (dict(Hq=0), INV), (dict(H=0)
               (dict(n_seqs=-1), INV), (dict(n_seqs=3), INV), (dict(dtype=2), INV), (dict(decay=3), INV),
               (dict(decay=-1), INV), (dict(scale=float("nan")), INV), (dict(scale=float("inf")), INV),
               (dict(ld_q=127), INV), (dict(ld_k=-1), INV), (dict(ld_v=511), INV), (dict(ld_g=3), INV),
-              (dict(ld_v=2 ** 62), INV), (dict(B=65536, T=65536), UNS), (dict(B=2 ** 21, T=1, H=2048), UNS)]
+              (dict(ld_v=2 ** 62), INV), (dict(B=65536, T=65536), UNS), (dict(B=2 ** 21, T=1, H=2048), UNS),
+              (dict(ld_q=2 ** 22 + 1), UNS), (dict(ld_k=2 ** 22 + 1), UNS), (dict(ld_v=2 ** 22 + 1), UNS),
+              (dict(ld_g=2 ** 22 + 1), UNS), (dict(T=1, Hq=1, H=2 ** 16, d_v=128), UNS)]
 BAD_GATED = [(dict(n_tokens=-1), INV), (dict(H=0), INV), (dict(d=0), INV), (dict(d=8193), UNS), (dict(H=70000), UNS),
              (dict(dtype=2), INV), (dict(activation=KDA_ACT_NONE), INV), (dict(activation=3), INV),
              (dict(eps=-1.0), INV), (dict(eps=float("nan")), INV), (dict(eps=float("inf")), INV), (dict(ld_x=1023), INV),
