@@ -110,6 +110,11 @@ struct Gate {
     a = silu ? z * s : s;
     slope = silu ? s * (1.f + z * c) : s * c;
   }
+  // a(z) alone: below -88 the sigmoid is 0, within what fp32 holds as a normal number
+  __device__ __forceinline__ static float value(float z, int silu) {
+    const float s = __builtin_amdgcn_rcpf(1.f + exp2_fast(-kLog2e * z));
+    return silu ? z * s : s;
+  }
 };
 
 __device__ __forceinline__ int64_t row_at(int row, int H, int D, int64_t ld) {
@@ -151,7 +156,7 @@ block_forward(const BlockNormArgs a, T* __restrict__ y, T* __restrict__ total) {
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       const float n = x.v[i][e] * r * w.v[i][e];
-      o.v[i][e] = GATED ? n * Gate(z.v[i][e], a.act).a : n;
+      o.v[i][e] = GATED ? n * Gate::value(z.v[i][e], a.act) : n;
     }
   if (at > last) return;
   store_row<T, LANES>(y + flat, sub, a.D, o);
