@@ -64,7 +64,10 @@ inline LinearPlan plan_linear(int64_t tokens, int rows, int64_t T, bool packed, 
     // Two workgroups for every compute unit, unless their states, one for every
     // slot and head, then cost more than the second workgroup hides: at least
     // the tokens whose keys and values are half a state (256 with 128 channels
-    // of both).  Shorter slots only where not even one each would be left.
+    // of both; half of that took 61.5 us against 55.4 for 4096 tokens of 16
+    // heads, and their gradients 153 against 139).  Where that leaves more than
+    // one each, as for 16384 tokens, two take 147 us and one 163.  Shorter slots
+    // only where not even one each would be left.
     auto slots_of = [&](int64_t groups) {
       const int64_t n = groups / H < 1 ? 1 : groups / H;
       return ceil_div(ceil_div(tokens, n), kLinearChunk) * kLinearChunk;

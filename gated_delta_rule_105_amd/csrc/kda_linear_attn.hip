@@ -24,6 +24,18 @@
 //   dg_t = sum_{s >= t} (x_s - y_s) + <S_end, dS>
 // of the end of the sequence or slot.  A token's product with itself, which
 // has no decay, would be the largest of either sum and is left out of both.
+//
+// A prompt goes in three launches, so that a few rows fill the device: the
+// state that every slot of tokens hands on (linear_states), the true states
+// from those (linear_chain), the outputs (linear_forward); the gradients in
+// five at most.  Necessary bytes are few (a large copy would take 13.5 us for
+// 4096 tokens of 16 heads of 128 in bf16, the matrix products 4.4): what
+// bounds it is the length of a chunk's chain of phases, products of 16-row
+// tiles with waits for LDS between them.  That case takes 51 to 55 us (16 + 8.4
+// + 30.5 in the kernels); its two rows of 2048 tokens backward 120 us (25 + 11.4
+// + 83 + 5.6); 16384 tokens of 32 heads of 128 keys and 64 values that share one
+// query and key 150 us (47 + 9 + 110); 5003 tokens of 6 fp32 heads 95 us (20 +
+// 12 + 64).
 #include "kda_layer_device.h"
 #include "kda_linear.h"
 #include "kda_rows.h"
@@ -34,11 +46,14 @@ namespace {
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
-// A workgroup has a wave for every 16 columns of the state (channels of V).
+// A workgroup has a wave for every 16 columns of the state (channels of V):
+// waves of 32 columns read half of LDS for the same products, but a chunk's
+// phases then wait longer (the prompt of 4096 tokens took 78 us against 66).
 template <int DV> constexpr int kWaves = DV / 16;
 template <int DV> constexpr int kThreads = 64 * kWaves<DV>;
 
-// Tokens of a chunk: both types then fill LDS alike.
+// Tokens of a chunk: both types then fill LDS alike, and two workgroups of
+// the widest heads share a compute unit (80 KB each).
 template <typename T> constexpr int kTokens = sizeof(T) == 2 ? 64 : 32;
 
 // Orders LDS accesses only: the next chunk's loads stay in flight across it.
@@ -118,8 +133,8 @@ __device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
 // ---- operands rounded from fp32 ---------------------------------------------------
 // bf16 operands that are not inputs are sums of pieces of 8 bits each: two
 // (2^-17 of the value) where they only go into bf16 results, which rounds
-// those a hundred times more coarsely; three (2^-25) for the state, which is
-// handed out in fp32.  One piece for the products with P and S would double
+// those a hundred times more coarsely (the forward states of the backward pass
+// among them); three (2^-25) for a state that may be handed out in fp32.  One piece for the products with P and S would double
 // the outputs' mean square error.
 template <typename T> struct Pieces;
 template <> struct Pieces<float> {
@@ -600,7 +615,12 @@ struct Slot {
 // (blockIdx.y = 1) the gradient of the state at its start, of the sequence
 // that entered.  Rows and columns: k and v.  In the backward pass (TR) the
 // transposed states are wanted: v and k, and for the gradients dout and q.
-template <typename T, int DK, int DV, bool BACK, typename F>
+// 16 us for 4096 tokens of 16 bf16 heads, 256 workgroups of four chunks: 5300
+// cycles a chunk, of them 1540 of matrix instructions (three pieces of V) and
+// 1850 with their operands' reads; the first chunk waits 2800 for memory.  A
+// second set of tiles in LDS, one barrier a chunk, and the decays of four
+// chunks at once measured the same (57.1 and 58.4 us for the three launches).
+template <typename T, int DK, int DV, bool BACK, int PIECES, typename F>
 __device__ __forceinline__ void states_range(const LinearArgs& a, const View& k, const View& v, int h, int t0, int end,
                                              char* smem, State<DK, DV>& st, double* total, F&& enter) {
   constexpr int C = kTokens<T>, THREADS = kThreads<DV>;
@@ -638,7 +658,7 @@ __device__ __forceinline__ void states_range(const LinearArgs& a, const View& k,
     if (total) *total += d->sum[C - 1];
     typename Frag<T>::type vf[2];
     own_columns<T, DV>(V, lv, c0, vf);
-    step_state<T, DK, DV, Pieces<T>::STATE>(K, lk, vf, *d, lane, st);
+    step_state<T, DK, DV, PIECES>(K, lk, vf, *d, lane, st);
     decays(i + 1);
     lds_barrier();
   };
@@ -684,7 +704,8 @@ linear_states(const LinearArgs a, const T* __restrict__ dout, const float* __res
                                   TR ? a.dk : a.dv, lane, wave);
     };
     const View k{(const T*)a.k + hq * a.dk, a.ld_k, a.dk}, v{(const T*)a.v + h * a.dv, a.ld_v, a.dv};
-    states_range<T, DK, DV, false>(a, TR ? v : k, TR ? k : v, h, own ? start : w.lo, w.hi, smem, st, &total, enter);
+    states_range<T, DK, DV, false, TR ? Pieces<T>::OUT : Pieces<T>::STATE>(
+        a, TR ? v : k, TR ? k : v, h, own ? start : w.lo, w.hi, smem, st, &total, enter);
     st.store(ends + at, lane, wave);
     if (!own && threadIdx.x == 0) sums[(int64_t)w.slot * a.H + h] = total;
   } else if constexpr (TR) {
@@ -695,7 +716,8 @@ linear_states(const LinearArgs a, const T* __restrict__ dout, const float* __res
                                   a.dk, lane, wave);
     };
     const View q{(const T*)a.q + hq * a.dk, a.ld_q, a.dk}, d{dout + h * a.dv, (int64_t)a.H * a.dv, a.dv};
-    states_range<T, DK, DV, true>(a, d, q, h, w.lo, ends_here ? before : w.hi, smem, st, nullptr, enter);
+    states_range<T, DK, DV, true, Pieces<T>::STATE>(a, d, q, h, w.lo, ends_here ? before : w.hi, smem, st, nullptr,
+                                                    enter);
     st.store(adj + at, lane, wave);
   }
 }
@@ -703,7 +725,10 @@ linear_states(const LinearArgs a, const T* __restrict__ dout, const float* __res
 // True states at the slots' ends out of what each slot made of a zero state,
 // in place: S_i <- S_i + decay_i S_{i-1} where a sequence passes through slot
 // i; likewise (blockIdx.y = 1) the gradients from the last slot to the first.
-// A lane takes four elements; loads go ahead of the chain in batches.
+// A lane takes four elements; a batch of eight slots is loaded while the one
+// before is passed through (without: 2 to 5 us more; batches of 16 6 us more).
+// 8.4 us for 16 slots of 16 heads of 128 by 128, 33.5 MB read and written (4.0
+// TB/s, with hits in the caches).
 __global__ void __launch_bounds__(256)
 linear_chain(int H, int64_t quads, int n_slots, float* __restrict__ ends, float* __restrict__ adj,
              const double* __restrict__ sums, const int* __restrict__ kinds) {
@@ -753,6 +778,13 @@ linear_chain(int H, int64_t quads, int n_slots, float* __restrict__ ends, float*
 // ---- outputs -------------------------------------------------------------------------------
 // One form for the outputs and the three gradients ("sweep"): rows of Q meet
 // rows of K, whose weights sum rows of V.
+// A chunk of 64 bf16 tokens of 128 by 128 channels takes a workgroup 12,800
+// cycles, and the same beside a second one on the compute unit: 3100 are of
+// matrix instructions, 4300 of the vector unit (rounding to pieces, decays),
+// the rest waits, for LDS (480 KB read a chunk) and at three barriers.  Where
+// one workgroup a unit is left, two that share a slot, the second after a pass
+// over the first half for its state, took the same time as one (30.3 and 32.4
+// us for the prompt's sweep): the second pass's start costs what it hides.
 enum Role { kForward, kDq, kDk, kDv };
 
 struct Sweep {
@@ -1164,7 +1196,8 @@ linear_backward(const LinearArgs a, const LinearGrads g, const LinearWork x) {
 }
 
 // The decays' gradients: a wave takes one slot of one head, 64 tokens at a
-// time from each sequence's end, as suffix sums in 64 bits.
+// time from each sequence's end, as suffix sums in 64 bits.  5.5 us for 4096
+// tokens of 16 heads: four dependent rounds of 64 tokens a wave.
 template <typename T>
 __global__ void __launch_bounds__(64)
 linear_decay_grad(const LinearArgs a, const LinearWork x, T* __restrict__ dg) {
@@ -1205,7 +1238,8 @@ linear_decay_grad(const LinearArgs a, const LinearWork x, T* __restrict__ dg) {
   }
 }
 
-// Gradients of shared queries and keys: the sum over the heads that share.
+// Gradients of shared queries and keys: the sum over the heads that share, in
+// the order of the heads (atomics would change with the order of workgroups).
 // Tokens behind the last sequence have none.
 template <typename T>
 __global__ void __launch_bounds__(256)
@@ -1221,8 +1255,11 @@ linear_shared(const LinearArgs a, const float* __restrict__ pq, const float* __r
 }
 
 // ---- one token ------------------------------------------------------------------------------
-// The state is read once and written once.  A workgroup owns one (sequence,
-// head); a thread 4 columns of every (threads / LC)-th row.
+// The state is read once and written once, which is all that counts: 256
+// sequences of 32 heads of 128 by 128, 1.08 GB, 211 us, the rate of a large
+// copy (5.1 TB/s).  A workgroup owns one (sequence, head); a thread 4 columns of
+// every (threads / LC)-th row, with all its loads issued before the first use.
+// 4 sequences of 8 heads of 64 by 64 take 3.7 us, a launch and one round trip.
 template <typename T, int DK, int DV>
 __global__ void __launch_bounds__(DK * DV / 16)
 linear_step(const LinearArgs a, float* __restrict__ state, T* __restrict__ o) {
