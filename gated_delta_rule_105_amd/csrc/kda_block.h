@@ -53,7 +53,8 @@ constexpr int kBlockNormThreads = 256;
 constexpr int kBlockNormParts = 512;
 
 inline bool block_norm_fits(int64_t rows, int D, int elem) {
-  return rows <= INT32_MAX && grid_fits(ceil_div(rows, kBlockNormThreads / block_norm_shape(D, elem).lanes), kBlockNormThreads);
+  const int64_t each = kBlockNormThreads / block_norm_shape(D, elem).lanes;
+  return rows <= INT32_MAX && grid_fits(ceil_div(rows, each), kBlockNormThreads);
 }
 inline int64_t block_norm_parts(int64_t rows, int D, int elem) {
   const int64_t n = ceil_div(rows, kBlockNormThreads / block_norm_shape(D, elem).lanes);

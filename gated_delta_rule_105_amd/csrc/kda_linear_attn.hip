@@ -134,8 +134,9 @@ __device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
 // bf16 operands that are not inputs are sums of pieces of 8 bits each: two
 // (2^-17 of the value) where they only go into bf16 results, which rounds
 // those a hundred times more coarsely (the forward states of the backward pass
-// among them); three (2^-25) for a state that may be handed out in fp32.  One piece for the products with P and S would double
-// the outputs' mean square error.
+// among them); three (2^-25) for a state that may be handed out in fp32.  One
+// piece for the products with P and S would double the outputs' mean square
+// error.
 template <typename T> struct Pieces;
 template <> struct Pieces<float> {
   static constexpr int OUT = 1, STATE = 1;
@@ -789,7 +790,7 @@ enum Role { kForward, kDq, kDk, kDv };
 
 struct Sweep {
   View q, k, v;
-  View other;       // the rows that an output's state part is multiplied with for the decays' gradients
+  View other;       // the rows that outputs are multiplied with for the decays' gradients
   void* out;        // [tokens, H, v.d], this head's first element; fp32 with `wide`
   bool wide;
   float p_scale, row_scale, col_scale;

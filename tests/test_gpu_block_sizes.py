@@ -39,3 +39,48 @@ def test_backward(name):
         check(key, g[key], rg[key], rm[key], n)
     check("dg", g["dg"], rg["dg"], ref.suffix_magnitudes(**p, **u, cu=cu), n)
 
+
+
+def shifted(shape, dtype):
+    """A contiguous tensor one element behind a vector's boundary, between elements that nothing may write."""
+    n = 1
+    for s in shape:
+        n *= s
+    whole = torch.full((n + 2,), 7.0, dtype=dtype, device="cuda")
+    return whole, whole[1:-1].view(shape)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 40, 7])
+def test_outputs_and_gradients_at_single_elements(dtype, d):
+    """What a call writes lies at any element, as its inputs do: bit for bit what it is elsewhere."""
+    dt = linear.DT[dtype]
+    p, cu, u = linear.inputs(B=2, T=70, Hq=2, H=2, dk=d, dv=d, dtype=dtype, seed=4)
+    note(f"outputs at single elements {dtype} {d}")
+    o, _ = kda.linear_attn_forward(**p)
+    whole, odd = shifted(o.shape, dt)
+    kda.linear_attn_forward(**p, o=odd)
+    seen = [(whole, odd, o)]
+    g = kda.linear_attn_backward(**p, **u)
+    out = {k: shifted(g[k].shape, dt) for k in ("dq", "dk", "dv", "dg")}
+    do_whole, do = shifted(o.shape, dt)
+    do.copy_(u["do"])
+    kda.linear_attn_backward(**p, do=do, dht=u["dht"], out={k: v[1] for k, v in out.items()})
+    seen += [(*out[k], g[k]) for k in out] + [(do_whole, do, u["do"])]
+    y = kda.gated_norm_forward(o, p["v"])
+    whole, odd = shifted(y.shape, dt)
+    kda.gated_norm_forward(o, p["v"], y=odd)
+    seen.append((whole, odd, y))
+    n = kda.gated_norm_backward(o, p["v"], u["do"])
+    out = {k: shifted(n[k].shape, dt) for k in ("dx", "dgate")}
+    kda.gated_norm_backward(o, p["v"], do, out={k: v[1] for k, v in out.items()})
+    seen += [(*out[k], n[k]) for k in out]
+    x, r = o.flatten(2), u["do"].flatten(2)
+    y, total = kda.residual_norm_forward(x, r)
+    a, b = shifted(y.shape, dt), shifted(y.shape, dt)
+    kda.residual_norm_forward(x, r, y=a[1], total=b[1])
+    seen += [(*a, y), (*b, total)]
+    torch.cuda.synchronize()
+    for whole, odd, want in seen:
+        assert torch.equal(odd, want)
+        assert whole[0] == 7.0 and whole[-1] == 7.0
