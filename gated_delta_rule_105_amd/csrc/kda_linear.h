@@ -45,6 +45,8 @@ struct LinearPlan {
 // The kernels' tiles hold 64 or 128 channels of either kind; so do the states
 // in the workspace.
 constexpr int linear_pad(int d) { return d <= 64 ? 64 : 128; }
+// Workgroups that a compute unit holds, by the tiles' channels.
+constexpr int linear_groups_of_unit(int dk, int dv) { return dk <= 64 && dv <= 64 ? 3 : 2; }
 constexpr size_t linear_record(int dk, int dv) { return (size_t)linear_pad(dk) * linear_pad(dv); }
 
 inline LinearPlan plan_linear(int64_t tokens, int rows, int64_t T, bool packed, int H, int n_cu, int dk, int dv,
@@ -61,8 +63,8 @@ inline LinearPlan plan_linear(int64_t tokens, int rows, int64_t T, bool packed, 
     p.slot = T;
     p.n_slots = rows;
   } else {
-    // Two workgroups for every compute unit, unless their states, one for every
-    // slot and head, then cost more than the second workgroup hides: at least
+    // As many workgroups as every compute unit holds, unless their states, one
+    // for every slot and head, then cost more than the others hide: at least
     // the tokens whose keys and values are half a state (256 with 128 channels
     // of both; half of that took 61.5 us against 55.4 for 4096 tokens of 16
     // heads, and their gradients 153 against 139).  Where that leaves more than
@@ -72,9 +74,9 @@ inline LinearPlan plan_linear(int64_t tokens, int rows, int64_t T, bool packed, 
       const int64_t n = groups / H < 1 ? 1 : groups / H;
       return ceil_div(ceil_div(tokens, n), kLinearChunk) * kLinearChunk;
     };
-    const int64_t two = slots_of(2 * cus), one = slots_of(cus);
+    const int64_t full = slots_of(linear_groups_of_unit(dk, dv) * cus), one = slots_of(cus);
     const int64_t least = ceil_div(4 * dk * dv / (dk + dv), kLinearChunk) * kLinearChunk;
-    p.slot = two >= least ? two : one < least ? one : least;
+    p.slot = full >= least ? full : one < least ? one : least;
     p.n_slots = ceil_div(tokens, p.slot);
   }
   p.carry = p.n_slots > 1 && (packed || p.slot % T != 0);

@@ -51,6 +51,8 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 // phases then wait longer (the prompt of 4096 tokens took 78 us against 66).
 template <int DV> constexpr int kWaves = DV / 16;
 template <int DV> constexpr int kThreads = 64 * kWaves<DV>;
+// the waves of a SIMD that registers are left for
+template <int DK, int DV> constexpr int kWavesOfSimd = linear_groups_of_unit(DK, DV) * kWaves<DV> / 4;
 
 // Tokens of a chunk: both types then fill LDS alike, and two workgroups of
 // the widest heads share a compute unit (80 KB each).
@@ -679,7 +681,7 @@ __device__ __forceinline__ void states_range(const LinearArgs& a, const View& k,
 template <typename T, int DK, int DV>
 constexpr int kStatesLds = kTileBytes<T, DK> + kTileBytes<T, DV> + 2 * (int)sizeof(Decays<T>);
 template <typename T, int DK, int DV, bool TR>
-__global__ void __launch_bounds__(kThreads<DV>, 2 * kThreads<DV> / 256)
+__global__ void __launch_bounds__(kThreads<DV>, (kWavesOfSimd<DK, DV>))
 linear_states(const LinearArgs a, const T* __restrict__ dout, const float* __restrict__ dht, float* __restrict__ ends,
               float* __restrict__ adj, double* __restrict__ sums, int* __restrict__ kinds) {
   __shared__ __align__(16) char smem[kStatesLds<T, DK, DV>];
@@ -797,10 +799,16 @@ struct Sweep {
   float* dots;      // [H, tokens], this head's row (null: none)
 };
 
+// P's rows have 16 elements more than C, as the inputs'; with 64 channels of
+// both kinds 8 (rows of a tile then share banks), so that a third workgroup
+// fits on the compute unit (52 KB; gradients of 4096 packed tokens of 16 heads
+// 121 us against 131).
+template <typename T, int DK, int DV> constexpr int kPWidth = DK == 64 && DV == 64 ? kTokens<T> - 8 : kTokens<T>;
+
 template <typename T, int DK, int DV>
 struct SweepLds {
   T q[kTokens<T> * kLd<DK>], k[kTokens<T> * kLd<DK>], v[kTokens<T> * kLd<DV>];
-  T p[Pieces<T>::OUT][kTokens<T> * kLd<kTokens<T>>];
+  T p[Pieces<T>::OUT][kTokens<T> * kLd<kPWidth<T, DK, DV>>];
   Decays<T> d[2];  // of this chunk and the next
   int wild;
   float dot[kWaves<DV>][kTokens<T>];
@@ -885,10 +893,11 @@ __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w,
     const Decays<T>& d = m.d[buf];
 
     // P, shared out by tiles
+    constexpr int PW = kPWidth<T, DK, DV>;
     auto p_tile = [&](int tile) {
       const int ln = here(lane), g = ln >> 4, i16 = ln & 15;
       const Lane<T, DK> lk(ln);
-      const Lane<T, C> lp(ln);
+      const Lane<T, PW> lp(ln);
       int ra, rb;
       tile_of(tile, &ra, &rb);
       const int rt = BACK ? rb : ra, ct = BACK ? ra : rb;
@@ -926,7 +935,7 @@ __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w,
       f32x4 x = p;
 #pragma unroll
       for (int c = 0; c < OUT; ++c) {
-        T* at = m.p[c] + lp.row + 16 * rt * kLd<C> + 16 * ct;
+        T* at = m.p[c] + lp.row + 16 * rt * kLd<PW> + 16 * ct;
         if constexpr (sizeof(T) == 2) {
           const uint2 b = make_uint2(__builtin_bit_cast(uint32_t, f32x2_to_bf16x2(x[0], x[1])),
                                      __builtin_bit_cast(uint32_t, f32x2_to_bf16x2(x[2], x[3])));
@@ -976,7 +985,7 @@ __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w,
     decays(buf ^ 1, n_next);
     lds_barrier();
     // the chunk's own part
-    const Lane<T, C> lp(ln);
+    const Lane<T, PW> lp(ln);
     frag vf[2];
     own_columns<T, DV>(m.v, Lane<T, DV>(ln), c0, vf);
     if (!strict || n > 1)  // the one token may hold an infinity, which a zero is not multiplied with
@@ -987,7 +996,7 @@ __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w,
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) {
             if (BACK ? KB * (kb + 1) <= 16 * rt : KB * kb > 16 * rt) continue;  // zeros of P
-            acc[rt] = mma(vf[kb], row_frag<C>(m.p[c], lp, 16 * rt, KB * kb), acc[rt]);
+            acc[rt] = mma(vf[kb], row_frag<PW>(m.p[c], lp, 16 * rt, KB * kb), acc[rt]);
           }
     if (strict) {
       float s[RT];
@@ -1120,7 +1129,7 @@ __device__ __forceinline__ void sweep_slot(const LinearArgs& a, const Sweep& w, 
 }
 
 template <typename T, int DK, int DV>
-__global__ void __launch_bounds__(kThreads<DV>, 2 * kThreads<DV> / 256)
+__global__ void __launch_bounds__(kThreads<DV>, (kWavesOfSimd<DK, DV>))
 linear_forward(const LinearArgs a, const float* __restrict__ ends, T* __restrict__ o, float* __restrict__ ht) {
   __shared__ __align__(16) SweepLds<T, DK, DV> m;
   const int h = (int)(blockIdx.x % (unsigned)a.H), hq = h / (a.H / a.Hq);
@@ -1178,7 +1187,8 @@ __device__ __forceinline__ void gradient(const LinearArgs& a, const LinearGrads&
 // The workgroups of a launch take its roles in turn: all three where their
 // workgroups are of one size, else those with columns of d_k, and dv alone.
 template <typename T, int DK, int DV, Role FIRST, int COUNT>
-__global__ void __launch_bounds__(kThreads<FIRST == kDv ? DV : DK>, 2 * kThreads<FIRST == kDv ? DV : DK> / 256)
+__global__ void __launch_bounds__(kThreads<(FIRST == kDv ? DV : DK)>,
+                                  (kWavesOfSimd<(FIRST == kDv ? DK : DV), (FIRST == kDv ? DV : DK)>))
 linear_backward(const LinearArgs a, const LinearGrads g, const LinearWork x) {
   typedef SweepLds<T, DV, DK> OfKeys;
   typedef SweepLds<T, DK, DV> OfValues;

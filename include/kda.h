@@ -648,7 +648,7 @@ typedef struct {
  * Outputs must not overlap each other, the inputs or the workspace.  The
  * workspace (kda_linear_attn_workspace_size; 0 bytes when the batch alone
  * fills the device) holds the state of every range of tokens that the call
- * scans side by side: about two states for every compute unit at most.
+ * scans side by side: about three states for every compute unit at most.
  * Token rows (ld_q .. ld_g, and H d_k, H d_v) lie at most 2^22 elements apart,
  * and a batch has fewer than 2^31 - 4096 tokens (KDA_ERR_UNSUPPORTED).
  */

@@ -7,10 +7,10 @@ LINEAR = {
     # as many tokens as the states are worth
     "least-tokens": dict(B=1, T=2500, Hq=2, H=8, dk=16, dv=16, dtype="bf16", slots=(128, 20)),
     "least-tokens-f32": dict(B=2, T=1250, Hq=8, H=8, dk=8, dv=20, dtype="f32", slots=(128, 20)),
-    # two for every unit
-    "two-for-each-unit": dict(B=1, T=8300, Hq=4, H=8, dk=16, dv=12, dtype="bf16", slots=(192, 44)),
-    "two-packed": dict(B=1, T=0, Hq=2, H=8, dk=12, dv=16, dtype="bf16", lengths=[3000, 1, 0, 5400, 63, 64, 65],
-                       slots=(192, 45)),
+    # as many as every unit holds: three of 64 columns
+    "three-for-each-unit": dict(B=1, T=8300, Hq=3, H=6, dk=16, dv=12, dtype="bf16", slots=(128, 65)),
+    "three-packed": dict(B=1, T=0, Hq=2, H=6, dk=12, dv=16, dtype="bf16", lengths=[3000, 1, 0, 5400, 63, 64, 65],
+                         slots=(128, 68)),
     "wide-slots": dict(B=1, T=600, Hq=2, H=12, dk=100, dv=72, dtype="bf16", slots=(64, 10)),
 }
 
