@@ -690,7 +690,9 @@ __device__ __forceinline__ void state_out(const unsigned char* smem, int buf, f3
         const uint2 p = __builtin_bit_cast(uint2, to_bf16x4(acc));
         __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, p), ro, voff, soff, 0);
       } else {
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc), ro, voff, soff, 0);
+        // 16 bytes: the row in the lanes' offset, for behind a store with a scalar one the compiler leaves no wait state
+        // before the next write of acc's registers
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc), ro, voff + (uint32_t)soff, 0, 0);
       }
     }
   }
