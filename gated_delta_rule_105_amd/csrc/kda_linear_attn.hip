@@ -133,19 +133,14 @@ __device__ __forceinline__ float swap_sum(float x, float y) {
 __device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
 
 // ---- operands rounded from fp32 ---------------------------------------------------
-// bf16 operands that are not inputs are sums of pieces of 8 bits each: two
-// (2^-17 of the value) where they only go into bf16 results, which rounds
-// those a hundred times more coarsely (the forward states of the backward pass
-// among them); three (2^-25) for a state that may be handed out in fp32.  One
-// piece for the products with P and S would double the outputs' mean square
-// error.
+// bf16 operands that are not inputs (weights, states, decayed values) are sums
+// of three pieces of 8 bits each, which is all of an fp32 number.  Two pieces
+// would leave ten times as many outputs off the rounding of their value (2e-3
+// of them against 2e-4), and a sum that cancels without its last bits.
 template <typename T> struct Pieces;
 template <> struct Pieces<float> {
-  static constexpr int OUT = 1, STATE = 1;
-  template <int N>
-  __device__ static __forceinline__ void cut(const f32x4 (&x)[1], f32x4 (&f)[N]) {
-    f[0] = x[0];
-  }
+  static constexpr int COUNT = 1;
+  __device__ static __forceinline__ f32x4 next(f32x4 (&x)[1]) { return x[0]; }
 };
 __device__ __forceinline__ bf16x8 round8(const f32x4& a, const f32x4& b) { return frag_from_acc(a, b); }
 __device__ __forceinline__ f32x4 low4(const bf16x8& f, int half) {
@@ -155,16 +150,13 @@ __device__ __forceinline__ f32x4 low4(const bf16x8& f, int half) {
                  __uint_as_float(b & 0xffff0000u)};
 }
 template <> struct Pieces<bf16_t> {
-  static constexpr int OUT = 2, STATE = 3;
-  template <int N>
-  __device__ static __forceinline__ void cut(const f32x4 (&x)[2], bf16x8 (&f)[N]) {
-    f32x4 a = x[0], b = x[1];
-#pragma unroll
-    for (int p = 0; p < N; ++p) {
-      f[p] = round8(a, b);
-      a -= low4(f[p], 0);
-      b -= low4(f[p], 1);
-    }
+  static constexpr int COUNT = 3;
+  // the largest piece of what is left of x, and the rest
+  __device__ static __forceinline__ bf16x8 next(f32x4 (&x)[2]) {
+    const bf16x8 f = round8(x[0], x[1]);
+    x[0] -= low4(f, 0);
+    x[1] -= low4(f, 1);
+    return f;
   }
 };
 // accumulator tiles that make one operand
@@ -563,10 +555,10 @@ struct State {
 // ---- a chunk's step of the state ------------------------------------------------------
 // S <- whole S + K^T (col V): V's fragments are this wave's own columns,
 // scaled and cut to pieces; K's are read from LDS as they are.
-template <typename T, int DK, int DV, int PIECES>
+template <typename T, int DK, int DV>
 __device__ __forceinline__ void step_state(const T* K, const Lane<T, DK>& lk, const typename Frag<T>::type (&vf)[2],
                                            const Decays<T>& d, int lane, State<DK, DV>& st) {
-  constexpr int KB = Elem<T>::KB;
+  constexpr int KB = Elem<T>::KB, PIECES = Pieces<T>::COUNT;
   const int g = lane >> 4;
   const float whole = d.whole;
 #pragma unroll
@@ -578,7 +570,8 @@ __device__ __forceinline__ void step_state(const T* K, const Lane<T, DK>& lk, co
     widen(vf[kb], x);
 #pragma unroll
     for (int h = 0; h < kAccs<T>; ++h) x[h] *= *(const f32x4*)(d.col + KB * kb + 16 * h + 4 * g);
-    Pieces<T>::template cut<PIECES>(x, f);
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p) f[p] = Pieces<T>::next(x);
     // four row tiles at a time: a product's result is not wanted by the next
 #pragma unroll
     for (int m = 0; m < DK / 16; m += 4) {
@@ -623,7 +616,7 @@ struct Slot {
 // 1850 with their operands' reads; the first chunk waits 2800 for memory.  A
 // second set of tiles in LDS, one barrier a chunk, and the decays of four
 // chunks at once measured the same (57.1 and 58.4 us for the three launches).
-template <typename T, int DK, int DV, bool BACK, int PIECES, typename F>
+template <typename T, int DK, int DV, bool BACK, typename F>
 __device__ __forceinline__ void states_range(const LinearArgs& a, const View& k, const View& v, int h, int t0, int end,
                                              char* smem, State<DK, DV>& st, double* total, F&& enter) {
   constexpr int C = kTokens<T>, THREADS = kThreads<DV>;
@@ -661,7 +654,7 @@ __device__ __forceinline__ void states_range(const LinearArgs& a, const View& k,
     if (total) *total += d->sum[C - 1];
     typename Frag<T>::type vf[2];
     own_columns<T, DV>(V, lv, c0, vf);
-    step_state<T, DK, DV, PIECES>(K, lk, vf, *d, lane, st);
+    step_state<T, DK, DV>(K, lk, vf, *d, lane, st);
     decays(i + 1);
     lds_barrier();
   };
@@ -707,8 +700,7 @@ linear_states(const LinearArgs a, const T* __restrict__ dout, const float* __res
                                   TR ? a.dk : a.dv, lane, wave);
     };
     const View k{(const T*)a.k + hq * a.dk, a.ld_k, a.dk}, v{(const T*)a.v + h * a.dv, a.ld_v, a.dv};
-    states_range<T, DK, DV, false, TR ? Pieces<T>::OUT : Pieces<T>::STATE>(
-        a, TR ? v : k, TR ? k : v, h, own ? start : w.lo, w.hi, smem, st, &total, enter);
+    states_range<T, DK, DV, false>(a, TR ? v : k, TR ? k : v, h, own ? start : w.lo, w.hi, smem, st, &total, enter);
     st.store(ends + at, lane, wave);
     if (!own && threadIdx.x == 0) sums[(int64_t)w.slot * a.H + h] = total;
   } else if constexpr (TR) {
@@ -719,8 +711,7 @@ linear_states(const LinearArgs a, const T* __restrict__ dout, const float* __res
                                   a.dk, lane, wave);
     };
     const View q{(const T*)a.q + hq * a.dk, a.ld_q, a.dk}, d{dout + h * a.dv, (int64_t)a.H * a.dv, a.dv};
-    states_range<T, DK, DV, true, Pieces<T>::STATE>(a, d, q, h, w.lo, ends_here ? before : w.hi, smem, st, nullptr,
-                                                    enter);
+    states_range<T, DK, DV, true>(a, d, q, h, w.lo, ends_here ? before : w.hi, smem, st, nullptr, enter);
     st.store(adj + at, lane, wave);
   }
 }
@@ -799,27 +790,44 @@ struct Sweep {
   float* dots;      // [H, tokens], this head's row (null: none)
 };
 
-// P's rows have 16 elements more than C, as the inputs'; with 64 channels of
-// both kinds 8 (rows of a tile then share banks), so that a third workgroup
-// fits on the compute unit (52 KB; gradients of 4096 packed tokens of 16 heads
-// 121 us against 131).
-template <typename T, int DK, int DV> constexpr int kPWidth = DK == 64 && DV == 64 ? kTokens<T> - 8 : kTokens<T>;
+// P's tiles on and beside the diagonal, in the order that waves take them.
+__device__ __forceinline__ void tile_of(int t, int* a, int* b) {
+  *a = t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3;
+  *b = t - *a * (*a + 1) / 2;
+}
+template <typename T> constexpr int kRowTiles = kTokens<T> / 16;
+template <typename T> constexpr int kPTiles = kRowTiles<T> * (kRowTiles<T> + 1) / 2;
+
+// Tiles of P in LDS are in the order of the lanes, four elements of a row
+// each: the lane that formed them is the one that reads them.
+// P's operand of row tile rt for the tokens from KB kb on; the other side of
+// the diagonal (BACK: before rt) is zeros.
+template <bool BACK, int KB>
+__device__ __forceinline__ bf16x8 p_frag(const bf16_t* P, int rt, int kb, int lane) {
+  bf16x4 x[2];
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int ct = 2 * kb + half, hi = ct > rt ? ct : rt, lo = ct > rt ? rt : ct;
+    x[half] = (BACK ? ct >= rt : ct <= rt) ? *(const bf16x4*)(P + (hi * (hi + 1) / 2 + lo) * 256 + 4 * lane)
+                                           : __builtin_bit_cast(bf16x4, (uint64_t)0);
+  }
+  return (bf16x8){x[0][0], x[0][1], x[0][2], x[0][3], x[1][0], x[1][1], x[1][2], x[1][3]};
+}
+template <bool BACK, int KB>
+__device__ __forceinline__ f32x4 p_frag(const float* P, int rt, int ct, int lane) {
+  const int hi = ct > rt ? ct : rt, lo = ct > rt ? rt : ct;
+  return *(const f32x4*)(P + (hi * (hi + 1) / 2 + lo) * 256 + 4 * lane);
+}
 
 template <typename T, int DK, int DV>
 struct SweepLds {
   T q[kTokens<T> * kLd<DK>], k[kTokens<T> * kLd<DK>], v[kTokens<T> * kLd<DV>];
-  T p[Pieces<T>::OUT][kTokens<T> * kLd<kPWidth<T, DK, DV>>];
+  T p[Pieces<T>::COUNT][kPTiles<T> * 256];
   Decays<T> d[2];  // of this chunk and the next
   int wild;
   float dot[kWaves<DV>][kTokens<T>];
   float diagonal[kTokens<T>];  // of P, where it is kept apart
 };
-
-// the tiles on and beside the diagonal, in the order that waves take them
-__device__ __forceinline__ void tile_of(int t, int* a, int* b) {
-  *a = t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3;
-  *b = t - *a * (*a + 1) / 2;
-}
 
 // Tokens [t0, end) of one sequence; the state before them (BACK: the gradient
 // of the state after them) comes from `enter`, called when the first loads are
@@ -827,10 +835,9 @@ __device__ __forceinline__ void tile_of(int t, int* a, int* b) {
 template <typename T, int DK, int DV, Role R, typename F>
 __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w, int h, int t0, int end,
                                             SweepLds<T, DK, DV>& m, State<DK, DV>& st, F&& enter) {
-  // the state of these two roles is handed out at a sequence's end
-  constexpr bool BACK = R == kDk || R == kDv, KEPT = R == kForward || R == kDv;
-  constexpr int C = kTokens<T>, KB = Elem<T>::KB, RT = C / 16, TILES = RT * (RT + 1) / 2;
-  constexpr int OUT = Pieces<T>::OUT, WAVES = kWaves<DV>, THREADS = kThreads<DV>;
+  constexpr bool BACK = R == kDk || R == kDv;
+  constexpr int C = kTokens<T>, KB = Elem<T>::KB, RT = kRowTiles<T>, TILES = kPTiles<T>;
+  constexpr int PIECES = Pieces<T>::COUNT, WAVES = kWaves<DV>, THREADS = kThreads<DV>;
   typedef typename Frag<T>::type frag;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), c0 = wave * 16;
   const int chunks = (end - t0 + C - 1) / C;
@@ -893,11 +900,9 @@ __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w,
     const Decays<T>& d = m.d[buf];
 
     // P, shared out by tiles
-    constexpr int PW = kPWidth<T, DK, DV>;
     auto p_tile = [&](int tile) {
       const int ln = here(lane), g = ln >> 4, i16 = ln & 15;
       const Lane<T, DK> lk(ln);
-      const Lane<T, PW> lp(ln);
       int ra, rb;
       tile_of(tile, &ra, &rb);
       const int rt = BACK ? rb : ra, ct = BACK ? ra : rb;
@@ -934,8 +939,8 @@ __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w,
       }
       f32x4 x = p;
 #pragma unroll
-      for (int c = 0; c < OUT; ++c) {
-        T* at = m.p[c] + lp.row + 16 * rt * kLd<PW> + 16 * ct;
+      for (int c = 0; c < PIECES; ++c) {
+        T* at = m.p[c] + tile * 256 + 4 * ln;
         if constexpr (sizeof(T) == 2) {
           const uint2 b = make_uint2(__builtin_bit_cast(uint32_t, f32x2_to_bf16x2(x[0], x[1])),
                                      __builtin_bit_cast(uint32_t, f32x2_to_bf16x2(x[2], x[3])));
@@ -965,18 +970,19 @@ __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w,
     for (int rt = 0; rt < RT; ++rt) acc[rt] = (f32x4){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int kb = 0; kb < DK / KB; ++kb) {
-      frag sf[OUT];
       f32x4 s[kAccs<T>];
 #pragma unroll
       for (int e = 0; e < kAccs<T>; ++e) s[e] = st.s[kAccs<T> * kb + e];
-      Pieces<T>::template cut<OUT>(s, sf);
       frag qf[RT];
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) qf[rt] = row_frag<DK>(m.q, lk, 16 * rt, KB * kb);
+      // a piece at a time: three together would cost registers
 #pragma unroll
-      for (int c = OUT - 1; c >= 0; --c)
+      for (int c = 0; c < PIECES; ++c) {
+        const frag sf = Pieces<T>::next(s);
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) acc[rt] = mma(sf[c], qf[rt], acc[rt]);
+        for (int rt = 0; rt < RT; ++rt) acc[rt] = mma(sf, qf[rt], acc[rt]);
+      }
     }
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) acc[rt] *= d.row[16 * rt + i16];
@@ -985,18 +991,17 @@ __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w,
     decays(buf ^ 1, n_next);
     lds_barrier();
     // the chunk's own part
-    const Lane<T, PW> lp(ln);
     frag vf[2];
     own_columns<T, DV>(m.v, Lane<T, DV>(ln), c0, vf);
     if (!strict || n > 1)  // the one token may hold an infinity, which a zero is not multiplied with
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-        for (int c = OUT - 1; c >= 0; --c)
+        for (int c = PIECES - 1; c >= 0; --c)
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) {
             if (BACK ? KB * (kb + 1) <= 16 * rt : KB * kb > 16 * rt) continue;  // zeros of P
-            acc[rt] = mma(vf[kb], row_frag<PW>(m.p[c], lp, 16 * rt, KB * kb), acc[rt]);
+            acc[rt] = mma(vf[kb], p_frag<BACK, KB>(m.p[c], rt, kb, ln), acc[rt]);
           }
     if (strict) {
       float s[RT];
@@ -1040,7 +1045,7 @@ __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w,
     } else {
       out_as(T{});
     }
-    step_state<T, DK, DV, KEPT ? Pieces<T>::STATE : OUT>(m.k, Lane<T, DK>(here(lane)), vf, d, lane, st);
+    step_state<T, DK, DV>(m.k, Lane<T, DK>(here(lane)), vf, d, lane, st);
     lds_barrier();
     if (by_rows) Stage<T, DV, THREADS>::write(m.v, y, t, n);
     if (strict && (int)threadIdx.x < n) {
@@ -1075,8 +1080,6 @@ __device__ __forceinline__ void sweep_slot(const LinearArgs& a, const Sweep& w, 
   const int64_t floats = (int64_t)a.dk * a.dv, record = DK * DV;
   const int rows = w.q.d, cols = w.v.d;
   State<DK, DV> st;
-  // all of P beside the tiles that are written stays zero
-  for (int x = threadIdx.x; x < (int)(sizeof(m.p) / 16); x += kThreads<DV>) ((uint4*)m.p)[x] = make_uint4(0, 0, 0, 0);
   if (threadIdx.x == 0) m.wild = 0;
   lds_barrier();
   auto of_slot = [&](int i) { return enter + ((int64_t)i * a.H + h) * record; };
