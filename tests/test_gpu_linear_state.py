@@ -19,6 +19,40 @@ pytestmark = pytest.mark.gpu
 STEP = 2.0 ** -24
 
 
+@pytest.mark.parametrize("d_k,d_v", [(4, 8)])
+def test_state_that_only_decays(d_k, d_v):
+    B, T, H, chunk = 16, 8192, 16, 32
+    note(f"linear_attn state that only decays {d_k} {d_v}")
+    gen = torch.Generator().manual_seed(11)
+    g = -2e-3 * torch.rand(B, T, H, generator=gen)
+    zero = torch.zeros(B, T, H, d_k, device="cuda")
+    v = torch.zeros(B, T, H, d_v, device="cuda")
+    one = torch.ones(B, H, d_k, d_v, device="cuda")
+    o, ht = kda.linear_attn_forward(zero, zero, v, g.cuda(), h0=one)
+    r = kda.linear_attn_backward(zero, zero, v, v, g.cuda(), h0=one, dht=one)
+    torch.cuda.synchronize()
+    want = torch.exp(g.double().sum(1))[..., None, None]
+    for name, got in (("ht", ht), ("dh0", r["dh0"])):
+        off = (got.cpu().double() / want - 1) / STEP
+        assert float(off.square().mean()) <= T // chunk * (1.3 ** 2 + 1), name
+
+
+def test_steps_that_only_decay():
+    """The same by single tokens: a decay and a product of each."""
+    N, H, T = 16, 16, 4096
+    note("linear_attn_step that only decays")
+    gen = torch.Generator().manual_seed(12)
+    g = -2e-3 * torch.rand(T, N, H, generator=gen)
+    zero = torch.zeros(N, H, 4, device="cuda")
+    state = torch.ones(N, H, 4, 4, device="cuda")
+    on_device = g.cuda()
+    for t in range(T):
+        kda.linear_attn_step(zero, zero, zero, state, on_device[t])
+    torch.cuda.synchronize()
+    off = (state.cpu().double() / torch.exp(g.double().sum(0))[..., None, None] - 1) / STEP
+    assert float(off.square().mean()) <= T * (1.3 ** 2 + 1)
+
+
 def test_state_that_only_grows():
     """Without a decay the state is a sum of T / 32 chunks' sums, each less than sqrt(32) of its own size beside it:
     the state's roundings are one a chunk."""
