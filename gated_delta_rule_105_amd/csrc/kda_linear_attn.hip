@@ -210,7 +210,8 @@ template <typename T, int W, int THREADS> struct Stage {
     for (int i = 0; i < N; ++i)
       v[i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(rows, off, i * RPP * step, 0));
   }
-  __device__ __forceinline__ void store(T* X, const View& x, int tok, int n) {
+  // Whether a row of fewer channels than a vector has holds an infinity or a NaN.
+  __device__ __forceinline__ bool store(T* X, const View& x, int tok, int n) {
     const int thread = here((int)threadIdx.x), c = thread % VPR * VE, r = thread / VPR;
     if (x.d % VE != 0 && x.d >= VE) {
       const bool tail = c < x.d && c + VE > x.d;
@@ -236,12 +237,17 @@ template <typename T, int W, int THREADS> struct Stage {
       }
     }
     // rows of fewer channels than a vector has, over the zeros that the same lane wrote
+    bool narrow_wild = false;
     if (x.d < VE && c == 0)
 #pragma unroll 1
       for (int k = r; k < n; k += RPP)
 #pragma unroll 1
-        for (int e = 0; e < x.d; ++e)
-          X[k * kLd<W> + (((e >> 2) ^ ((k >> 2) & 3)) << 2) + (e & 3)] = ((const T*)x.p)[(int64_t)(tok + k) * x.ld + e];
+        for (int e = 0; e < x.d; ++e) {
+          const T y = ((const T*)x.p)[(int64_t)(tok + k) * x.ld + e];
+          X[k * kLd<W> + (((e >> 2) ^ ((k >> 2) & 3)) << 2) + (e & 3)] = y;
+          narrow_wild |= (__float_as_uint(Elem<T>::to_f32(y)) & 0x7f800000u) == 0x7f800000u;
+        }
+    return narrow_wild;
   }
   // Back to memory, from the places that store() gives a lane, so that it may
   // write them anew without a barrier.  Whole vectors only.
@@ -268,8 +274,8 @@ template <typename T, int W, int THREADS> struct Stage {
   }
   // Whether some row may hold an infinity or a NaN: the largest magnitude of
   // all that was read, so that zeros for what is not there need no care.
-  __device__ __forceinline__ bool wild(const View& x) const {
-    if (x.d < VE) return true;
+  // Narrow rows are not in the registers: store() tells of them.
+  __device__ __forceinline__ bool wild() const {
     if constexpr (sizeof(T) == 2) {
       typedef uint16_t pair __attribute__((ext_vector_type(2)));
       pair most = {0, 0};
@@ -921,10 +927,10 @@ __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w,
   enter();
   decays(0, n);
   while (true) {
-    if (!single && n > 1 && __ballot(sv.wild(w.v)) != 0 && lane == 0) m.wild = 1;
     sq.store(m.q, w.q, t, n);
     sk.store(m.k, w.k, t, n);
-    sv.store(m.v, w.v, t, n);
+    const bool narrow_wild = sv.store(m.v, w.v, t, n);
+    if (!single && n > 1 && __ballot(narrow_wild || sv.wild()) != 0 && lane == 0) m.wild = 1;
     lds_barrier();
     if (!single && uniform(m.wild)) {
       lds_barrier();  // all have read it

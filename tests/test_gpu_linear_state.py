@@ -19,7 +19,7 @@ pytestmark = pytest.mark.gpu
 STEP = 2.0 ** -24
 
 
-@pytest.mark.parametrize("d_k,d_v", [(4, 8)])
+@pytest.mark.parametrize("d_k,d_v", [(4, 8), (4, 3), (2, 8)])
 def test_state_that_only_decays(d_k, d_v):
     B, T, H, chunk = 16, 8192, 16, 32
     note(f"linear_attn state that only decays {d_k} {d_v}")
