@@ -100,19 +100,30 @@ __device__ __forceinline__ void row_sums(float (&v)[K], float (*lds)[kWaves]) {
 
 __device__ __forceinline__ float inv_norm(float ss, int D, float eps) { return 1.f / sqrtf(ss / (float)D + eps); }
 
+// e^x within 3 times 2^-24 of itself: x in units of a factor 2 is a rounded
+// product, and what it left out is a factor of its own (without it the result
+// is |x| roundings off: 3.7e-6 of a gate at -86).
+__device__ __forceinline__ float exp_of(float x) {
+  constexpr float kLn2Rest = -1.9046542e-9f;  // ln 2 - kLn2
+  const float hi = x * kLog2e, e = exp2_fast(hi);
+  const float rest = __builtin_fmaf(-hi, kLn2Rest, __builtin_fmaf(-hi, kLn2, x));
+  // past what fp32 holds there is no rest, only 0 or an infinity
+  return __builtin_fabsf(x) < 87.f ? __builtin_fmaf(e, rest, e) : e;
+}
+
 // a(z) and a'(z).  Of the sigmoid and its complement the smaller is e^-|z|
 // times the larger, so neither is a difference.
 struct Gate {
   float a, slope;
   __device__ __forceinline__ Gate(float z, int silu) {
-    const float e = exp2_fast(-kLog2e * __builtin_fabsf(z)), big = __builtin_amdgcn_rcpf(1.f + e), small = e * big;
+    const float e = exp_of(-__builtin_fabsf(z)), big = __builtin_amdgcn_rcpf(1.f + e), small = e * big;
     const float s = z < 0.f ? small : big, c = z < 0.f ? big : small;
     a = silu ? z * s : s;
     slope = silu ? s * (1.f + z * c) : s * c;
   }
   // a(z) alone: below -88 the sigmoid is 0, within what fp32 holds as a normal number
   __device__ __forceinline__ static float value(float z, int silu) {
-    const float s = __builtin_amdgcn_rcpf(1.f + exp2_fast(-kLog2e * z));
+    const float s = __builtin_amdgcn_rcpf(1.f + exp_of(-z));
     return silu ? z * s : s;
   }
 };
