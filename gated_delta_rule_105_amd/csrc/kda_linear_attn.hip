@@ -473,15 +473,16 @@ template <typename T> struct Decays {
   double sum[kTokens<T>];               // running sums
   float row[kTokens<T>], col[kTokens<T>];  // factors of the state's part of an output, and of a token's part in the state
   float whole;
-  __device__ __forceinline__ void fill(float g, int n, bool back, float row_scale, float col_scale, int lane) {
+  // `lone`: a single token is none away from itself, also where its decay is a NaN
+  __device__ __forceinline__ void fill(float g, int n, bool back, bool lone, float row_scale, float col_scale, int lane) {
     const double s = wave_sums(lane < n ? log2_decay(g) : 0.0);
     const uint64_t w = __builtin_bit_cast(uint64_t, s);
     const double all = __builtin_bit_cast(
         double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(w >> 32), 63) << 32 |
                     (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)w, 63));
-    const float since = decay_of(s), until = decay_of(all - s);
+    const float since = decay_of(s), until = decay_of(lone ? 0.0 : all - s);
     if (lane < kTokens<T>) {
-      sum[lane] = s;
+      sum[lane] = lone ? 0.0 : s;
       row[lane] = (back ? until : since) * row_scale;
       col[lane] = (back ? since : until) * col_scale;
     }
@@ -701,7 +702,7 @@ __device__ __forceinline__ void states_range(const LinearArgs& a, const View& k,
     sv[set.value].load(v, start_of(i), size_of(i));
   };
   auto decays = [&](int i) {
-    if (wave == 0) both[i & 1].fill(g.get(), size_of(i), BACK, 1.f, BACK ? a.scale : 1.f, lane);
+    if (wave == 0) both[i & 1].fill(g.get(), size_of(i), BACK, false, 1.f, BACK ? a.scale : 1.f, lane);
   };
   auto chunk = [&](auto set, int i) {
     sk[set.value].store(K, k, start_of(i), size_of(i));
@@ -912,7 +913,8 @@ __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w,
     sv.load(w.v, t, n);
   };
   // chunk i is [t, t + n); one that holds an infinity or a NaN among V is
-  // walked token by token (one < n), so that a weight of zero never meets it
+  // walked token by token (one < n), so that a weight of zero never meets it,
+  // and one with a NaN among its decays, back in time
   int i = 0, one = 0;
   auto start_of = [&](int c) { return t0 + (BACK ? chunks - 1 - c : c) * C; };
   auto size_of = [&](int t) { return end - t < C ? end - t : C; };
@@ -920,7 +922,11 @@ __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w,
   bool single = false;
   // one wave does the decays of a chunk, ahead of it
   auto decays = [&](int b, int n) {
-    if (wave == WAVES - 1) m.d[b].fill(gd.get(), n, BACK, w.row_scale, w.col_scale, lane);
+    if (wave != WAVES - 1) return;
+    m.d[b].fill(gd.get(), n, BACK, n == 1, w.row_scale, w.col_scale, lane);
+    // Back in time a NaN does not concern the tokens behind it, but it is in
+    // all the running sums there.
+    if (BACK && n > 1 && __ballot(lane < n && gd.get() != gd.get()) != 0 && lane == 0) m.wild = 1;
   };
   gd.load(t, n, lane);
   load(t, n);
