@@ -468,8 +468,8 @@ template <typename T> struct LogDecays {
   }
 };
 
-// Decays of a chunk's tokens in LDS.
-template <typename T> struct Decays {
+// Decays of a chunk's tokens in LDS, read four at a time.
+template <typename T> struct alignas(16) Decays {
   double sum[kTokens<T>];               // running sums
   float row[kTokens<T>], col[kTokens<T>];  // factors of the state's part of an output, and of a token's part in the state
   float whole;
@@ -489,6 +489,9 @@ template <typename T> struct Decays {
     if (lane == 0) whole = decay_of(all);
   }
 };
+
+// rows and columns of the second of two lie where 16-byte reads want them
+static_assert(sizeof(Decays<bf16_t>) % 16 == 0 && sizeof(Decays<float>) % 16 == 0, "");
 
 // ---- states in registers ----------------------------------------------------------
 // State tiles: rows the channels that a product sums over (16 m + 4 g + r in
