@@ -473,6 +473,7 @@ template <typename T> struct alignas(16) Decays {
   double sum[kTokens<T>];               // running sums
   float row[kTokens<T>], col[kTokens<T>];  // factors of the state's part of an output, and of a token's part in the state
   float whole;
+  int undefined;  // a NaN is among them
   // `lone`: a single token is none away from itself, also where its decay is a NaN
   __device__ __forceinline__ void fill(float g, int n, bool back, bool lone, float row_scale, float col_scale, int lane) {
     const double s = wave_sums(lane < n ? log2_decay(g) : 0.0);
@@ -486,7 +487,8 @@ template <typename T> struct alignas(16) Decays {
       row[lane] = (back ? until : since) * row_scale;
       col[lane] = (back ? since : until) * col_scale;
     }
-    if (lane == 0) whole = decay_of(all);
+    const bool nan = __ballot(lane < n && g != g) != 0;
+    if (lane == 0) whole = decay_of(all), undefined = nan;
   }
 };
 
@@ -927,9 +929,6 @@ __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w,
   auto decays = [&](int b, int n) {
     if (wave != WAVES - 1) return;
     m.d[b].fill(gd.get(), n, BACK, n == 1, w.row_scale, w.col_scale, lane);
-    // Back in time a NaN does not concern the tokens behind it, but it is in
-    // all the running sums there.
-    if (BACK && n > 1 && __ballot(lane < n && gd.get() != gd.get()) != 0 && lane == 0) m.wild = 1;
   };
   gd.load(t, n, lane);
   load(t, n);
@@ -941,7 +940,10 @@ __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w,
     const bool narrow_wild = sv.store(m.v, w.v, t, n);
     if (!single && n > 1 && __ballot(narrow_wild || sv.wild()) != 0 && lane == 0) m.wild = 1;
     lds_barrier();
-    if (!single && uniform(m.wild)) {
+    // Back in time a NaN among the decays does not concern the tokens behind
+    // it, but it is in all the running sums there.  (It lies with the chunk's
+    // decays: the next chunk's are written while others may still read here.)
+    if (!single && n > 1 && uniform(m.wild | (BACK ? m.d[buf].undefined : 0))) {
       lds_barrier();  // all have read it
       if (threadIdx.x == 0) m.wild = 0;
       single = true;
