@@ -593,7 +593,7 @@ struct State {
 // ---- a chunk's step of the state ------------------------------------------------------
 // S <- whole S + K^T (col V): V's fragments are this wave's own columns,
 // scaled and cut to pieces; K's are read from LDS as they are.
-template <typename T, int DK, int DV>
+template <typename T, int DK, int DV, int ROWS = 4>
 __device__ __forceinline__ void step_state(const T* K, const Lane<T, DK>& lk, const typename Frag<T>::type (&vf)[2],
                                            const Decays<T>& d, int lane, State<DK, DV>& st) {
   constexpr int KB = Elem<T>::KB, PIECES = Pieces<T>::COUNT;
@@ -636,16 +636,16 @@ __device__ __forceinline__ void step_state(const T* K, const Lane<T, DK>& lk, co
       scaled(kb, x);
 #pragma unroll
       for (int p = 0; p < PIECES; ++p) f[p] = Pieces<T>::next(x);
-      // four row tiles at a time: a product's result is not wanted by the next
+      // ROWS row tiles at a time: a product's result is not wanted by the next
 #pragma unroll
-      for (int m = 0; m < DK / 16; m += 4) {
-        typename Frag<T>::type kf[4];
+      for (int m = 0; m < DK / 16; m += ROWS) {
+        typename Frag<T>::type kf[ROWS];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) kf[i] = col_frag<DK>(K, lk, KB * kb, 16 * (m + i));
+        for (int i = 0; i < ROWS; ++i) kf[i] = col_frag<DK>(K, lk, KB * kb, 16 * (m + i));
 #pragma unroll
         for (int p = PIECES - 1; p >= 0; --p)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) st.s[m + i] = mma(kf[i], f[p], st.s[m + i]);
+          for (int i = 0; i < ROWS; ++i) st.s[m + i] = mma(kf[i], f[p], st.s[m + i]);
       }
     }
   }
@@ -1115,7 +1115,12 @@ __device__ __forceinline__ void sweep_range(const LinearArgs& a, const Sweep& w,
     } else {
       out_as(T{});
     }
-    step_state<T, DK, DV>(m.k, Lane<T, DK>(here(lane)), vf, d, lane, st);
+    // The widest gradients leave fewer registers for it (2x2048 tokens of 16
+    // heads of 128 127 us with four row tiles at a time, 123 with two; other
+    // sizes within 1 percent).
+    constexpr int ROWS = R != kForward && DK == 128 && DV == 128 ? 2 : 4;
+    if (ROWS == 2) fence();
+    step_state<T, DK, DV, ROWS>(m.k, Lane<T, DK>(here(lane)), vf, d, lane, st);
     lds_barrier();
     if (by_rows) Stage<T, DV, THREADS>::write(m.v, y, t, n);
     if (strict && (int)threadIdx.x < n) {
