@@ -10,11 +10,12 @@
 // with mean(n dn) = r mean(x dn), so that both sums of a row are taken of its
 // inputs at once.  All of it is bound by memory: every element is read once
 // and written once, a row stays in registers between its sums and its outputs.
-// Measured, bf16 (a large copy reaches 5.13 TB/s): forward 65536 heads of 128,
-// gated, 50.3 MB, 10.1 us (with hits in the last-level cache); 4096 tokens of
-// 4096 channels, residual, 134 MB, 21.7 us (6.2 TB/s, part of it from the cache); backward 131072 heads of
-// 128, gated, 168 MB, 39 us of which the kernel 33 (5.1 TB/s); 8192 tokens of
-// 2048 channels, residual, 201 MB, 43.5 us (4.6 TB/s).
+// Measured, bf16, on inputs that change from call to call (a large copy reaches
+// 5.13 TB/s): forward 65536 heads of 128, gated, 50.3 MB, 10.0 us (with hits in
+// the last-level cache); 4096 tokens of 4096 channels, residual, 134 MB, 23.0 us
+// (5.8 TB/s, part of it from the cache); backward 131072 heads of 128, gated, 168
+// MB, 37.9 us (4.4 TB/s); 8192 tokens of 2048 channels, residual, 201 MB, 45 us
+// (4.5 TB/s); on the same inputs again 32 and 37 us.
 #include "kda_block.h"
 #include "kda_layer_device.h"
 

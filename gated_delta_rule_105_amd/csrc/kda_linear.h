@@ -60,6 +60,10 @@ inline LinearPlan plan_linear(int64_t tokens, int rows, int64_t T, bool packed, 
     p.slot = 1;
     p.n_slots = 1;
   } else if (!packed && (int64_t)rows * H >= cus) {
+    // Rows of their own from one workgroup a compute unit on, without a pass for
+    // states: 8 rows of 4096 tokens of 32 heads of 128 359 us, with slots for
+    // two workgroups a unit 431 (gradients 1091 and 1200); 16 rows of 1024 tokens
+    // of 16 heads 95 and 126 (285 and 358; 64 channels 64 and 78, fp32 224 and 303).
     p.slot = T;
     p.n_slots = rows;
   } else {
@@ -69,7 +73,10 @@ inline LinearPlan plan_linear(int64_t tokens, int rows, int64_t T, bool packed, 
     // of both; half of that took 61.5 us against 55.4 for 4096 tokens of 16
     // heads, and their gradients 153 against 139).  Where that leaves more than
     // one each, as for 16384 tokens, two take 147 us and one 163.  Shorter slots
-    // only where not even one each would be left.
+    // only where not even one each would be left.  Rows and sequences shorter
+    // than a slot go one after the other in its workgroup (255 rows of one token
+    // of one head 479 us, 256 of them, each a slot, 14; 256 packed tokens that
+    // are sequences of 16 heads 547).
     auto slots_of = [&](int64_t groups) {
       const int64_t n = groups / H < 1 ? 1 : groups / H;
       return ceil_div(ceil_div(tokens, n), kLinearChunk) * kLinearChunk;

@@ -7,10 +7,10 @@
 // state before it:
 //   P = scale (Q K^T) o D,  D_ij = e^{G_i - G_j} for j <= i and 0 above,
 //   O = P V + scale e^{G} Q S,   S <- e^{G_C} S + K^T (e^{G_C - G} V).
-// No factor is above 1, so nothing overflows that the recurrence would not
-// make overflow.  The running sums are kept in 64 bits: a decay between two
-// tokens is the difference of two of them, which a strongly decaying token
-// before both would take digits from in 32.
+// No decay is above 1, so none overflows.  (Q K^T is a product that the
+// recurrence does not form: it has to stay inside fp32.)  The running sums are
+// kept in 64 bits: a decay between two tokens is the difference of two of them,
+// which a strongly decaying token before both would take digits from in 32.
 //
 // The gradients are the same computation three times over.  dq is the forward
 // form with (dout, v, k) for (q, k, v) and the transposed state; dv and dk are
@@ -31,11 +31,11 @@
 // five at most.  Necessary bytes are few (a large copy would take 13.5 us for
 // 4096 tokens of 16 heads of 128 in bf16, the matrix products 4.4): what
 // bounds it is the length of a chunk's chain of phases, products of 16-row
-// tiles with waits for LDS between them.  That case takes 51 to 55 us (16 + 8.4
-// + 30.5 in the kernels); its two rows of 2048 tokens backward 120 us (25 + 11.4
-// + 83 + 5.6); 16384 tokens of 32 heads of 128 keys and 64 values that share one
-// query and key 150 us (47 + 9 + 110); 5003 tokens of 6 fp32 heads 95 us (20 +
-// 12 + 64).
+// tiles with waits for LDS between them.  That case takes 52.5 us a call; its two
+// rows of 2048 tokens backward 123 to 130; 16384 tokens of 32 heads of 128 keys
+// and 64 values that share one query and key 149 to 155; 5003 tokens of 6 fp32
+// heads 97.  In a kernel trace, whose calls are up to 17 percent longer, the
+// launches take 16 + 8.7 + 33, 26 + 11.6 + 85 + 5.8, 50 + 9 + 122 and 21 + 12 + 66.
 #include "kda_layer_device.h"
 #include "kda_linear.h"
 #include "kda_rows.h"
@@ -837,10 +837,10 @@ linear_chain(int H, int64_t quads, int n_slots, float* __restrict__ ends, float*
 // ---- outputs -------------------------------------------------------------------------------
 // One form for the outputs and the three gradients ("sweep"): rows of Q meet
 // rows of K, whose weights sum rows of V.
-// A chunk of 64 bf16 tokens of 128 by 128 channels takes a workgroup 12,800
-// cycles, and the same beside a second one on the compute unit: 3100 are of
-// matrix instructions, 4300 of the vector unit (rounding to pieces, decays),
-// the rest waits, for LDS (480 KB read a chunk) and at three barriers.  Where
+// A chunk of 64 bf16 tokens of 128 by 128 channels takes a workgroup 13,600
+// cycles, and two beside each other on a compute unit 26,000: 3900 each are of
+// matrix instructions, 5200 of the vector unit (rounding to pieces, decays),
+// the rest waits, for LDS (510 KB read a chunk) and at three barriers.  Where
 // one workgroup a unit is left, two that share a slot, the second after a pass
 // over the first half for its state, took the same time as one (30.3 and 32.4
 // us for the prompt's sweep): the second pass's start costs what it hides.

@@ -641,7 +641,8 @@ typedef struct {
  *   o       : [B, T, H, d_v] dtype, written
  *   ht      : [S, H, d_k, d_v] fp32, written, or NULL
  * Tokens go through in chunks of 64 (fp32: 32): the decay from one token of a
- * chunk to another is one factor, which is 0 below 2^-126.
+ * chunk to another is one factor, which is 0 below 2^-126, and the products of
+ * queries with keys are formed in fp32, where they have to be finite.
  * A NaN or Inf reaches its own and later tokens of its sequence and head (an
  * infinity as an infinity or a NaN), never an earlier token, another sequence
  * or another head.
@@ -674,6 +675,9 @@ int kda_linear_attn_step(const kda_linear_desc_t* d, const void* q, const void* 
  *   dg      : [B, T, H] dtype or NULL (not written); 0 where g is above 0.
  *             NULL unless the decay is KDA_DECAY_TOKEN (the others are constants)
  *   dh0     : [S, H, d_k, d_v] fp32 or NULL (not written)
+ * dg is summed up from the end of its sequence: a token's is off by what the
+ * roundings of later tokens' inner products (q . dq, k . dk) leave, back to the
+ * last token whose factor is 0, whose own dg is 0.
  * A NaN or Inf reaches the gradients that the recurrence carries it to, and
  * may reach all of its sequence's and head's dg.
  * The workspace holds the states and their gradients between ranges of tokens
@@ -693,7 +697,9 @@ int kda_linear_attn_backward(const kda_linear_desc_t* d, const void* q, const vo
  * output gate), and what stands between that layer's output and the next
  * block (the residual sum and the norm of it).  Slices and alignment as
  * above.  KDA_ERR_UNSUPPORTED: norms over more than 8192 channels, more than
- * 65536 heads, 2^31 rows (tokens times heads) or more.
+ * 65536 heads, 2^31 rows (tokens times heads) or more.  A row's sum of squares
+ * is held in fp32: past its range (values of 2^64) the norm's factor is 0, and
+ * without an epsilon below it (2^-75) an infinity.
  */
 
 /* Shape of one gated norm. */
