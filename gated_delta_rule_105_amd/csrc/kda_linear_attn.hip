@@ -864,7 +864,7 @@ template <typename T> constexpr int kRowTiles = kTokens<T> / 16;
 template <typename T> constexpr int kPTiles = kRowTiles<T> * (kRowTiles<T> + 1) / 2;
 
 // Tiles of P in LDS are in the order of the lanes, four elements of a row
-// each: the lane that formed them is the one that reads them.
+// each: what a lane of one wave forms, the same lane of every wave reads.
 // P's operand of row tile rt for the tokens from KB kb on; the other side of
 // the diagonal (BACK: before rt) is zeros.
 template <bool BACK, int KB>
